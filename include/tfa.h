@@ -79,8 +79,10 @@ typedef enum {
     TFA_ERR_SEQLENS = 14,    /* (tfa_check_status) a variable-length call met an
                                 inconsistent cu_seqlens entry; that call's output is
                                 invalid                                                  */
-    TFA_ERR_RING = 15        /* ring cache without a window, ring_rows not a positive
+    TFA_ERR_RING = 15,       /* ring cache without a window, ring_rows not a positive
                                 multiple of 64, or ring_rows < window - 1 + L            */
+    TFA_ERR_ROPE = 16        /* rot not a multiple of 16 in [0, D], eps negative or not
+                                finite, or mscale not finite                             */
 } tfa_status;
 
 /* Minimum query length accepted by the tiled operator (tiny-llm Week 2 Day 5,
@@ -247,6 +249,57 @@ int tfa_prefill_backward_saved(const void *q, const void *k, const void *v, cons
                                const float *lse, const void *dout, void *dq, void *dk, void *dv,
                                int B, int Hq, int Hkv, int L, int S, int D, float scale,
                                int causal, int window, const float *key_mask, tfa_stream_t stream);
+
+/* tfa_qk_norm_rope -- RMS norms of queries and keys for each head and the
+ * rotary position in one pass.  For a head row x of D channels at position p:
+ *   y = x w / sqrt(mean(x^2) + eps)            (y = x without weights)
+ *   (o_a, o_b) = mscale (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = p inv_freq[i]
+ * for the rot / 2 pairs i; channels from rot on pass through.  Computed in fp32
+ * (the angle in 64 bits), rounded to bf16 once.
+ *   q, k          bf16 [B, L, Hq, D] / [B, L, Hkv, D], any strides with the
+ *                 channels contiguous: views of a joint projection are fine
+ *   q_out, k_out  bf16, likewise: [B, Hq, L, D] for the attention entry points,
+ *                 or rows of a key cache.  May be the inputs themselves (the same
+ *                 pointers and strides); any other overlap is undefined.
+ *   strides       HOST array of 12: the element strides over (batch, token, head)
+ *                 of q, k, q_out, k_out, multiples of 8
+ *   q_weight, k_weight  bf16 [D], or both NULL: no norm
+ *   inv_freq      fp64 [rot / 2] device: radians per position of each pair (scaled
+ *                 for long contexts by the caller); unread when rot == 0
+ *   positions     int32 device: [B] with positions_per_row == 0 (row i of sequence
+ *                 b is at positions[b] + i), [B, L] with positions_per_row != 0;
+ *                 NULL: row i of every sequence is at first_position + i
+ *   rot           rotated channels, a multiple of 16 in [0, D]; 0: norms only
+ *   interleaved   0: pair i is channels (i, i + rot / 2); else (2i, 2i + 1)
+ * Device pointers 16-byte aligned (inv_freq 8, positions 4).  Hq need not be a
+ * multiple of Hkv here.  Asynchronous on `stream`, no workspace, capturable
+ * from the first call. */
+int tfa_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const long long *strides,
+                     const void *q_weight, const void *k_weight, const double *inv_freq,
+                     const int *positions, int positions_per_row, int first_position,
+                     int B, int L, int Hq, int Hkv, int D, int rot, int interleaved,
+                     float eps, float mscale, tfa_stream_t stream);
+
+/* tfa_qk_norm_rope_backward -- the gradient of tfa_qk_norm_rope.
+ *   dq_out, dk_out  upstream gradients (of q_out, k_out)
+ *   q, k            the forward's inputs (unread, may be NULL, without weights)
+ *   dq, dk          bf16, written: gradients of q and k; may be dq_out and dk_out
+ *                   or q and k themselves (the same pointers and strides)
+ *   dq_weight, dk_weight  fp32 [D], written: gradients of the weights, summed over
+ *                   all rows in a fixed order (unread without weights)
+ *   strides         HOST array of 18: (batch, token, head) strides of dq_out,
+ *                   dk_out, q, k, dq, dk
+ *   workspace       device memory of tfa_qk_norm_rope_workspace(D) bytes, 4-byte
+ *                   aligned, with weights only; not shared by calls that overlap
+ * The other arguments are the forward's. */
+int tfa_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                              void *dq, void *dk, float *dq_weight, float *dk_weight,
+                              const long long *strides, const void *q_weight, const void *k_weight,
+                              const double *inv_freq, const int *positions, int positions_per_row,
+                              int first_position, int B, int L, int Hq, int Hkv, int D, int rot,
+                              int interleaved, float eps, float mscale, void *workspace,
+                              tfa_stream_t stream);
+size_t tfa_qk_norm_rope_workspace(int D);
 
 /* Debug flags for tfa_prefill_debug. */
 #define TFA_DEBUG_NO_TILE_SKIP  1u /* visit every key tile, even fully masked ones   */

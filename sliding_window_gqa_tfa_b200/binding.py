@@ -9,6 +9,7 @@ fails, it raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -35,6 +36,7 @@ TFA_ERR_CAPTURE = 12
 TFA_ERR_SOFTCAP = 13
 TFA_ERR_SEQLENS = 14
 TFA_ERR_RING = 15
+TFA_ERR_ROPE = 16
 MAX_VARLEN_SEQS = 1024
 
 TFA_DEBUG_NO_TILE_SKIP = 1
@@ -107,6 +109,13 @@ def lib():
             L.tfa_plan_pieces.argtypes = [i32] * 9 + [P, i32, ctypes.POINTER(i32),
                                                       ctypes.POINTER(ctypes.c_longlong)]
             L.tfa_plan_pieces.restype = i32
+            LL, dims = ctypes.POINTER(ctypes.c_longlong), [i32] * 7
+            L.tfa_qk_norm_rope.argtypes = [P] * 4 + [LL, P, P, P, P, i32, i32] + dims + [f32, f32, P]
+            L.tfa_qk_norm_rope.restype = i32
+            L.tfa_qk_norm_rope_backward.argtypes = [P] * 8 + [LL, P, P, P, P, i32, i32] + dims + [f32, f32, P, P]
+            L.tfa_qk_norm_rope_backward.restype = i32
+            L.tfa_qk_norm_rope_workspace.argtypes = [i32]
+            L.tfa_qk_norm_rope_workspace.restype = ctypes.c_size_t
             _lib = L
     return _lib
 
@@ -114,7 +123,7 @@ def lib():
 def declared_symbols() -> list[str]:
     """Names of the functions include/tfa.h declares."""
     text = open(HEADER).read()
-    return sorted(set(re.findall(r"^\s*(?:int|const char \*)\s*(tfa_\w+)\s*\(", text, re.M)))
+    return sorted(set(re.findall(r"^\s*(?:int|size_t|const char \*)\s*(tfa_\w+)\s*\(", text, re.M)))
 
 
 def last_error() -> str:
@@ -468,3 +477,180 @@ def prefill_host(q, k, v, *, scale=None, causal=True, window=0, key_mask=None, o
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_prefill_host")
     return out
+
+
+# ------------------------------------------- norms and rotary positions of q and k
+_NO_SCOPE = contextlib.nullcontext()
+
+
+def _scope(device, stream):
+    """Makes `device` current for a call, and `stream` where one is given, so that
+    what the call allocates belongs to the stream that uses it."""
+    import torch
+
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("stream belongs to another device than the tensors")
+        return torch.cuda.stream(stream)
+    return _NO_SCOPE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _check_on(t, name, dtype, ndim, device=None, rows=False):
+    """Checks a CUDA tensor's type, dimensions and device; rows: any strides, as
+    long as the last dimension is contiguous (else all of it must be)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if rows:
+        if t.shape[-1] != 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have a contiguous last dimension")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def rope_inv_freq(rot, base=10000.0, *, scaling=None, factor=1.0, original=8192, device=None):
+    """(inv_freq, mscale) for qk_norm_rope: fp64 [rot/2] radians per position, base^(-2i/rot).
+
+    scaling: None; "linear" (every pair's frequency divided by factor); "llama3" or
+    "yarn" (pairs that turn less than once in the `original` positions are divided
+    by factor, those that turn more than 4, or 32, times are kept, between them a
+    linear ramp over the turns; yarn's mscale is 0.1 ln(factor) + 1)."""
+    import torch
+
+    if rot < 0 or rot % 2:
+        raise ValueError("rot must be even and >= 0")
+    if not (factor > 0 and original > 0 and base > 0):
+        raise ValueError("base, factor and original must be positive")
+    f = torch.tensor([float(base) ** (-2.0 * i / rot) for i in range(rot // 2)], dtype=torch.float64)
+    mscale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling in ("llama3", "yarn"):
+        fast = 4.0 if scaling == "llama3" else 32.0
+        keep = ((original * f / (2 * math.pi) - 1.0) / (fast - 1.0)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1 - keep)
+        if scaling == "yarn" and factor > 1:
+            mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling is not None:
+        raise ValueError('scaling must be None, "linear", "llama3" or "yarn"')
+    return f.to("cuda" if device is None else device), mscale
+
+
+def _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight):
+    """Checks shared by the pass and its gradient; the C call's middle arguments."""
+    import torch
+
+    dev = q.device
+    _check_on(k, "k", torch.bfloat16, 4, dev, rows=True)
+    B, L, Hq, D = q.shape
+    if k.shape[0] != B or k.shape[1] != L or k.shape[3] != D:
+        raise ValueError("q and k disagree on batch, tokens or head dimension")
+    _check_on(inv_freq, "inv_freq", torch.float64, 1, dev)
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight must be given together")
+    if q_weight is not None:
+        for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            _check_on(t, n, torch.bfloat16, 1, dev)
+            if t.shape[0] != D:
+                raise ValueError(f"{n} must hold one weight per channel")
+    per_row, first, ptr = 0, 0, None
+    if isinstance(positions, int):
+        first = positions
+    else:
+        _check_on(positions, "positions", torch.int32, positions.dim() if isinstance(positions, torch.Tensor) else 1, dev)
+        per_row = int(positions.dim() == 2)
+        if tuple(positions.shape) != ((B, L) if per_row else (B,)):
+            raise ValueError("positions must be an int, [B] or [B, L]")
+        ptr = positions.data_ptr()
+    return (q_weight.data_ptr() if q_weight is not None else None,
+            k_weight.data_ptr() if k_weight is not None else None, inv_freq.data_ptr(), ptr, per_row,
+            first), (B, L, Hq, k.shape[2], D, 2 * inv_freq.shape[0])
+
+
+def _strides(*tensors):
+    """(batch, token, head) element strides of (tensor, token axis) pairs."""
+    s = []
+    for t, axis in tensors:
+        a = t.stride()
+        s += (a[0], a[axis], a[3 - axis])
+    return (ctypes.c_longlong * len(s))(*s)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, mscale=1.0,
+                 q_out=None, k_out=None, stream=None):
+    """(q_out [B,Hq,L,D], k_out [B,Hkv,L,D]) bf16 of the projections q [B,L,Hq,D] and
+    k [B,L,Hkv,D] (bf16, any strides with contiguous channels): RMS norms for each
+    head (with q_weight and k_weight, bf16 [D]) and the rotary position, in one pass.
+
+    positions: int32 [B] (of each sequence's first row) or [B,L] on the device, or
+    an int.  inv_freq: fp64 [rot/2] on the device (rope_inv_freq), rot a multiple of
+    16 up to D, the other channels pass through.  q_out and k_out may be views, e.g.
+    a key cache's rows, in [B,H,L,D] order.  Raises TfaError on a nonzero status."""
+    import torch
+
+    _check_on(q, "q", torch.bfloat16, 4, rows=True)
+    mid, dims = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight)
+    B, L, Hq, Hkv, D, rot = dims
+    with _scope(q.device, stream):
+        if q_out is None:
+            q_out = torch.empty((B, Hq, L, D), dtype=torch.bfloat16, device=q.device)
+        if k_out is None:
+            k_out = torch.empty((B, Hkv, L, D), dtype=torch.bfloat16, device=q.device)
+        for t, n, h in ((q_out, "q_out", Hq), (k_out, "k_out", Hkv)):
+            _check_on(t, n, torch.bfloat16, 4, q.device, rows=True)
+            if t.shape != (B, h, L, D):
+                raise ValueError(f"{n} must be [B, H, L, D]")
+        rc = lib().tfa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+                                    _strides((q, 1), (k, 1), (q_out, 2), (k_out, 2)), *mid, *dims, int(interleaved),
+                                    eps, mscale, torch.cuda.current_stream().cuda_stream)
+    if rc != TFA_OK:
+        raise TfaError(rc, "tfa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6,
+                          interleaved=False, mscale=1.0, out=None, stream=None):
+    """(dq, dk, dq_weight, dk_weight): the gradient of qk_norm_rope for upstream
+    dq_out [B,Hq,L,D] and dk_out [B,Hkv,L,D] (bf16, any strides with contiguous
+    channels).  dq [B,L,Hq,D] and dk [B,L,Hkv,D] are bf16 (views in `out` are fine);
+    the weights' are fp32 [D], None without weights."""
+    import torch
+
+    _check_on(dq_out, "dq_out", torch.bfloat16, 4, rows=True)
+    _check_on(q, "q", torch.bfloat16, 4, dq_out.device, rows=True)
+    mid, dims = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight)
+    B, L, Hq, Hkv, D, rot = dims
+    _check_on(dk_out, "dk_out", torch.bfloat16, 4, q.device, rows=True)
+    if dq_out.shape != (B, Hq, L, D) or dk_out.shape != (B, Hkv, L, D):
+        raise ValueError("dq_out and dk_out must be [B, H, L, D]")
+    with _scope(q.device, stream):
+        if out is None:
+            out = (torch.empty((B, L, Hq, D), dtype=torch.bfloat16, device=q.device),
+                   torch.empty((B, L, Hkv, D), dtype=torch.bfloat16, device=q.device))
+        dq, dk = out
+        for t, n, ref in ((dq, "dq", q), (dk, "dk", k)):
+            _check_on(t, n, torch.bfloat16, 4, q.device, rows=True)
+            if t.shape != ref.shape:
+                raise ValueError(f"{n} has the wrong shape")
+        dwq = dwk = ws = None
+        if q_weight is not None:
+            dw = torch.empty((2, D), dtype=torch.float32, device=q.device)
+            dwq, dwk = dw[0], dw[1]
+            ws = torch.empty(lib().tfa_qk_norm_rope_workspace(D), dtype=torch.uint8, device=q.device)
+        rc = lib().tfa_qk_norm_rope_backward(
+            dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+            dwq.data_ptr() if ws is not None else None, dwk.data_ptr() if ws is not None else None,
+            _strides((dq_out, 2), (dk_out, 2), (q, 1), (k, 1), (dq, 1), (dk, 1)), *mid, *dims, int(interleaved), eps,
+            mscale, ws.data_ptr() if ws is not None else None, torch.cuda.current_stream().cuda_stream)
+    if rc != TFA_OK:
+        raise TfaError(rc, "tfa_qk_norm_rope_backward")
+    return dq, dk, dwq, dwk

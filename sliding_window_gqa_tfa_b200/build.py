@@ -1,6 +1,9 @@
 """Build libtfa.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a.
 
-    python -m sliding_window_gqa_tfa_b200.build [--verbose]
+    python -m sliding_window_gqa_tfa_b200.build [--verbose] [--changed]
+
+Every source is compiled again unless --changed is given (then only those whose
+source, or any header, is newer than the object).
 
 The library is written next to this file; it links the CUDA runtime
 statically and resolves the driver's cuTensorMapEncodeTiled at run time, so it
@@ -16,7 +19,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtfa.so")
-SOURCES = [os.path.join(CSRC, "tfa.cu")]
+OBJ = os.path.join(HERE, "_build")  # object files (git-ignored)
+SOURCES = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith(".cu")]
 HEADERS = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
     os.path.join(ROOT, "include", "tfa.h")]
 
@@ -39,16 +43,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-           "-Xcompiler", "-fPIC,-O2", "-shared", "-I", os.path.join(ROOT, "include"),
-           "-o", tmp] + SOURCES
+    base = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
+            "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include")]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
+        base.insert(1, "-Xptxas=-v")
+    # one object per source, compiled side by side; an object newer than its
+    # source and every header is kept
+    os.makedirs(OBJ, exist_ok=True)
+    header_time = max(os.path.getmtime(f) for f in HEADERS)
+    objs, running = [], []
+    for src in SOURCES:
+        obj = os.path.join(OBJ, os.path.basename(src) + ".o")
+        objs.append(obj)
+        if force or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(src), header_time):
+            cmd = base + ["-c", "-o", obj + f".tmp{os.getpid()}", src]
+            running.append((cmd, obj, subprocess.Popen(cmd)))
+    failed = [(cmd, p.returncode) for cmd, _, p in running if p.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
+    for _, obj, _ in running:
+        os.replace(obj + f".tmp{os.getpid()}", obj)
+    subprocess.run(base + ["-shared", "-o", tmp] + objs, check=True)
     os.replace(tmp, LIB)
     return LIB
 
 
 if __name__ == "__main__":
-    build(force=True, verbose="--verbose" in sys.argv)
+    build(force="--changed" not in sys.argv, verbose="--verbose" in sys.argv)
     print(LIB)

@@ -19,6 +19,7 @@
 
 #include "../../include/tfa.h"
 #include "tfa_bwd.cuh"
+#include "tfa_internal.h"
 #include "tfa_kernel.cuh"
 
 namespace {
@@ -507,6 +508,18 @@ int ensure_capacity(DeviceState &st, int i, size_t bytes) {
 }
 
 }  // namespace
+
+namespace tfa {
+int report_cuda(const char *what, cudaError_t e) { return cuda_fail(what, e); }
+int device_info(cudaStream_t stream, unsigned **status, int *sm_count) {
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *st = nullptr;
+    if (int rc = device_state(stream, &st)) return rc;
+    *status = st->status;
+    *sm_count = st->sm_count;
+    return TFA_OK;
+}
+}  // namespace tfa
 
 extern "C" int tfa_prefill(const void *q, const void *k, const void *v, void *o, int B, int Hq,
                            int Hkv, int L, int S, int D, float scale, int causal, int window,
@@ -1007,6 +1020,8 @@ extern "C" const char *tfa_status_string(int status) {
         case TFA_ERR_SEQLENS: return "inconsistent cu_seqlens in a variable-length call; its output is invalid";
         case TFA_ERR_RING: return "ring cache needs a window, ring_rows a multiple of 64 and >= window - 1 + L";
         case TFA_ERR_FLAGS: return "unknown debug flags";
+        case TFA_ERR_ROPE:
+            return "rot must be a multiple of 16 up to D, eps finite and >= 0, mscale finite";
         default: return "unknown status";
     }
 }

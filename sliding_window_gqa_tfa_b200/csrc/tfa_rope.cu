@@ -1,0 +1,444 @@
+// tfa_rope.cu -- norms of queries and keys for each head with the rotary
+// position in the same pass, and its gradient.
+//
+// For a head row x of D channels at position p (all in fp32, rounded to bf16
+// once at the end):
+//   y = x r w,  r = 1 / sqrt(mean(x^2) + eps)         (y = x without weights)
+//   (o_a, o_b) = m (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = p f_i
+// for the rot / 2 pairs i: channels (i, i + rot / 2), or (2i, 2i + 1) where the
+// pairs are interleaved; channels from rot on pass through.
+// The angle is taken in 64 bits, reduced to a fraction of a turn there and only
+// then rounded: p f_i in fp32 would be off by p f_i 2^-24 radians, 0.06 at
+// position 10^6.
+// Gradient, with g the rotated-back dy (the transposed rotation) and h = x r:
+//   dw += g h,   dx = r (w g - h mean(w g h)).
+//
+// Layout: a row is D / 8 lanes of 16 bytes, so a warp instruction moves whole
+// 128-byte lines; tokens come in the projection's order ([B, L, H, D], any
+// strides) and leave in the attention's ([B, H, L, D], or a cache's rows), so
+// no separate transpose reads the data again.
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/tfa.h"
+#include "tfa_internal.h"
+
+namespace tfa {
+namespace rope {
+
+constexpr int kThreads = 256;
+constexpr int kBwdBlocks = 592;  // gradient kernel: most blocks, so most partial sums of a weight
+
+struct Strides {
+    long long b, l, h;  // elements
+};
+struct Params {
+    const __nv_bfloat16 *q, *k;    // forward: inputs; gradient: the forward's inputs
+    const __nv_bfloat16 *dq, *dk;  // gradient: upstream
+    __nv_bfloat16 *qo, *ko;
+    Strides sq, sk, sdq, sdk, sqo, sko;
+    const __nv_bfloat16 *wq, *wk;
+    const double *inv_freq;
+    const int *pos;
+    int pos_per_row, pos0;
+    int B, L, Hq, Hkv, rot;
+    int rows_per_block;  // forward: head rows of a token that one block takes
+    float eps, mscale;
+    int conj;   // rotate back (a gradient)
+    int inter;  // pairs of neighbouring channels (2i, 2i + 1)
+    float *partial;  // gradient: [blocks][2][D]
+};
+
+__device__ __forceinline__ int position(const Params &p, int b, int l) {
+    if (!p.pos) return p.pos0 + l;
+    return p.pos_per_row ? __ldg(p.pos + static_cast<long long>(b) * p.L + l) : __ldg(p.pos + b) + l;
+}
+
+// cos and sin (times mscale) of the rot / 2 angles of one position, by the
+// block's first threads.
+__device__ __forceinline__ void fill_table(const Params &p, int pos, float2 *tab) {
+    if (threadIdx.x < static_cast<unsigned>(p.rot >> 1)) {
+        constexpr double kInv2Pi = 0.15915494309189533577;
+        double turns = static_cast<double>(pos) * p.inv_freq[threadIdx.x] * kInv2Pi;
+        turns -= rint(turns);
+        float s, c;
+        sincospif(2.f * static_cast<float>(turns), &s, &c);
+        tab[threadIdx.x] = make_float2(c * p.mscale, (p.conj ? -s : s) * p.mscale);
+    }
+}
+
+__device__ __forceinline__ void unpack(const uint4 &v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The lane's cos / sin factors: half layout, 8 pairs; interleaved, 4.
+template <bool INTER>
+struct Factors {
+    float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
+    __device__ __forceinline__ void load(const float2 *tab, int lane8, int rot) {
+        const int half = rot >> 4;  // lanes of a half (half layout)
+        if (lane8 * 8 >= rot) {
+#pragma unroll
+            for (int e = 0; e < (INTER ? 4 : 8); ++e) c[e] = 1.f, s[e] = 0.f;
+            return;
+        }
+        const int i0 = INTER ? lane8 * 4 : (lane8 < half ? lane8 : lane8 - half) * 8;
+#pragma unroll
+        for (int e = 0; e < (INTER ? 4 : 8); ++e) {
+            const float2 t = tab[i0 + e];
+            c[e] = t.x;
+            // the first of a pair takes - sin, the second + sin
+            s[e] = INTER ? t.y : (lane8 < half ? -t.y : t.y);
+        }
+    }
+    // Rotates the lane's 8 channels; every lane of the warp calls it (the half
+    // layout's partners sit rot / 16 lanes away).
+    __device__ __forceinline__ void rotate(float (&y)[8], int lane8, int rot) const {
+        if constexpr (INTER) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = y[2 * e], b = y[2 * e + 1];
+                y[2 * e] = fmaf(a, c[e], -b * s[e]);
+                y[2 * e + 1] = fmaf(b, c[e], a * s[e]);
+            }
+        } else {
+            const int half = rot >> 4;
+            const int lane = threadIdx.x & 31;
+            const int partner = lane8 * 8 >= rot ? lane : (lane8 < half ? lane + half : lane - half);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float o = __shfl_sync(0xffffffffu, y[e], partner);
+                y[e] = fmaf(y[e], c[e], o * s[e]);
+            }
+        }
+    }
+};
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <int D, bool NORM, bool INTER>
+__global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ Params p) {
+    constexpr int LPR = D / 8, kSlots = kThreads / LPR;
+    __shared__ float2 tab[D / 2];
+    const int token = blockIdx.x, b = token / p.L, l = token - b * p.L;
+    const int lane8 = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+    const int n_rows = p.Hq + p.Hkv;
+    const int row0 = blockIdx.y * p.rows_per_block;
+    const int row1 = min(row0 + p.rows_per_block, n_rows);
+    const __nv_bfloat16 *q = p.q + b * p.sq.b + l * p.sq.l + lane8 * 8;
+    const __nv_bfloat16 *k = p.k + b * p.sk.b + l * p.sk.l + lane8 * 8;
+    __nv_bfloat16 *qo = p.qo + b * p.sqo.b + l * p.sqo.l + lane8 * 8;
+    __nv_bfloat16 *ko = p.ko + b * p.sko.b + l * p.sko.l + lane8 * 8;
+    // the first rows are on their way while the table is computed
+    constexpr int kAhead = 4;
+    uint4 x[kAhead];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int row = base + slot + u * kSlots;
+            x[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < row1)
+                x[u] = *reinterpret_cast<const uint4 *>(row < p.Hq ? q + row * p.sq.h : k + (row - p.Hq) * p.sk.h);
+        }
+    };
+    load(row0);
+    fill_table(p, position(p, b, l), tab);
+    float wq[8], wk[8];
+    if constexpr (NORM) {
+        unpack(*reinterpret_cast<const uint4 *>(p.wq + lane8 * 8), wq);
+        unpack(*reinterpret_cast<const uint4 *>(p.wk + lane8 * 8), wk);
+    }
+    __syncthreads();
+    Factors<INTER> f;
+    f.load(tab, lane8, p.rot);
+    for (int base = row0; base < row1; base += kAhead * kSlots) {
+        if (base > row0) load(base);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int row = base + slot + u * kSlots;
+            if (base + u * kSlots >= row1) break;  // block-uniform
+            float y[8];
+            unpack(x[u], y);
+            if constexpr (NORM) {
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+                const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] *= r * (row < p.Hq ? wq[e] : wk[e]);
+            }
+            f.rotate(y, lane8, p.rot);
+            if (row < row1)
+                *reinterpret_cast<uint4 *>(row < p.Hq ? qo + row * p.sqo.h : ko + (row - p.Hq) * p.sko.h) = pack(y);
+        }
+    }
+}
+
+// Gradient with norms: blocks walk the tokens, so that the weights' gradients
+// gather in registers over all of a block's rows; one partial sum per block,
+// added up in block order by the second kernel (the same order every time).
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ Params p) {
+    constexpr int LPR = D / 8, kSlots = kThreads / LPR;
+    __shared__ float2 tab[2][D / 2];
+    __shared__ float red[kSlots][D + 4];
+    const int lane8 = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+    const int n_rows = p.Hq + p.Hkv, n_tokens = p.B * p.L;
+    float wq[8], wk[8], gq[8], gk[8];
+    unpack(*reinterpret_cast<const uint4 *>(p.wq + lane8 * 8), wq);
+    unpack(*reinterpret_cast<const uint4 *>(p.wk + lane8 * 8), wk);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gq[e] = gk[e] = 0.f;
+    int which = 0;
+    for (int token = blockIdx.x; token < n_tokens; token += gridDim.x, which ^= 1) {
+        const int b = token / p.L, l = token - b * p.L;
+        fill_table(p, position(p, b, l), tab[which]);
+        __syncthreads();  // one a token: the other table is the next token's
+        Factors<INTER> f;
+        f.load(tab[which], lane8, p.rot);
+        for (int base = 0; base < n_rows; base += kSlots) {
+            const int row = base + slot;
+            const bool isq = row < p.Hq, in = row < n_rows;
+            const int h = isq ? row : row - p.Hq;
+            uint4 xv = make_uint4(0u, 0u, 0u, 0u), gv = xv;
+            if (in) {
+                const __nv_bfloat16 *xp = isq ? p.q + b * p.sq.b + l * p.sq.l + h * p.sq.h
+                                              : p.k + b * p.sk.b + l * p.sk.l + h * p.sk.h;
+                const __nv_bfloat16 *gp = isq ? p.dq + b * p.sdq.b + l * p.sdq.l + h * p.sdq.h
+                                              : p.dk + b * p.sdk.b + l * p.sdk.l + h * p.sdk.h;
+                xv = *reinterpret_cast<const uint4 *>(xp + lane8 * 8);
+                gv = *reinterpret_cast<const uint4 *>(gp + lane8 * 8);
+            }
+            float x[8], g[8];
+            unpack(xv, x);
+            unpack(gv, g);
+            f.rotate(g, lane8, p.rot);
+            float ss = 0.f, dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ss = fmaf(x[e], x[e], ss);
+                dot = fmaf(g[e] * (isq ? wq[e] : wk[e]), x[e], dot);
+            }
+            ss = row_sum<LPR>(ss);
+            dot = row_sum<LPR>(dot);
+            const float r = rsqrtf(ss * (1.f / D) + p.eps);
+            const float m = dot * r * r * (1.f / D);  // h mean(w g h) = x m
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float gx = g[e] * x[e] * r;
+                if (in) {
+                    if (isq) gq[e] += gx;
+                    else gk[e] += gx;
+                }
+                o[e] = r * fmaf(-x[e], m, g[e] * (isq ? wq[e] : wk[e]));
+            }
+            if (in) {
+                __nv_bfloat16 *op = isq ? p.qo + b * p.sqo.b + l * p.sqo.l + h * p.sqo.h
+                                        : p.ko + b * p.sko.b + l * p.sko.l + h * p.sko.h;
+                *reinterpret_cast<uint4 *>(op + lane8 * 8) = pack(o);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) red[slot][lane8 * 8 + e] = t ? gk[e] : gq[e];
+        __syncthreads();
+        if (threadIdx.x < D) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) s += red[i][threadIdx.x];
+            p.partial[(static_cast<size_t>(blockIdx.x) * 2 + t) * D + threadIdx.x] = s;
+        }
+    }
+}
+
+// dw[2][D] = sum over blocks of partial[block][2][D]: 32 columns a block, 8
+// threads a column, always in the same order.
+__global__ void __launch_bounds__(256) weight_kernel(const float *partial, int blocks, int cols, float *dwq,
+                                                     float *dwk) {
+    __shared__ float red[8][33];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), s = threadIdx.x >> 5;
+    float sum = 0.f;
+    for (int i = s; i < blocks; i += 8) sum += partial[static_cast<size_t>(i) * cols + c];
+    red[s][threadIdx.x & 31] = sum;
+    __syncthreads();
+    if (s == 0) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) sum += red[i][threadIdx.x & 31];
+        const int half = cols >> 1;
+        if (c < half) dwq[c] = sum;
+        else dwk[c - half] = sum;
+    }
+}
+
+int check(const Params &p, int D) {
+    if (p.Hq < 1 || p.Hkv < 1) return TFA_ERR_HEADS;
+    if (p.B < 1 || p.L < 1 || static_cast<long long>(p.B) * p.L > 0x7fffffffll - 1024 || p.Hq > (1 << 20) ||
+        p.Hkv > (1 << 20))
+        return TFA_ERR_SHAPE;
+    if (D != 64 && D != 128) return TFA_ERR_HEAD_DIM;
+    if (p.rot < 0 || p.rot > D || p.rot % 16 != 0 || !std::isfinite(p.eps) || p.eps < 0.f || !std::isfinite(p.mscale))
+        return TFA_ERR_ROPE;
+    if (p.rot > 0 && !p.inv_freq) return TFA_ERR_NULL;
+    if ((p.wq == nullptr) != (p.wk == nullptr)) return TFA_ERR_NULL;
+    return TFA_OK;
+}
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool aligned(const Strides &s) { return s.b % 8 == 0 && s.l % 8 == 0 && s.h % 8 == 0; }
+Strides strides(const long long *s) { return Strides{s[0], s[1], s[2]}; }
+
+int launch_forward(Params &p, int D, cudaStream_t stream) {
+    const int n_rows = p.Hq + p.Hkv, slots = kThreads / (D / 8);
+    const int tokens = p.B * p.L;
+    // A block takes all of a token's rows, so that its angles are computed once,
+    // unless that leaves SMs without a block (decoding): then one round of rows.
+    p.rows_per_block = tokens >= 4 * 148 ? n_rows : slots;
+    const dim3 grid(tokens, (n_rows + p.rows_per_block - 1) / p.rows_per_block);
+    const bool norm = p.wq != nullptr;
+    using Kern = void (*)(Params);
+    auto pick = [&](bool inter) -> Kern {
+        if (D == 128)
+            return norm ? (inter ? forward_kernel<128, true, true> : forward_kernel<128, true, false>)
+                        : (inter ? forward_kernel<128, false, true> : forward_kernel<128, false, false>);
+        return norm ? (inter ? forward_kernel<64, true, true> : forward_kernel<64, true, false>)
+                    : (inter ? forward_kernel<64, false, true> : forward_kernel<64, false, false>);
+    };
+    pick(p.inter != 0)<<<grid, kThreads, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TFA_OK : report_cuda("qk_norm_rope launch", e);
+}
+
+int launch_backward(Params &p, int D, float *dwq, float *dwk, cudaStream_t stream) {
+    const int tokens = p.B * p.L;
+    const int blocks = tokens < kBwdBlocks ? tokens : kBwdBlocks;
+    using Kern = void (*)(Params);
+    const Kern kern = D == 128 ? (p.inter ? backward_kernel<128, true> : backward_kernel<128, false>)
+                               : (p.inter ? backward_kernel<64, true> : backward_kernel<64, false>);
+    kern<<<blocks, kThreads, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return report_cuda("qk_norm_rope gradient launch", e);
+    weight_kernel<<<2 * D / 32, 256, 0, stream>>>(p.partial, blocks, 2 * D, dwq, dwk);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? TFA_OK : report_cuda("norm weight gradient launch", e);
+}
+
+}  // namespace rope
+}  // namespace tfa
+
+using tfa::rope::aligned;
+using tfa::rope::strides;
+
+extern "C" int tfa_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const long long *strd,
+                                const void *q_weight, const void *k_weight, const double *inv_freq,
+                                const int *positions, int positions_per_row, int first_position, int B, int L, int Hq,
+                                int Hkv, int D, int rot, int interleaved, float eps, float mscale,
+                                tfa_stream_t stream) {
+    if (!q || !k || !q_out || !k_out || !strd) return TFA_ERR_NULL;
+    tfa::rope::Params p = {};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.qo = static_cast<__nv_bfloat16 *>(q_out);
+    p.ko = static_cast<__nv_bfloat16 *>(k_out);
+    p.sq = strides(strd);
+    p.sk = strides(strd + 3);
+    p.sqo = strides(strd + 6);
+    p.sko = strides(strd + 9);
+    p.wq = static_cast<const __nv_bfloat16 *>(q_weight);
+    p.wk = static_cast<const __nv_bfloat16 *>(k_weight);
+    p.inv_freq = inv_freq;
+    p.pos = positions;
+    p.pos_per_row = positions_per_row;
+    p.pos0 = first_position;
+    p.B = B;
+    p.L = L;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.rot = rot;
+    p.eps = eps;
+    p.mscale = mscale;
+    p.inter = interleaved ? 1 : 0;
+    if (const int rc = tfa::rope::check(p, D)) return rc;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(q_weight, 16) ||
+        !aligned(k_weight, 16) || !aligned(inv_freq, 8) || !aligned(positions, 4) || !aligned(p.sq) ||
+        !aligned(p.sk) || !aligned(p.sqo) || !aligned(p.sko))
+        return TFA_ERR_ALIGN;
+    return tfa::rope::launch_forward(p, D, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t tfa_qk_norm_rope_workspace(int D) {
+    return static_cast<size_t>(tfa::rope::kBwdBlocks) * 2 * (D < 0 ? 0 : D) * sizeof(float);
+}
+
+extern "C" int tfa_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                                         void *dq, void *dk, float *dq_weight, float *dk_weight,
+                                         const long long *strd, const void *q_weight, const void *k_weight,
+                                         const double *inv_freq, const int *positions, int positions_per_row,
+                                         int first_position, int B, int L, int Hq, int Hkv, int D, int rot,
+                                         int interleaved, float eps, float mscale, void *workspace,
+                                         tfa_stream_t stream) {
+    if (!dq_out || !dk_out || !dq || !dk || !strd) return TFA_ERR_NULL;
+    const bool norm = q_weight && k_weight;
+    if (norm && (!q || !k || !dq_weight || !dk_weight || !workspace)) return TFA_ERR_NULL;
+    tfa::rope::Params p = {};
+    // without norms the gradient is the rotation back, the forward's kernel on dq_out and dk_out
+    p.q = static_cast<const __nv_bfloat16 *>(norm ? q : dq_out);
+    p.k = static_cast<const __nv_bfloat16 *>(norm ? k : dk_out);
+    p.dq = static_cast<const __nv_bfloat16 *>(dq_out);
+    p.dk = static_cast<const __nv_bfloat16 *>(dk_out);
+    p.qo = static_cast<__nv_bfloat16 *>(dq);
+    p.ko = static_cast<__nv_bfloat16 *>(dk);
+    p.sdq = strides(strd);
+    p.sdk = strides(strd + 3);
+    p.sq = norm ? strides(strd + 6) : p.sdq;
+    p.sk = norm ? strides(strd + 9) : p.sdk;
+    p.sqo = strides(strd + 12);
+    p.sko = strides(strd + 15);
+    p.wq = static_cast<const __nv_bfloat16 *>(q_weight);
+    p.wk = static_cast<const __nv_bfloat16 *>(k_weight);
+    p.inv_freq = inv_freq;
+    p.pos = positions;
+    p.pos_per_row = positions_per_row;
+    p.pos0 = first_position;
+    p.B = B;
+    p.L = L;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.rot = rot;
+    p.eps = eps;
+    p.mscale = mscale;
+    p.inter = interleaved ? 1 : 0;
+    p.conj = 1;
+    p.partial = static_cast<float *>(workspace);
+    if (const int rc = tfa::rope::check(p, D)) return rc;
+    if (!aligned(p.q, 16) || !aligned(p.k, 16) || !aligned(dq_out, 16) || !aligned(dk_out, 16) || !aligned(dq, 16) ||
+        !aligned(dk, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(inv_freq, 8) ||
+        !aligned(positions, 4) || !aligned(dq_weight, 4) || !aligned(dk_weight, 4) || !aligned(workspace, 4) ||
+        !aligned(p.sq) || !aligned(p.sk) || !aligned(p.sdq) || !aligned(p.sdk) || !aligned(p.sqo) || !aligned(p.sko))
+        return TFA_ERR_ALIGN;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return norm ? tfa::rope::launch_backward(p, D, dq_weight, dk_weight, s) : tfa::rope::launch_forward(p, D, s);
+}
