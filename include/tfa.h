@@ -67,7 +67,8 @@ typedef enum {
     TFA_ERR_SHORT_QUERY = 3, /* L < 9: the tiled operator rejects short queries          */
     TFA_ERR_SHAPE = 4,       /* B < 1, S < L, or a size whose element count overflows    */
     TFA_ERR_HEAD_DIM = 5,    /* D not 64 or 128                                          */
-    TFA_ERR_WINDOW = 6,      /* window > 0 without causal (no page defines it)           */
+    TFA_ERR_WINDOW = 6,      /* window > 0 without causal (no page defines it), or first
+                                negative, or > 0 without a window                        */
     TFA_ERR_ALIGN = 7,       /* a tensor pointer is not 16-byte aligned, key_mask not 4  */
     TFA_ERR_CUDA = 8,        /* a CUDA runtime/driver call failed (launch, encode, ...)  */
     TFA_ERR_TIMEOUT = 9,     /* a kernel wait gave up; the output of that call is invalid */
@@ -77,12 +78,14 @@ typedef enum {
                                 capture (it would allocate); call once outside capture   */
     TFA_ERR_SOFTCAP = 13,    /* softcap not finite, negative, or > 0 with scale == 0     */
     TFA_ERR_SEQLENS = 14,    /* (tfa_check_status) a variable-length call met an
-                                inconsistent cu_seqlens entry; that call's output is
+                                inconsistent cu_seqlens entry, or a 4-bit cache call
+                                rows outside the capacity; that call's output is
                                 invalid                                                  */
     TFA_ERR_RING = 15,       /* ring cache without a window, ring_rows not a positive
                                 multiple of 64, or ring_rows < window - 1 + L            */
-    TFA_ERR_ROPE = 16        /* rot not a multiple of 16 in [0, D], eps negative or not
+    TFA_ERR_ROPE = 16,       /* rot not a multiple of 16 in [0, D], eps negative or not
                                 finite, or mscale not finite                             */
+    TFA_ERR_CACHE = 17       /* rows outside a 4-bit cache's capacity (known on the host) */
 } tfa_status;
 
 /* Minimum query length accepted by the tiled operator (tiny-llm Week 2 Day 5,
@@ -300,6 +303,63 @@ int tfa_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void
                               int interleaved, float eps, float mscale, void *workspace,
                               tfa_stream_t stream);
 size_t tfa_qk_norm_rope_workspace(int D);
+
+/* The 4-bit key/value cache.  Per position and KV head the D channels (64 or 128)
+ * are held in groups of 32: a minimum m and a step s = bf16((max - m) / 15), both
+ * bf16, and a 4-bit code c = rint((x - m) / s) in [0, 15] per channel (all 0 where
+ * s = 0); the value is c s + m.  A group that holds a value that is not finite,
+ * or whose range is not, has s = m = NaN and reads back as NaN.  Four
+ * caller-owned device tensors, 16-byte aligned:
+ *   k_codes, v_codes  uint8 [B, Hkv, capacity, D / 2]: byte i of a row holds
+ *                     channel 2i in its low and 2i + 1 in its high four bits
+ *   k_meta, v_meta    bf16 [B, Hkv, capacity, D / 32, 2]: (s, m) of each group
+ * 1 <= capacity <= 2^30.  At D = 128 a position takes 160 bytes, 0.31 of bf16's. */
+
+/* tfa_kv4_append -- writes L new rows of every sequence into the cache.
+ *   k, v      bf16 [B, Hkv, L, D], 16-byte aligned, any strides with the channels
+ *             contiguous; strides: HOST array of 6, the element strides over
+ *             (batch, head, row) of k and v, multiples of 8
+ *   start     int32 [B] device: row i of sequence b goes to cache row start[b] + i;
+ *             start[b] < 0: the sequence takes nothing.  Rows at or past the
+ *             capacity are not written, and tfa_check_status returns
+ *             TFA_ERR_SEQLENS.  NULL: every sequence starts at first_row, checked
+ *             here (TFA_ERR_CACHE).
+ * Other rows of the cache are left as they are.  Asynchronous on `stream`. */
+int tfa_kv4_append(const void *k, const void *v, const long long *strides,
+                   void *k_codes, void *k_meta, void *v_codes, void *v_meta,
+                   const int *start, int first_row, int B, int Hkv, int L, int capacity, int D,
+                   tfa_stream_t stream);
+
+/* tfa_kv4_read -- the values of `rows` cached rows of every sequence, from
+ * start[b] (or first_row) on, rounded to bf16: k, v [B, Hkv, rows, D], written.
+ * A sequence with start[b] < 0 reads as zeros, as do rows at or past the
+ * capacity (then tfa_check_status returns TFA_ERR_SEQLENS). */
+int tfa_kv4_read(const void *k_codes, const void *k_meta, const void *v_codes, const void *v_meta,
+                 void *k, void *v, const int *start, int first_row,
+                 int B, int Hkv, int rows, int capacity, int D, tfa_stream_t stream);
+
+/* tfa_kv4_decode -- tfa_decode over the 4-bit cache, sequences of their own lengths.
+ *   q, o      bf16 [B, Hq, L, D], 1 <= L <= TFA_MAX_DECODE_ROWS, B <= 1024
+ *   lens      int32 [B] device: cached positions of each sequence, its L new rows
+ *             among them (they are the last).  Row i is at position p = lens[b] - L
+ *             + i and sees the positions j <= p, with a window (window > 0) those
+ *             with j > p - window or j < first.  A row that sees none (lens[b] = 0,
+ *             an idle sequence) is written as zeros.  lens[b] < 0 or past the
+ *             capacity counts as 0, and tfa_check_status returns TFA_ERR_SEQLENS.
+ *   first     first tokens that stay visible outside the window, >= 0; > 0 needs
+ *             a window (TFA_ERR_WINDOW)
+ *   softcap, sinks  as for tfa_attention_ex
+ *   workspace device memory of tfa_kv4_decode_workspace(Hq, Hkv, L, D) bytes,
+ *             16-byte aligned; not shared by calls that overlap
+ * The codes enter the products exactly; the softmax weights times a step are
+ * rounded to bf16.  Asynchronous on `stream`; after one call on the device
+ * (which creates its status word) it may be captured, and each replay reads the
+ * lengths anew. */
+int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_meta, const void *v_codes, const void *v_meta,
+                   const int *lens, void *o, int B, int Hq, int Hkv, int L, int capacity, int D,
+                   float scale, int window, int first, float softcap, const float *sinks,
+                   void *workspace, tfa_stream_t stream);
+size_t tfa_kv4_decode_workspace(int Hq, int Hkv, int L, int D);
 
 /* Debug flags for tfa_prefill_debug. */
 #define TFA_DEBUG_NO_TILE_SKIP  1u /* visit every key tile, even fully masked ones   */

@@ -37,6 +37,7 @@ TFA_ERR_SOFTCAP = 13
 TFA_ERR_SEQLENS = 14
 TFA_ERR_RING = 15
 TFA_ERR_ROPE = 16
+TFA_ERR_CACHE = 17
 MAX_VARLEN_SEQS = 1024
 
 TFA_DEBUG_NO_TILE_SKIP = 1
@@ -114,6 +115,14 @@ def lib():
             L.tfa_qk_norm_rope.restype = i32
             L.tfa_qk_norm_rope_backward.argtypes = [P] * 8 + [LL, P, P, P, P, i32, i32] + dims + [f32, f32, P, P]
             L.tfa_qk_norm_rope_backward.restype = i32
+            L.tfa_kv4_append.argtypes = [P, P, LL] + [P] * 5 + [i32] * 6 + [P]
+            L.tfa_kv4_append.restype = i32
+            L.tfa_kv4_read.argtypes = [P] * 7 + [i32] * 6 + [P]
+            L.tfa_kv4_read.restype = i32
+            L.tfa_kv4_decode.argtypes = [P] * 7 + [i32] * 6 + [f32, i32, i32, f32, P, P, P]
+            L.tfa_kv4_decode.restype = i32
+            L.tfa_kv4_decode_workspace.argtypes = [i32] * 4
+            L.tfa_kv4_decode_workspace.restype = ctypes.c_size_t
             L.tfa_qk_norm_rope_workspace.argtypes = [i32]
             L.tfa_qk_norm_rope_workspace.restype = ctypes.c_size_t
             _lib = L
@@ -654,3 +663,139 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_qk_norm_rope_backward")
     return dq, dk, dwq, dwk
+
+
+# ---------------------------------------------------- the 4-bit key/value cache
+KV4_GROUP = 32
+
+
+def kv4_cache(B, Hkv, capacity, D, device=None):
+    """(k_codes, k_meta, v_codes, v_meta): an empty 4-bit cache (every value 0)."""
+    import torch
+
+    if D not in (64, 128):
+        raise ValueError("head dimension must be 64 or 128")
+    dev = "cuda" if device is None else device
+    out = []
+    for _ in range(2):
+        out.append(torch.zeros((B, Hkv, capacity, D // 2), dtype=torch.uint8, device=dev))
+        out.append(torch.zeros((B, Hkv, capacity, D // KV4_GROUP, 2), dtype=torch.bfloat16, device=dev))
+    return tuple(out)
+
+
+def _kv4_check(k_codes, k_meta, v_codes, v_meta):
+    """Checks a cache's tensors; (B, Hkv, capacity, D, device)."""
+    import torch
+
+    _check_on(k_codes, "k_codes", torch.uint8, 4)
+    dev = k_codes.device
+    B, Hkv, cap, half = k_codes.shape
+    meta = (B, Hkv, cap, half // (KV4_GROUP // 2), 2)
+    _check_on(v_codes, "v_codes", torch.uint8, 4, dev)
+    _check_on(k_meta, "k_meta", torch.bfloat16, 5, dev)
+    _check_on(v_meta, "v_meta", torch.bfloat16, 5, dev)
+    if v_codes.shape != k_codes.shape or k_meta.shape != meta or v_meta.shape != meta:
+        raise ValueError("a 4-bit cache is codes [B,Hkv,capacity,D/2] and meta [B,Hkv,capacity,D/32,2], twice")
+    return B, Hkv, cap, 2 * half, dev
+
+
+def _kv4_start(start, B, dev):
+    """(device pointer or None, first row) of an int or int32 [B]."""
+    import torch
+
+    if isinstance(start, int):
+        return None, start
+    _check_on(start, "start", torch.int32, 1, dev)
+    if start.shape[0] != B:
+        raise ValueError("start must hold one row per sequence")
+    return start.data_ptr(), 0
+
+
+def kv4_append(k, v, k_codes, k_meta, v_codes, v_meta, *, start, stream=None):
+    """Writes k, v (bf16 [B,Hkv,L,D], any strides with contiguous channels) into the
+    4-bit cache: row i of sequence b at cache row start[b] + i.  start: int32 [B] on
+    the device (negative: nothing for that sequence), or an int for all."""
+    import torch
+
+    B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
+    _check_on(k, "k", torch.bfloat16, 4, dev, rows=True)
+    _check_on(v, "v", torch.bfloat16, 4, dev, rows=True)
+    if k.shape != v.shape or k.shape[0] != B or k.shape[1] != Hkv or k.shape[3] != D:
+        raise ValueError("k and v must be [B,Hkv,L,D] of the cache's B, Hkv and D")
+    ptr, first = _kv4_start(start, B, dev)
+    strides = (ctypes.c_longlong * 6)(*k.stride()[:3], *v.stride()[:3])
+    with _scope(dev, stream):
+        rc = lib().tfa_kv4_append(k.data_ptr(), v.data_ptr(), strides, k_codes.data_ptr(), k_meta.data_ptr(),
+                                  v_codes.data_ptr(), v_meta.data_ptr(), ptr, first, B, Hkv, k.shape[2], cap, D,
+                                  torch.cuda.current_stream().cuda_stream)
+    if rc != TFA_OK:
+        raise TfaError(rc, "tfa_kv4_append")
+
+
+def kv4_read(k_codes, k_meta, v_codes, v_meta, *, start=0, rows=None, out=None, stream=None):
+    """(k, v) bf16 [B,Hkv,rows,D]: the values of cached rows start[b] .. start[b] + rows - 1
+    (start: int32 [B] on the device, or an int; rows: by default all from start on)."""
+    import torch
+
+    B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
+    ptr, first = _kv4_start(start, B, dev)
+    if rows is None:
+        if ptr is not None:
+            raise ValueError("rows must be given with a start for each sequence")
+        rows = cap - first
+    with _scope(dev, stream):
+        if out is None:
+            out = (torch.empty((B, Hkv, rows, D), dtype=torch.bfloat16, device=dev),
+                   torch.empty((B, Hkv, rows, D), dtype=torch.bfloat16, device=dev))
+        for t, n in zip(out, ("k", "v")):
+            _check_on(t, n, torch.bfloat16, 4, dev)
+            if t.shape != (B, Hkv, rows, D):
+                raise ValueError(f"{n} must be [B,Hkv,rows,D]")
+        rc = lib().tfa_kv4_read(k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(), v_meta.data_ptr(),
+                                out[0].data_ptr(), out[1].data_ptr(), ptr, first, B, Hkv, rows, cap, D,
+                                torch.cuda.current_stream().cuda_stream)
+    if rc != TFA_OK:
+        raise TfaError(rc, "tfa_kv4_read")
+    return out
+
+
+def kv4_decode(q, k_codes, k_meta, v_codes, v_meta, lens, *, scale=None, window=0, first=0, softcap=0.0, sinks=None,
+               out=None, workspace=None, stream=None):
+    """Decoding attention [B,Hq,L,D] (1 <= L <= 8) over the 4-bit cache: lens, int32 [B]
+    on the device, holds each sequence's cached positions, its L new rows last among
+    them.  window > 0: the last `window` positions and the `first` first ones.
+    workspace: uint8 of tfa_kv4_decode_workspace bytes, by default allocated here."""
+    import torch
+
+    B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
+    _check_on(q, "q", torch.bfloat16, 4, dev)
+    _check_on(lens, "lens", torch.int32, 1, dev)
+    Hq, L = q.shape[1], q.shape[2]
+    if q.shape[0] != B or q.shape[3] != D or lens.shape[0] != B:
+        raise ValueError("q, lens and the cache disagree")
+    if sinks is not None:
+        _check_on(sinks, "sinks", torch.float32, 1, dev)
+        if sinks.shape[0] != Hq:
+            raise ValueError("sinks must hold one logit per query head")
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _check_on(out, "out", torch.bfloat16, 4, dev)
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+        need = lib().tfa_kv4_decode_workspace(Hq, Hkv, L, D)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _check_on(workspace, "workspace", torch.uint8, 1, dev)
+            if workspace.shape[0] < need:
+                raise ValueError(f"workspace must hold {need} bytes")
+        rc = lib().tfa_kv4_decode(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
+                                  v_meta.data_ptr(), lens.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, cap, D,
+                                  D ** -0.5 if scale is None else scale, window, first, softcap,
+                                  sinks.data_ptr() if sinks is not None else None, workspace.data_ptr(),
+                                  torch.cuda.current_stream().cuda_stream)
+    if rc != TFA_OK:
+        raise TfaError(rc, "tfa_kv4_decode")
+    return out

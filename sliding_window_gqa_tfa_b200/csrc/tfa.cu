@@ -1010,16 +1010,17 @@ extern "C" const char *tfa_status_string(int status) {
         case TFA_ERR_SHORT_QUERY: return "query shorter than the tiled operator's minimum (9 rows)";
         case TFA_ERR_SHAPE: return "invalid shape (B < 1, S < L, or sizes out of range)";
         case TFA_ERR_HEAD_DIM: return "head dimension must be 64 or 128";
-        case TFA_ERR_WINDOW: return "a sliding window requires causal attention";
+        case TFA_ERR_WINDOW: return "a sliding window requires causal attention, visible first tokens a window";
         case TFA_ERR_ALIGN: return "tensor pointers must be 16-byte aligned (key mask 4-byte)";
         case TFA_ERR_CUDA: return "a CUDA call failed";
         case TFA_ERR_TIMEOUT: return "a kernel wait timed out; the output is invalid";
         case TFA_ERR_SCALE: return "scale must be finite";
         case TFA_ERR_CAPTURE: return "first use of a device or stream inside a CUDA graph capture";
         case TFA_ERR_SOFTCAP: return "softcap must be finite and >= 0 (and needs a nonzero scale)";
-        case TFA_ERR_SEQLENS: return "inconsistent cu_seqlens in a variable-length call; its output is invalid";
+        case TFA_ERR_SEQLENS: return "inconsistent lengths on the device (cu_seqlens, or rows outside a cache); that output is invalid";
         case TFA_ERR_RING: return "ring cache needs a window, ring_rows a multiple of 64 and >= window - 1 + L";
         case TFA_ERR_FLAGS: return "unknown debug flags";
+        case TFA_ERR_CACHE: return "rows outside the cache's capacity";
         case TFA_ERR_ROPE:
             return "rot must be a multiple of 16 up to D, eps finite and >= 0, mscale finite";
         default: return "unknown status";

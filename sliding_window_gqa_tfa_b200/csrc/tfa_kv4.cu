@@ -1,0 +1,308 @@
+// tfa_kv4.cu -- a key/value cache held in 4 bits: writing rows into it, reading
+// them back, and attention over it.
+//
+// Format, per cached position and KV head: D channels in groups of 32.  A group
+// holds its minimum m and step s = bf16((max - m) / 15), and per channel the code
+// c = rint((x - m) / s) in 0..15; the value is c s + m.  Codes: D / 2 bytes, byte
+// i channel 2i (low half) and 2i + 1; steps and minima: one 32-bit word per
+// group, s in the low half.  A group that holds a value that is not finite (or
+// whose range is not) has s = m = NaN: it reads back as NaN.
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "../../include/tfa.h"
+#include "tfa_internal.h"
+#include "tfa_kv4_attn.cuh"
+#include "tfa_ptx.cuh"
+
+namespace tfa {
+namespace kv4 {
+
+constexpr int kGroup = 32;  // channels that share a step and a minimum
+
+struct Cache {
+    uint8_t *kc, *vc;   // [B, Hkv, cap, D / 2]
+    uint32_t *km, *vm;  // [B, Hkv, cap, D / 32]
+};
+
+// ------------------------------------------------------------ append and read
+struct AppendParams {
+    const __nv_bfloat16 *k, *v;
+    long long sk[3], sv[3];  // element strides over (batch, head, row)
+    Cache c;
+    const int *start;  // first cache row of each sequence; NULL: start0
+    int start0;
+    int B, Hkv, L, cap;
+    unsigned *status;
+};
+
+// One row of one tensor is D / 8 lanes of 16 bytes; four lanes share a group.
+// Bound by the bytes moved: 2 in, 0.625 out a channel.
+template <int D>
+__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
+    constexpr int LPR = D / 8;
+    const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;
+    const int lane8 = threadIdx.x % LPR;
+    const long long n_rows = static_cast<long long>(p.B) * p.Hkv * p.L;
+    const bool is_v = blockIdx.y != 0;
+    const bool in = row < n_rows;
+    const long long bh = in ? row / p.L : 0;
+    const int i = in ? static_cast<int>(row - bh * p.L) : 0;
+    const int b = static_cast<int>(bh / p.Hkv), h = static_cast<int>(bh - static_cast<long long>(b) * p.Hkv);
+    const long long *s = is_v ? p.sv : p.sk;
+    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+    if (in) raw = *reinterpret_cast<const uint4 *>((is_v ? p.v : p.k) + b * s[0] + h * s[1] + i * s[2] + lane8 * 8);
+    const long long first = p.start ? __ldg(p.start + b) : p.start0;
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(w[e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+    float lo = x[0], hi = x[0], odd = 0.f;  // odd: NaN once a value is not finite
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        lo = fminf(lo, x[e]);
+        hi = fmaxf(hi, x[e]);
+        odd = fmaf(x[e], 0.f, odd);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        odd += __shfl_xor_sync(0xffffffffu, odd, o);
+    }
+    const float step = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(hi - lo, 15.f)));
+    const bool fine = odd == 0.f && step <= 3.3895314e38f;  // finite values and a finite step
+    uint32_t code = 0u;
+    if (fine && step > 0.f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float q = rintf(__fdiv_rn(x[e] - lo, step));
+            code |= static_cast<uint32_t>(fminf(fmaxf(q, 0.f), 15.f)) << (4 * e);
+        }
+    }
+    if (!in || first < 0) return;  // a sequence without a place takes nothing
+    const long long at = first + i;
+    if (at >= p.cap) {
+        if (lane8 == 0) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
+        return;
+    }
+    const size_t dst = static_cast<size_t>(bh) * p.cap + at;
+    reinterpret_cast<uint32_t *>(is_v ? p.c.vc : p.c.kc)[dst * LPR + lane8] = code;
+    if ((lane8 & 3) == 0)
+        (is_v ? p.c.vm : p.c.km)[dst * (D / kGroup) + lane8 / 4] =
+            fine ? (__float_as_uint(step) >> 16) | (__float_as_uint(lo) & 0xffff0000u) : 0x7fc07fc0u;
+}
+
+struct ReadParams {
+    Cache c;
+    __nv_bfloat16 *k, *v;  // [B, Hkv, rows, D]
+    const int *start;
+    int start0;
+    int B, Hkv, rows, cap;
+    unsigned *status;
+};
+
+__device__ __forceinline__ uint4 values8(uint32_t code, uint32_t meta) {
+    const float s = __uint_as_float(meta << 16), m = __uint_as_float(meta & 0xffff0000u);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        w[e] = pack_bf16(fmaf(static_cast<float>((code >> (8 * e)) & 15u), s, m),
+                         fmaf(static_cast<float>((code >> (8 * e + 4)) & 15u), s, m));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
+    constexpr int LPR = D / 8;
+    const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;
+    const int lane8 = threadIdx.x % LPR;
+    if (row >= static_cast<long long>(p.B) * p.Hkv * p.rows) return;
+    const bool is_v = blockIdx.y != 0;
+    const long long bh = row / p.rows;
+    const int b = static_cast<int>(bh / p.Hkv);
+    const long long first = p.start ? __ldg(p.start + b) : p.start0;
+    const long long at = first + (row - bh * p.rows);
+    uint4 out = make_uint4(0u, 0u, 0u, 0u);
+    if (first >= 0 && at < p.cap) {
+        const size_t src = static_cast<size_t>(bh) * p.cap + at;
+        out = values8(__ldg(reinterpret_cast<const uint32_t *>(is_v ? p.c.vc : p.c.kc) + src * LPR + lane8),
+                      __ldg((is_v ? p.c.vm : p.c.km) + src * (D / kGroup) + lane8 / 4));
+    } else if (first >= 0 && lane8 == 0) {
+        atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
+    }
+    *reinterpret_cast<uint4 *>((is_v ? p.v : p.k) + static_cast<size_t>(row) * D + lane8 * 8) = out;
+}
+
+// --------------------------------------------------------------- host checks
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int check_cache(const void *kc, const void *km, const void *vc, const void *vm, int B, int Hkv, int cap, int D) {
+    if (!kc || !km || !vc || !vm) return TFA_ERR_NULL;
+    if (Hkv < 1) return TFA_ERR_HEADS;
+    if (B < 1 || cap < 1 || cap > (1 << 30) || static_cast<long long>(B) * Hkv * cap > (1ll << 40)) return TFA_ERR_SHAPE;
+    if (D != 64 && D != 128) return TFA_ERR_HEAD_DIM;
+    if (!aligned(kc, 16) || !aligned(km, 16) || !aligned(vc, 16) || !aligned(vm, 16)) return TFA_ERR_ALIGN;
+    return TFA_OK;
+}
+
+// Blocks of 256 threads for `rows` rows of D / 8 lanes; 0 if the grid cannot hold them.
+unsigned row_blocks(long long rows, int D) {
+    const long long n = (rows * (D / 8) + 255) / 256;
+    return n <= 0x7fffffffll ? static_cast<unsigned>(n) : 0u;
+}
+
+Cache cache_of(void *kc, void *km, void *vc, void *vm) {
+    return Cache{static_cast<uint8_t *>(kc), static_cast<uint8_t *>(vc), static_cast<uint32_t *>(km),
+                 static_cast<uint32_t *>(vm)};
+}
+
+// ------------------------------------------------------------------- decoding
+constexpr int kMaxCtas = 320;  // bounds the workspace whatever the device
+
+template <int D, int NB>
+int launch_decode(DecodeParams &p, int sms, cudaStream_t stream) {
+    using C = Cfg<D, NB>;
+    p.chunks = (p.rows + C::kRows - 1) / C::kRows;
+    // cheap next to the launch, and the attribute holds for the current device only
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return report_cuda("cudaFuncSetAttribute(kv4 decode smem)", e);
+    const int grid = sms * C::kCtasPerSm < kMaxCtas ? sms * C::kCtasPerSm : kMaxCtas;
+    decode_kernel<D, NB><<<grid, 32 * kWarps, C::kSmemBytes, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda("kv4 decode launch", e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.chunks));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, join_kernel<D, NB>, p, grid)) != cudaSuccess)
+        return report_cuda("kv4 join launch", e);
+    return TFA_OK;
+}
+
+}  // namespace kv4
+}  // namespace tfa
+
+using namespace tfa::kv4;
+
+extern "C" int tfa_kv4_append(const void *k, const void *v, const long long *strides, void *k_codes, void *k_meta,
+                              void *v_codes, void *v_meta, const int *start, int first_row, int B, int Hkv, int L,
+                              int capacity, int D, tfa_stream_t stream) {
+    if (!k || !v || !strides) return TFA_ERR_NULL;
+    if (int rc = check_cache(k_codes, k_meta, v_codes, v_meta, B, Hkv, capacity, D)) return rc;
+    if (L < 1) return TFA_ERR_SHAPE;
+    if (!start && (first_row < 0 || static_cast<long long>(first_row) + L > capacity)) return TFA_ERR_CACHE;
+    AppendParams p = {};
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    for (int i = 0; i < 3; ++i) {
+        p.sk[i] = strides[i];
+        p.sv[i] = strides[3 + i];
+        if (p.sk[i] % 8 || p.sv[i] % 8) return TFA_ERR_ALIGN;
+    }
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4)) return TFA_ERR_ALIGN;
+    const unsigned blocks = row_blocks(static_cast<long long>(B) * Hkv * L, D);
+    if (!blocks) return TFA_ERR_SHAPE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int sms = 0;
+    if (int rc = tfa::device_info(s, &p.status, &sms)) return rc;
+    p.c = cache_of(k_codes, k_meta, v_codes, v_meta);
+    p.start = start;
+    p.start0 = first_row;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.L = L;
+    p.cap = capacity;
+    (D == 128 ? append_kernel<128> : append_kernel<64>)<<<dim3(blocks, 2), 256, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TFA_OK : tfa::report_cuda("kv4 append launch", e);
+}
+
+extern "C" int tfa_kv4_read(const void *k_codes, const void *k_meta, const void *v_codes, const void *v_meta, void *k,
+                            void *v, const int *start, int first_row, int B, int Hkv, int rows, int capacity, int D,
+                            tfa_stream_t stream) {
+    if (!k || !v) return TFA_ERR_NULL;
+    if (int rc = check_cache(k_codes, k_meta, v_codes, v_meta, B, Hkv, capacity, D)) return rc;
+    if (rows < 1) return TFA_ERR_SHAPE;
+    if (!start && (first_row < 0 || static_cast<long long>(first_row) + rows > capacity)) return TFA_ERR_CACHE;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4)) return TFA_ERR_ALIGN;
+    const unsigned blocks = row_blocks(static_cast<long long>(B) * Hkv * rows, D);
+    if (!blocks) return TFA_ERR_SHAPE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    ReadParams p = {};
+    int sms = 0;
+    if (int rc = tfa::device_info(s, &p.status, &sms)) return rc;
+    p.c = cache_of(const_cast<void *>(k_codes), const_cast<void *>(k_meta), const_cast<void *>(v_codes),
+                   const_cast<void *>(v_meta));
+    p.k = static_cast<__nv_bfloat16 *>(k);
+    p.v = static_cast<__nv_bfloat16 *>(v);
+    p.start = start;
+    p.start0 = first_row;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.rows = rows;
+    p.cap = capacity;
+    (D == 128 ? read_kernel<128> : read_kernel<64>)<<<dim3(blocks, 2), 256, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TFA_OK : tfa::report_cuda("kv4 read launch", e);
+}
+
+extern "C" size_t tfa_kv4_decode_workspace(int Hq, int Hkv, int L, int D) {
+    if (Hkv < 1 || Hq < 1 || L < 1 || D < 1) return 0;
+    const int nb = static_cast<long long>(Hq / Hkv) * L <= 8 ? 1 : 2;
+    return static_cast<size_t>(2 * kMaxCtas) * 8 * nb * (D + 2) * sizeof(float);
+}
+
+extern "C" int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_meta, const void *v_codes,
+                              const void *v_meta, const int *lens, void *o, int B, int Hq, int Hkv, int L,
+                              int capacity, int D, float scale, int window, int first, float softcap,
+                              const float *sinks, void *workspace, tfa_stream_t stream) {
+    if (!q || !o || !lens || !workspace) return TFA_ERR_NULL;
+    if (int rc = check_cache(k_codes, k_meta, v_codes, v_meta, B, Hkv, capacity, D)) return rc;
+    if (Hq < 1 || Hq % Hkv != 0) return TFA_ERR_HEADS;
+    if (B > kMaxSeqs || L < 1 || L > TFA_MAX_DECODE_ROWS || static_cast<long long>(B) * Hq * L > (1ll << 30))
+        return TFA_ERR_SHAPE;
+    if (first < 0 || (first > 0 && window <= 0)) return TFA_ERR_WINDOW;
+    if (!std::isfinite(scale)) return TFA_ERR_SCALE;
+    if (!std::isfinite(softcap) || softcap < 0.f || (softcap > 0.f && scale == 0.f)) return TFA_ERR_SOFTCAP;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lens, 4) || !aligned(sinks, 4) || !aligned(workspace, 16))
+        return TFA_ERR_ALIGN;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    DecodeParams p = {};
+    int sms = 0;
+    if (int rc = tfa::device_info(s, &p.status, &sms)) return rc;
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.o = static_cast<__nv_bfloat16 *>(o);
+    p.kc = static_cast<const uint8_t *>(k_codes);
+    p.vc = static_cast<const uint8_t *>(v_codes);
+    p.km = static_cast<const uint32_t *>(k_meta);
+    p.vm = static_cast<const uint32_t *>(v_meta);
+    p.lens = lens;
+    p.sinks = sinks;
+    p.part = static_cast<float *>(workspace);
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.L = L;
+    p.G = Hq / Hkv;
+    p.cap = capacity;
+    p.rows = p.G * L;
+    p.window = window > 0 ? window : 0;
+    p.first = first;
+    p.scale = scale;
+    p.scale_log2 = scale * kLog2e;
+    p.softcap = softcap;
+    if (p.rows <= 8) return D == 128 ? launch_decode<128, 1>(p, sms, s) : launch_decode<64, 1>(p, sms, s);
+    return D == 128 ? launch_decode<128, 2>(p, sms, s) : launch_decode<64, 2>(p, sms, s);
+}

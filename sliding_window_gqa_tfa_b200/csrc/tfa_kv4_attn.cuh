@@ -1,0 +1,627 @@
+// tfa_kv4_attn.cuh -- decoding attention over the 4-bit cache.
+//
+// For a query row q of a KV group and cached position j, with s and m the step
+// and minimum of a group of 32 channels and c its codes:
+//   q.k_j = sum_groups [ s (sum_d q_d c_d) + m (sum_d q_d) ],
+//   o     = sum_j p_j v_j = sum_j [ (p_j s) (c_d - 8) + p_j (m + 8 s) ]   per channel d,
+// so the tensor core multiplies q and p s with the codes themselves, exact as
+// bf16, and K and V are never rounded.  (c - 8: p s is rounded to bf16, so its
+// factor should have no mean; against c the error was 0.0040 of the output
+// instead of 0.0023.)  A code becomes bf16 by one logical operation: 0x4300 | c
+// is 128 + c; the 128 comes off K's sums as part of m (m - 128 s), and 136 off
+// V's codes by one subtraction for two.
+//
+// What bounds it is reading the cache (1.25 D bytes a position and head) as long
+// as a group's rows are few, so the products are transposed: positions (K) and
+// channels (V) are the 16-row side of mma.m16n8k16, the query rows its 8-column
+// side, and eight rows cost what the codes need anyway.  Every warp walks its own
+// 32-position steps with its own asynchronous copies and its own running
+// maximum and sum; nothing in the loop waits for another warp.  The fragments
+// come straight from the codes: a lane's word of 8 codes gives four bf16 pairs,
+// in an order of channels that q is laid out in once.
+//
+// The steps of all (sequence, KV head, chunk of rows) segments are cut into equal
+// ranges, one per CTA; lengths are read on the device.  A segment that lies in
+// one CTA is finished there; the pieces of a cut one go to a workspace and are
+// joined by a second kernel (m* = max m, l* = sum 2^(m - m*) l, likewise O).
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "tfa_ptx.cuh"
+
+namespace tfa {
+namespace kv4 {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kStep = 32;      // positions of a warp's step
+constexpr int kWarps = 8;
+constexpr int kMaxSeqs = 1024;  // sequences of a call
+constexpr int kCtaMinSteps = kWarps;  // steps that a CTA takes at least
+
+struct DecodeParams {
+    const __nv_bfloat16 *q;  // [B, Hq, L, D]
+    __nv_bfloat16 *o;        // [B, Hq, L, D]
+    const uint8_t *kc, *vc;  // [B, Hkv, cap, D / 2]
+    const uint32_t *km, *vm;  // [B, Hkv, cap, D / 32]
+    const int *lens;          // [B]
+    const float *sinks;       // [Hq] or nullptr
+    float *part;              // workspace: [2 CTAs][rows (D + 2)]
+    unsigned *status;
+    int B, Hq, Hkv, L, G, cap;
+    int rows;                 // G L: query rows of a KV head
+    int chunks;               // of 8 NB rows
+    int window, first;
+    float scale, scale_log2, softcap;
+};
+
+// The steps of one sequence: the first `fs` cover the first tokens that stay
+// visible, the others the window (or everything) from step fs + gap on.
+struct Span {
+    int n;      // cached positions
+    int steps;  // in all
+    int fs, gap;
+};
+__device__ __forceinline__ Span span_of(const DecodeParams &p, int b) {
+    Span s;
+    s.n = __ldg(p.lens + b);
+    if (s.n < 0 || s.n > p.cap) s.n = 0;
+    s.fs = s.gap = s.steps = 0;
+    if (s.n == 0) return s;
+    s.steps = (s.n + kStep - 1) / kStep;
+    if (p.window > 0) {
+        // 64 bits: a window may be as large as an int
+        const long long lo = static_cast<long long>(s.n) - p.L - p.window + 1;  // first position in the window
+        const int first_step = lo > 0 ? static_cast<int>(lo / kStep) : 0;
+        const int keep = (min(p.first, s.n) + kStep - 1) / kStep;
+        if (first_step > keep) {
+            s.fs = keep;
+            s.gap = first_step - keep;
+            s.steps -= s.gap;
+        }
+    }
+    return s;
+}
+
+// Prefix sums of the sequences' steps, by the block's threads: pre[b] for b in [0, B].
+__device__ __forceinline__ void prefix_steps(const DecodeParams &p, long long *pre, bool report) {
+    __shared__ int steps[kMaxSeqs];
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+        const int n = __ldg(p.lens + b);
+        if (report && (n < 0 || n > p.cap)) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
+        steps[b] = span_of(p, b).steps;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x, per = (p.B + 31) / 32;
+        const int a0 = min(lane * per, p.B), a1 = min(a0 + per, p.B);
+        long long sum = 0;
+        for (int i = a0; i < a1; ++i) sum += steps[i];
+        long long incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += y;
+        }
+        long long run = incl - sum;
+        for (int i = a0; i < a1; ++i) {
+            pre[i] = run;
+            run += steps[i];
+        }
+        if (a1 == p.B) pre[p.B] = incl;  // (lanes without a share hold the total too)
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int ctas_used(long long W, int grid) {
+    const long long n = (W + kCtaMinSteps - 1) / kCtaMinSteps;
+    return n < grid ? static_cast<int>(n) : grid;
+}
+__device__ __forceinline__ long long range_begin(long long W, int used, int c) { return W * c / used; }
+
+// -------------------------------------------------------------- instructions
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// Transpose of an 8 x 8 matrix of 16-bit words, a row's two words per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// Codes i and i + 4 of a word (bits 4 i and 16 + 4 i) as the bf16 pair 128 + c.
+template <int I>
+__device__ __forceinline__ uint32_t pair128(uint32_t w) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w >> (4 * I)), "r"(0x000f000fu), "r"(0x43004300u));
+    return r;
+}
+__device__ __forceinline__ uint32_t minus136(uint32_t x) {
+    const __nv_bfloat162 c = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
+    __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&x), c);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool in) {
+    const int n = in ? BYTES : 0;  // 0: the destination is filled with zeros
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+
+template <int D, int NB>
+struct Cfg {
+    static constexpr int kGroups = D / 32;
+    static constexpr int kRowBytes = D / 2, kMetaBytes = D / 8;
+    static constexpr int kRows = 8 * NB;
+    static constexpr int kCtasPerSm = NB == 1 ? 2 : 1;
+    static constexpr int kStages = (NB == 1 && D == 128) ? 2 : 4;  // what shared memory holds
+    static constexpr int kHalfStage = kStep * (kRowBytes + kMetaBytes);  // K or V of a step
+    static constexpr int kPipeBytes = kWarps * kStages * 2 * kHalfStage;
+    static constexpr int kOutStride = D + 4;  // floats; the 4 keep the writes of a warp in different banks
+    // joining the warps, over the pipeline's buffers: O, m and l of each
+    static constexpr int kJoinBytes = kWarps * kRows * (kOutStride + 2) * 4;
+    static constexpr int kSmemBytes = kPipeBytes > kJoinBytes ? kPipeBytes : kJoinBytes;
+    static constexpr int kSlotFloats = kRows * (D + 2);
+};
+
+// Position of 16-byte chunk c of row r: rows two (D = 128) or four (D = 64) apart
+// would meet in the same banks.
+template <int D>
+__device__ __forceinline__ int chunk_at(int r, int c) {
+    return D == 128 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1);
+}
+// Row of a 16-row tile that matrix row `s` holds: a lane's two pairs of V rows are
+// then t, t + 4 and t + 8, t + 12, whose banks differ across t.
+__device__ __forceinline__ int row_of(int s) { return (s & 8) + ((s & 7) >> 1) + 4 * (s & 1); }
+
+// O += P V for one 16-row tile.  SAFE: a position that a row does not see adds
+// nothing even where its step or minimum is not finite.
+template <int D, int NB, bool SAFE>
+__device__ __forceinline__ void add_values(float (&o)[D / 16][NB][4], float (&om)[D / 32][NB][2],
+                                           const float (&pr)[NB][4], uint32_t vcodes, uint32_t vmeta, int tile, int g,
+                                           int t) {
+    using C = Cfg<D, NB>;
+    // steps and minima of the tile's rows g and g + 8 (as the scores' layout has them)
+    const int r0 = tile * 16 + row_of(g), r1 = tile * 16 + row_of(g + 8);
+    uint32_t m0[C::kGroups], m1[C::kGroups];
+#pragma unroll
+    for (int gr = 0; gr < C::kGroups; ++gr) {
+        m0[gr] = lds32(vmeta + r0 * C::kMetaBytes + gr * 4);
+        m1[gr] = lds32(vmeta + r1 * C::kMetaBytes + gr * 4);
+    }
+#pragma unroll
+    for (int gr = 0; gr < C::kGroups; ++gr) {
+        // codes of channels 32 gr + 4 g .. + 3 of rows t, t + 4, t + 8, t + 12
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = tile * 16 + t + 4 * k;
+            w[k] = lds16(vcodes + r * C::kRowBytes + chunk_at<D>(r, gr) * 16 + g * 2);
+        }
+        const uint32_t wa = w[0] | (w[1] << 16), wb = w[2] | (w[3] << 16);
+        const uint32_t a0[4] = {minus136(pair128<0>(wa)), minus136(pair128<1>(wa)), minus136(pair128<0>(wb)),
+                                minus136(pair128<1>(wb))};
+        const uint32_t a1[4] = {minus136(pair128<2>(wa)), minus136(pair128<3>(wa)), minus136(pair128<2>(wb)),
+                                minus136(pair128<3>(wb))};
+        const float s0 = __uint_as_float(m0[gr] << 16), s1 = __uint_as_float(m1[gr] << 16);
+        const float n0 = fmaf(8.f, s0, __uint_as_float(m0[gr] & 0xffff0000u));
+        const float n1 = fmaf(8.f, s1, __uint_as_float(m1[gr] & 0xffff0000u));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const float *q = pr[nb];
+            auto times = [](float a, float b) { return SAFE && a == 0.f ? 0.f : a * b; };
+            // p s is rounded to bf16 here: 2^-9 of each term, as P is in the dense kernels
+            const uint32_t b[2] = {transpose8(pack_bf16(times(q[0], s0), times(q[1], s0))),
+                                   transpose8(pack_bf16(times(q[2], s1), times(q[3], s1)))};
+            mma(o[2 * gr][nb], a0, b);
+            mma(o[2 * gr + 1][nb], a1, b);
+            om[gr][nb][0] += times(q[0], n0) + times(q[2], n1);
+            om[gr][nb][1] += times(q[1], n0) + times(q[3], n1);
+        }
+    }
+}
+
+template <int D, int NB>
+__global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_kernel(const __grid_constant__ DecodeParams p) {
+    using C = Cfg<D, NB>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long pre[kMaxSeqs + 1];
+    grid_dep_launch();  // the joining kernel may be set up meanwhile; it waits for this one's end
+    prefix_steps(p, pre, blockIdx.x == 0);
+    const int HC = p.Hkv * p.chunks;
+    const long long W = pre[p.B] * HC;
+    const int used = ctas_used(W, gridDim.x);
+    if (static_cast<int>(blockIdx.x) >= used) return;
+    const long long begin = range_begin(W, used, blockIdx.x), end = range_begin(W, used, blockIdx.x + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t pipe = smem_addr(smem) + warp * C::kStages * 2 * C::kHalfStage;
+    float *jo = reinterpret_cast<float *>(smem);                      // [warp][row][kOutStride]
+    float *jm = jo + kWarps * C::kRows * C::kOutStride, *jl = jm + kWarps * C::kRows;  // [warp][row]
+
+    for (long long pos = begin; pos < end;) {
+        int lo = 0, hi = p.B - 1;  // the sequence that holds step `pos`: the last that begins at or before it
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (pre[mid] * HC <= pos) lo = mid;
+            else hi = mid - 1;
+        }
+        const int b = lo;
+        const Span sp = span_of(p, b);
+        const long long rel = pos - pre[b] * HC;
+        const int hc = static_cast<int>(rel / sp.steps), j0 = static_cast<int>(rel - static_cast<long long>(hc) * sp.steps);
+        const int j1 = static_cast<int>(min(static_cast<long long>(sp.steps), j0 + (end - pos)));
+        const int h = hc / p.chunks, row0 = (hc - h * p.chunks) * C::kRows;
+        const int n_rows = min(C::kRows, p.rows - row0);
+        const size_t plane = (static_cast<size_t>(b) * p.Hkv + h) * p.cap;
+        const size_t qrow = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.L + row0;
+
+        // copies of step j into stage st: codes in 16-byte chunks, steps and minima row by row
+        auto issue = [&](int j, int st) {
+            const int key0 = (j < sp.fs ? j : j + sp.gap) * kStep;
+            const uint32_t base = pipe + st * 2 * C::kHalfStage;
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                const uint8_t *codes = which ? p.vc : p.kc;
+                const uint32_t *meta = which ? p.vm : p.km;
+                const uint32_t dst = base + which * C::kHalfStage;
+                constexpr int kChunks = C::kRowBytes / 16;
+#pragma unroll
+                for (int i = 0; i < kStep * kChunks / 32; ++i) {
+                    const int r = (i * 32 + lane) / kChunks, c = (i * 32 + lane) % kChunks;
+                    const bool in = key0 + r < sp.n;
+                    cp_async<16>(dst + r * C::kRowBytes + chunk_at<D>(r, c) * 16,
+                                 codes + (plane + (in ? key0 + r : 0)) * C::kRowBytes + c * 16, in);
+                }
+                const bool in = key0 + lane < sp.n;
+                cp_async<C::kMetaBytes>(dst + kStep * C::kRowBytes + lane * C::kMetaBytes,
+                                        meta + (plane + (in ? key0 + lane : 0)) * C::kGroups, in);
+            }
+        };
+#pragma unroll
+        for (int st = 0; st < C::kStages - 1; ++st) {
+            if (j0 + warp + st * kWarps < j1) issue(j0 + warp + st * kWarps, st);
+            cp_commit();
+        }
+
+        // the query rows as B fragments: lane (g, t) holds row g's channels 32 gr + 8 t ..
+        // + 7, paired as the codes are (i, i + 4); qs: sums over a group for rows 2 t, 2 t + 1
+        uint32_t bq[NB][C::kGroups][2][2];
+        float qs[NB][C::kGroups][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int gr = 0; gr < C::kGroups; ++gr) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (8 * nb + g < n_rows)
+                    v = __ldg(reinterpret_cast<const uint4 *>(p.q + (qrow + 8 * nb + g) * D + 32 * gr + 8 * t));
+                bq[nb][gr][0][0] = __byte_perm(v.x, v.z, 0x5410);
+                bq[nb][gr][0][1] = __byte_perm(v.x, v.z, 0x7632);
+                bq[nb][gr][1][0] = __byte_perm(v.y, v.w, 0x5410);
+                bq[nb][gr][1][1] = __byte_perm(v.y, v.w, 0x7632);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                float s = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xffff0000u);
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                qs[nb][gr][0] = __shfl_sync(0xffffffffu, s, 8 * t);
+                qs[nb][gr][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4);
+            }
+        }
+
+        float o[D / 16][NB][4], om[C::kGroups][NB][2], m[NB][2], l[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][nb][e] = 0.f;
+#pragma unroll
+            for (int gr = 0; gr < C::kGroups; ++gr) om[gr][nb][0] = om[gr][nb][1] = 0.f;
+            m[nb][0] = m[nb][1] = -CUDART_INF_F;
+            l[nb][0] = l[nb][1] = 0.f;
+        }
+
+        int st = 0;
+        for (int j = j0 + warp; j < j1; j += kWarps) {
+            const int ahead = j + (C::kStages - 1) * kWarps;
+            if (ahead < j1) issue(ahead, st == 0 ? C::kStages - 1 : st - 1);
+            cp_commit();
+            cp_wait<C::kStages - 1>();
+            __syncwarp();
+            const uint32_t kcodes = pipe + st * 2 * C::kHalfStage, kmeta = kcodes + kStep * C::kRowBytes;
+            const uint32_t vcodes = kcodes + C::kHalfStage, vmeta = vcodes + kStep * C::kRowBytes;
+            st = st + 1 == C::kStages ? 0 : st + 1;
+            const int key0 = (j < sp.fs ? j : j + sp.gap) * kStep;
+
+            // scores: [tile][nb][(row g, rows 2t, 2t + 1), (row g + 8, ..)], log2 units
+            float sc[2][NB][4];
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                const int r0 = tile * 16 + row_of(g), r1 = tile * 16 + row_of(g + 8);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[tile][nb][e] = 0.f;
+#pragma unroll
+                for (int gr = 0; gr < C::kGroups; ++gr) {
+                    const uint32_t w0 = lds32(kcodes + r0 * C::kRowBytes + chunk_at<D>(r0, gr) * 16 + t * 4);
+                    const uint32_t w1 = lds32(kcodes + r1 * C::kRowBytes + chunk_at<D>(r1, gr) * 16 + t * 4);
+                    const uint32_t k0 = lds32(kmeta + r0 * C::kMetaBytes + gr * 4);
+                    const uint32_t k1 = lds32(kmeta + r1 * C::kMetaBytes + gr * 4);
+                    const uint32_t a0[4] = {pair128<0>(w0), pair128<0>(w1), pair128<1>(w0), pair128<1>(w1)};
+                    const uint32_t a1[4] = {pair128<2>(w0), pair128<2>(w1), pair128<3>(w0), pair128<3>(w1)};
+                    const float s0 = __uint_as_float(k0 << 16), s1 = __uint_as_float(k1 << 16);
+                    // the minimum, less what the 128 in every code adds
+                    const float n0 = fmaf(-128.f, s0, __uint_as_float(k0 & 0xffff0000u));
+                    const float n1 = fmaf(-128.f, s1, __uint_as_float(k1 & 0xffff0000u));
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma(acc, a0, bq[nb][gr][0]);
+                        mma(acc, a1, bq[nb][gr][1]);
+                        sc[tile][nb][0] = fmaf(s0, acc[0], fmaf(n0, qs[nb][gr][0], sc[tile][nb][0]));
+                        sc[tile][nb][1] = fmaf(s0, acc[1], fmaf(n0, qs[nb][gr][1], sc[tile][nb][1]));
+                        sc[tile][nb][2] = fmaf(s1, acc[2], fmaf(n1, qs[nb][gr][0], sc[tile][nb][2]));
+                        sc[tile][nb][3] = fmaf(s1, acc[3], fmaf(n1, qs[nb][gr][1], sc[tile][nb][3]));
+                    }
+                }
+            }
+            if (p.softcap > 0.f) {
+                const float u = p.scale / p.softcap, cap2 = p.softcap * kLog2e;
+#pragma unroll
+                for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[tile][nb][e] = cap2 * tanhf(sc[tile][nb][e] * u);
+            } else {
+#pragma unroll
+                for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[tile][nb][e] *= p.scale_log2;
+            }
+            // only steps at the causal edge, the tail or the window's edge hold hidden pairs
+            const int p0 = sp.n - p.L;  // position of a sequence's first new row
+            const bool edge = key0 + kStep - 1 > p0 ||
+                              (p.window > 0 && static_cast<long long>(key0) <= static_cast<long long>(sp.n) - 1 - p.window &&
+                               key0 + kStep > p.first);
+            if (edge) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int hi_k = p0 + (row0 + 8 * nb + 2 * t + e) % p.L;
+                        const long long lo_k = p.window > 0 ? static_cast<long long>(hi_k) - p.window + 1 : 0;
+#pragma unroll
+                        for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const int k = key0 + tile * 16 + row_of(g + 8 * half);
+                                if (k > hi_k || (k < lo_k && k >= p.first)) sc[tile][nb][2 * half + e] = -CUDART_INF_F;
+                            }
+                    }
+            }
+
+            // running maximum, kept until a score exceeds it by more than 2^8
+            bool grow = false;
+            float top[NB][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    top[nb][e] = fmaxf(fmaxf(sc[0][nb][e], sc[0][nb][2 + e]), fmaxf(sc[1][nb][e], sc[1][nb][2 + e]));
+                    grow |= top[nb][e] - m[nb][e] > 8.f;  // (false where both are -inf)
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = top[nb][e];
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                        x = fmaxf(x, m[nb][e]);
+                        const float f = m[nb][e] == -CUDART_INF_F ? 0.f : ex2(m[nb][e] - x);
+                        m[nb][e] = x;
+                        l[nb][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            o[i][nb][e] *= f;
+                            o[i][nb][2 + e] *= f;
+                        }
+#pragma unroll
+                        for (int gr = 0; gr < C::kGroups; ++gr) om[gr][nb][e] *= f;
+                    }
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mm = m[nb][e] == -CUDART_INF_F ? 0.f : m[nb][e];
+#pragma unroll
+                    for (int tile = 0; tile < 2; ++tile) {
+                        sc[tile][nb][e] = ex2(sc[tile][nb][e] - mm);
+                        sc[tile][nb][2 + e] = ex2(sc[tile][nb][2 + e] - mm);
+                        l[nb][e] += sc[tile][nb][e] + sc[tile][nb][2 + e];
+                    }
+                }
+            if (edge) {
+                add_values<D, NB, true>(o, om, sc[0], vcodes, vmeta, 0, g, t);
+                add_values<D, NB, true>(o, om, sc[1], vcodes, vmeta, 1, g, t);
+            } else {
+                add_values<D, NB, false>(o, om, sc[0], vcodes, vmeta, 0, g, t);
+                add_values<D, NB, false>(o, om, sc[1], vcodes, vmeta, 1, g, t);
+            }
+            __syncwarp();  // every lane has read the stage that the next copies fill
+        }
+        cp_wait<0>();
+
+        // join the warps: sums over the lanes that share a row, then m, l and O to shared memory
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], x);
+#pragma unroll
+                    for (int gr = 0; gr < C::kGroups; ++gr)
+                        om[gr][nb][e] += __shfl_xor_sync(0xffffffffu, om[gr][nb][e], x);
+                }
+            }
+        __syncthreads();  // every warp's copies have landed and been read
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 8 * nb + 2 * t + e;
+                float *dst = jo + (warp * C::kRows + row) * C::kOutStride;
+#pragma unroll
+                for (int gr = 0; gr < C::kGroups; ++gr)
+                    *reinterpret_cast<float4 *>(dst + 32 * gr + 4 * g) =
+                        make_float4(o[2 * gr][nb][e] + om[gr][nb][e], o[2 * gr][nb][2 + e] + om[gr][nb][e],
+                                    o[2 * gr + 1][nb][e] + om[gr][nb][e], o[2 * gr + 1][nb][2 + e] + om[gr][nb][e]);
+                if (g == 0) {
+                    jm[warp * C::kRows + row] = m[nb][e];
+                    jl[warp * C::kRows + row] = l[nb][e];
+                }
+            }
+        __syncthreads();
+        const bool whole = j0 == 0 && j1 == sp.steps;
+        float *slot = p.part + static_cast<size_t>(2 * blockIdx.x + (pos > begin ? 1 : 0)) * C::kSlotFloats;
+        for (int i = threadIdx.x; i < n_rows * (D / 4); i += 32 * kWarps) {
+            const int row = i / (D / 4), c4 = i % (D / 4);
+            float mx = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, jm[w * C::kRows + row]);
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float mw = jm[w * C::kRows + row];
+                if (mw == -CUDART_INF_F) continue;  // a warp without a visible position
+                const float f = ex2(mw - mx);
+                const float4 v = *reinterpret_cast<const float4 *>(jo + (w * C::kRows + row) * C::kOutStride + 4 * c4);
+                sum = fmaf(f, jl[w * C::kRows + row], sum);
+                a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
+            }
+            if (whole) {
+                if (p.sinks && mx > -CUDART_INF_F)
+                    sum += ex2(fmaf(__ldg(p.sinks + h * p.G + (row0 + row) / p.L), kLog2e, -mx));
+                const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+                *reinterpret_cast<uint2 *>(p.o + (qrow + row) * D + 4 * c4) =
+                    make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+            } else {
+                __stcg(reinterpret_cast<float4 *>(slot + row * D + 4 * c4), a);
+                if (c4 == 0) {
+                    __stcg(slot + C::kRows * D + row, mx);
+                    __stcg(slot + C::kRows * (D + 1) + row, sum);
+                }
+            }
+        }
+        __syncthreads();  // before the next segment's copies
+        pos += j1 - j0;
+    }
+}
+
+// Joins the pieces of the segments that were cut, and writes zeros for a sequence
+// without a position.  One block per segment.
+template <int D, int NB>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeParams p, int grid) {
+    using C = Cfg<D, NB>;
+    __shared__ long long pre[kMaxSeqs + 1];
+    prefix_steps(p, pre, false);  // the lengths are the caller's: no need to wait for them
+    const int HC = p.Hkv * p.chunks;
+    const int b = blockIdx.x / HC, hc = blockIdx.x - b * HC;
+    const int h = hc / p.chunks, row0 = (hc - h * p.chunks) * C::kRows;
+    const int n_rows = min(C::kRows, p.rows - row0);
+    const size_t qrow = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.L + row0;
+    const long long W = pre[p.B] * HC;
+    const int steps = static_cast<int>(pre[b + 1] - pre[b]);
+    if (steps == 0) {
+        grid_dep_wait();
+        for (int i = threadIdx.x; i < n_rows * (D / 4); i += 128)
+            *reinterpret_cast<uint2 *>(p.o + (qrow + i / (D / 4)) * D + 4 * (i % (D / 4))) = make_uint2(0u, 0u);
+        return;
+    }
+    const int used = ctas_used(W, grid);
+    const long long x0 = pre[b] * HC + static_cast<long long>(hc) * steps, x1 = x0 + steps;
+    auto cta_of = [&](long long x) {  // the CTA whose range holds step x
+        int c = static_cast<int>(x * used / W);
+        while (c + 1 < used && range_begin(W, used, c + 1) <= x) ++c;
+        while (range_begin(W, used, c) > x) --c;
+        return c;
+    };
+    const int c0 = cta_of(x0), c1 = cta_of(x1 - 1);
+    grid_dep_wait();
+    if (c0 == c1) return;  // it was finished where it was computed
+    auto slot_of = [&](int c) {
+        return p.part + static_cast<size_t>(2 * c + (c == c0 && range_begin(W, used, c) < x0 ? 1 : 0)) * C::kSlotFloats;
+    };
+    for (int i = threadIdx.x; i < n_rows * (D / 4); i += 128) {
+        const int row = i / (D / 4), c4 = i % (D / 4);
+        float mx = -CUDART_INF_F, sum = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kBatch = 8;  // pieces whose loads are in flight together
+        for (int k0 = c0; k0 <= c1; k0 += kBatch) {
+            float mk[kBatch], lk[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const bool in = k0 + u <= c1;
+                const float *s = slot_of(in ? k0 + u : k0);
+                mk[u] = in ? __ldcg(s + C::kRows * D + row) : -CUDART_INF_F;
+                lk[u] = __ldcg(s + C::kRows * (D + 1) + row);
+                v[u] = __ldcg(reinterpret_cast<const float4 *>(s + row * D + 4 * c4));
+            }
+            float mn = mx;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, mk[u]);
+            const float f0 = mx == -CUDART_INF_F ? 0.f : ex2(mx - mn);
+            sum *= f0, a.x *= f0, a.y *= f0, a.z *= f0, a.w *= f0;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (mk[u] == -CUDART_INF_F) continue;
+                const float f = ex2(mk[u] - mn);
+                sum = fmaf(f, lk[u], sum);
+                a.x = fmaf(f, v[u].x, a.x), a.y = fmaf(f, v[u].y, a.y);
+                a.z = fmaf(f, v[u].z, a.z), a.w = fmaf(f, v[u].w, a.w);
+            }
+            mx = mn;
+        }
+        if (p.sinks && mx > -CUDART_INF_F) sum += ex2(fmaf(__ldg(p.sinks + h * p.G + (row0 + row) / p.L), kLog2e, -mx));
+        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        *reinterpret_cast<uint2 *>(p.o + (qrow + row) * D + 4 * c4) =
+            make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+    }
+}
+
+}  // namespace kv4
+}  // namespace tfa

@@ -67,3 +67,77 @@ def test_rope_inv_freq_refusals():
     for a in (dict(rot=7), dict(rot=-2), dict(rot=16, scaling="other"), dict(rot=16, factor=0.0)):
         with pytest.raises(ValueError):
             tb.rope_inv_freq(device="cpu", **a)
+
+
+# ------------------------------------------------------------- the 4-bit cache
+def _append(**over):
+    a = dict(k=A16, v=A16, kc=A16, km=A16, vc=A16, vm=A16, start=A16, first=0, B=2, Hkv=2, L=5, cap=64, D=128, odd=None)
+    a.update(over)
+    return tb.lib().tfa_kv4_append(a["k"], a["v"], _strides(6, a["odd"]), a["kc"], a["km"], a["vc"], a["vm"], a["start"],
+                                   a["first"], a["B"], a["Hkv"], a["L"], a["cap"], a["D"], None)
+
+
+def _read(**over):
+    a = dict(k=A16, v=A16, kc=A16, km=A16, vc=A16, vm=A16, start=A16, first=0, B=2, Hkv=2, L=5, cap=64, D=128)
+    a.update(over)
+    return tb.lib().tfa_kv4_read(a["kc"], a["km"], a["vc"], a["vm"], a["k"], a["v"], a["start"], a["first"], a["B"],
+                                 a["Hkv"], a["L"], a["cap"], a["D"], None)
+
+
+@pytest.mark.parametrize("call", [_append, _read])
+@pytest.mark.parametrize("over,code", [
+    (dict(k=None), tb.TFA_ERR_NULL),
+    (dict(vm=None), tb.TFA_ERR_NULL),
+    (dict(kc=None), tb.TFA_ERR_NULL),
+    (dict(Hkv=0), tb.TFA_ERR_HEADS),
+    (dict(B=0), tb.TFA_ERR_SHAPE),
+    (dict(L=0), tb.TFA_ERR_SHAPE),
+    (dict(cap=0), tb.TFA_ERR_SHAPE),
+    (dict(cap=(1 << 30) + 1), tb.TFA_ERR_SHAPE),
+    (dict(B=1 << 20, Hkv=1 << 10, L=1 << 20, cap=1 << 10), tb.TFA_ERR_SHAPE),
+    (dict(D=96), tb.TFA_ERR_HEAD_DIM),
+    (dict(start=None, first=-1), tb.TFA_ERR_CACHE),
+    (dict(start=None, first=60), tb.TFA_ERR_CACHE),
+    (dict(start=None, first=2 ** 31 - 1), tb.TFA_ERR_CACHE),
+    (dict(v=MIS), tb.TFA_ERR_ALIGN),
+    (dict(km=MIS), tb.TFA_ERR_ALIGN),
+    (dict(start=ctypes.c_void_p(0x10002)), tb.TFA_ERR_ALIGN),
+])
+def test_cache_refusals(call, over, code):
+    assert call(**over) == code
+
+
+def test_append_refuses_odd_strides():
+    for i in range(6):
+        assert _append(odd=i) == tb.TFA_ERR_ALIGN
+
+
+def _decode(**over):
+    a = dict(q=A16, kc=A16, km=A16, vc=A16, vm=A16, lens=A16, o=A16, B=2, Hq=8, Hkv=2, L=1, cap=64, D=128, scale=0.1,
+             window=0, first=0, softcap=0.0, sinks=None, ws=A16)
+    a.update(over)
+    return tb.lib().tfa_kv4_decode(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(q=None), tb.TFA_ERR_NULL),
+    (dict(lens=None), tb.TFA_ERR_NULL),
+    (dict(ws=None), tb.TFA_ERR_NULL),
+    (dict(vc=None), tb.TFA_ERR_NULL),
+    (dict(Hq=7), tb.TFA_ERR_HEADS),
+    (dict(Hq=0), tb.TFA_ERR_HEADS),
+    (dict(L=0), tb.TFA_ERR_SHAPE),
+    (dict(L=9), tb.TFA_ERR_SHAPE),
+    (dict(B=1025), tb.TFA_ERR_SHAPE),
+    (dict(D=32), tb.TFA_ERR_HEAD_DIM),
+    (dict(first=-1, window=4), tb.TFA_ERR_WINDOW),
+    (dict(first=4), tb.TFA_ERR_WINDOW),
+    (dict(scale=float("nan")), tb.TFA_ERR_SCALE),
+    (dict(softcap=-1.0), tb.TFA_ERR_SOFTCAP),
+    (dict(softcap=1.0, scale=0.0), tb.TFA_ERR_SOFTCAP),
+    (dict(o=MIS), tb.TFA_ERR_ALIGN),
+    (dict(ws=MIS), tb.TFA_ERR_ALIGN),
+    (dict(sinks=ctypes.c_void_p(0x10002)), tb.TFA_ERR_ALIGN),
+])
+def test_kv4_decode_refusals(over, code):
+    assert _decode(**over) == code
