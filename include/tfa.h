@@ -304,6 +304,28 @@ int tfa_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void
                               tfa_stream_t stream);
 size_t tfa_qk_norm_rope_workspace(int D);
 
+/* tfa_prefill_first -- causal attention with a sliding window and `first` first
+ * tokens that stay visible outside it, for any L >= 1: row i (position p = S - L
+ * + i) sees key j iff j <= p and (j > p - window or j < first), and the key mask
+ * keeps it.  window > 0 and first >= 0, else TFA_ERR_WINDOW; with first = 0 it is
+ * tfa_prefill's window.  Key tiles that hold neither first tokens nor window are
+ * skipped without loading them.
+ *   lse      NULL, or as for tfa_prefill_lse (not with softcap or sinks:
+ *            TFA_ERR_SOFTCAP)
+ *   softcap, sinks  as for tfa_attention_ex
+ * Layouts, ownership, errors, scratch and graph capture as for tfa_prefill. */
+int tfa_prefill_first(const void *q, const void *k, const void *v, void *o, float *lse,
+                      int B, int Hq, int Hkv, int L, int S, int D, float scale, int window, int first,
+                      const float *key_mask, float softcap, const float *sinks, tfa_stream_t stream);
+
+/* tfa_prefill_first_backward -- gradients of tfa_prefill_first (no softcap, no
+ * sinks) from its saved output and log-sum-exp; arguments, workspace and errors as
+ * for tfa_prefill_backward_saved. */
+int tfa_prefill_first_backward(const void *q, const void *k, const void *v, const void *o,
+                               const float *lse, const void *dout, void *dq, void *dk, void *dv,
+                               int B, int Hq, int Hkv, int L, int S, int D, float scale,
+                               int window, int first, const float *key_mask, tfa_stream_t stream);
+
 /* The 4-bit key/value cache.  Per position and KV head the D channels (64 or 128)
  * are held in groups of 32: a minimum m and a step s = bf16((max - m) / 15), both
  * bf16, and a 4-bit code c = rint((x - m) / s) in [0, 15] per channel (all 0 where

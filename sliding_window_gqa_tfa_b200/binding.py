@@ -115,6 +115,10 @@ def lib():
             L.tfa_qk_norm_rope.restype = i32
             L.tfa_qk_norm_rope_backward.argtypes = [P] * 8 + [LL, P, P, P, P, i32, i32] + dims + [f32, f32, P, P]
             L.tfa_qk_norm_rope_backward.restype = i32
+            L.tfa_prefill_first.argtypes = [P] * 5 + [i32] * 6 + [f32, i32, i32, P, f32, P, P]
+            L.tfa_prefill_first.restype = i32
+            L.tfa_prefill_first_backward.argtypes = [P] * 9 + [i32] * 6 + [f32, i32, i32, P, P]
+            L.tfa_prefill_first_backward.restype = i32
             L.tfa_kv4_append.argtypes = [P, P, LL] + [P] * 5 + [i32] * 6 + [P]
             L.tfa_kv4_append.restype = i32
             L.tfa_kv4_read.argtypes = [P] * 7 + [i32] * 6 + [P]
@@ -250,11 +254,12 @@ def _check(t, name, dtype, ndim):
 
 
 def prefill(q, k, v, *, scale=None, causal=True, window=0, key_mask=None, out=None, stream=None,
-            debug_flags=0, softcap=0.0, sinks=None):
+            debug_flags=0, softcap=0.0, sinks=None, first=0):
     """Attention output [B,Hq,L,D] bf16 for bf16 q [B,Hq,L,D], k/v [B,Hkv,S,D] on one GPU.
 
     L >= 9 goes to tfa_prefill, 1 <= L <= 8 to tfa_decode; a softcap > 0 or
-    sinks (fp32 [Hq] on the device) go to tfa_attention_ex.  key_mask: optional
+    sinks (fp32 [Hq] on the device) go to tfa_attention_ex, first > 0 (first tokens
+    that stay visible outside a causal window) to tfa_prefill_first.  key_mask: optional
     fp32 [B,S] (1 keep / 0 drop).  Raises TfaError on a nonzero status."""
     import torch
 
@@ -284,13 +289,21 @@ def prefill(q, k, v, *, scale=None, causal=True, window=0, key_mask=None, out=No
             float(scale), int(bool(causal)), int(window),
             ctypes.c_void_p(key_mask.data_ptr()) if key_mask is not None else None,
             _stream_handle(stream))
-    if softcap or sinks is not None:
+    if softcap or sinks is not None or first:
         if debug_flags:
             raise ValueError("debug flags apply to tfa_prefill_debug only")
         if sinks is not None:
             _check(sinks, "sinks", torch.float32, 1)
             if sinks.shape[0] != Hq:
                 raise ValueError("sinks must hold one logit per query head")
+        if first:
+            if not causal:
+                raise ValueError("first tokens need causal attention with a window")
+            rc = lib().tfa_prefill_first(*args[:4], None, *args[4:11], int(window), int(first), args[13], float(softcap),
+                                         _ptr_or_none(sinks), args[14])
+            if rc != TFA_OK:
+                raise TfaError(rc, "tfa_prefill_first")
+            return out
         rc = tfa_attention_ex(*args[:14], float(softcap),
                               ctypes.c_void_p(sinks.data_ptr()) if sinks is not None else None,
                               args[14])
@@ -317,9 +330,10 @@ def tfa_prefill_backward(q, k, v, dout, dq, dk, dv, B, Hq, Hkv, L, S, D, scale, 
 
 
 def prefill_lse(q, k, v, *, scale=None, causal=True, window=0, key_mask=None, out=None, lse=None,
-                stream=None):
+                stream=None, first=0):
     """(o, lse): the forward of any L >= 1 and each row's base-2 log-sum-exp of
-    its scaled scores, fp32 [B,Hq,L] (+inf for a row with no allowed key)."""
+    its scaled scores, fp32 [B,Hq,L] (+inf for a row with no allowed key).  first: first
+    tokens that stay visible outside a causal window."""
     import torch
 
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
@@ -335,6 +349,16 @@ def prefill_lse(q, k, v, *, scale=None, causal=True, window=0, key_mask=None, ou
     lse = torch.empty((B, Hq, L), dtype=torch.float32, device=q.device) if lse is None else lse
     _check(out, "out", torch.bfloat16, 4)
     _check(lse, "lse", torch.float32, 3)
+    if first:
+        if not causal:
+            raise ValueError("first tokens need causal attention with a window")
+        _check_first_shapes(key_mask, out, lse, B, Hq, L, S, D)
+        rc = lib().tfa_prefill_first(*(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v, out, lse)),
+                                     B, Hq, Hkv, L, S, D, float(scale), int(window), int(first),
+                                     _ptr_or_none(key_mask), 0.0, None, _stream_handle(stream))
+        if rc != TFA_OK:
+            raise TfaError(rc, "tfa_prefill_first")
+        return out, lse
     rc = lib().tfa_prefill_lse(*(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v, out, lse)),
                                B, Hq, Hkv, L, S, D, float(scale), int(bool(causal)), int(window),
                                _ptr_or_none(key_mask), _stream_handle(stream))
@@ -343,11 +367,19 @@ def prefill_lse(q, k, v, *, scale=None, causal=True, window=0, key_mask=None, ou
     return out, lse
 
 
+def _check_first_shapes(key_mask, out, lse, B, Hq, L, S, D):
+    if key_mask is not None and tuple(key_mask.shape) != (B, S):
+        raise ValueError("key_mask must be [B, S]")
+    if tuple(out.shape) != (B, Hq, L, D) or tuple(lse.shape) != (B, Hq, L):
+        raise ValueError("out and lse must be [B,Hq,L,D] and [B,Hq,L]")
+
+
 def backward(q, k, v, dout, *, scale=None, causal=True, window=0, key_mask=None, out=None,
-             saved=None, stream=None):
+             saved=None, stream=None, first=0):
     """(dq, dk, dv) bf16 of the attention core for the upstream gradient dout
     [B,Hq,L,D]: recompute-based (the forward is re-run inside), or, given
-    saved=(o, lse) from prefill_lse on the same inputs, from those."""
+    saved=(o, lse) from prefill_lse on the same inputs, from those.  first: as for
+    prefill_lse, whose result is then needed in `saved`."""
     import torch
 
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (dout, "dout")):
@@ -372,6 +404,16 @@ def backward(q, k, v, dout, *, scale=None, causal=True, window=0, key_mask=None,
         _check(lse, "lse", torch.float32, 3)
         if tuple(o.shape) != tuple(q.shape) or tuple(lse.shape) != (B, Hq, L):
             raise ValueError("saved (o, lse) have the wrong shape")
+        if first:
+            if not causal:
+                raise ValueError("first tokens need causal attention with a window")
+            _check_first_shapes(key_mask, o, lse, B, Hq, L, S, D)
+            rc = lib().tfa_prefill_first_backward(
+                *(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v, o, lse, dout, dq, dk, dv)), B, Hq, Hkv, L, S, D,
+                float(scale), int(window), int(first), _ptr_or_none(key_mask), _stream_handle(stream))
+            if rc != TFA_OK:
+                raise TfaError(rc, "tfa_prefill_first_backward")
+            return dq, dk, dv
         rc = lib().tfa_prefill_backward_saved(
             *(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v, o, lse, dout, dq, dk, dv)),
             B, Hq, Hkv, L, S, D, float(scale), int(bool(causal)), int(window), _ptr_or_none(key_mask),
@@ -379,6 +421,8 @@ def backward(q, k, v, dout, *, scale=None, causal=True, window=0, key_mask=None,
         if rc != TFA_OK:
             raise TfaError(rc, "tfa_prefill_backward_saved")
         return dq, dk, dv
+    if first:
+        raise ValueError("the gradient with first tokens takes prefill_lse's result in `saved`")
     rc = tfa_prefill_backward(*(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v, dout, dq, dk, dv)),
                               B, Hq, Hkv, L, S, D, float(scale), int(bool(causal)), int(window),
                               _ptr_or_none(key_mask), _stream_handle(stream))

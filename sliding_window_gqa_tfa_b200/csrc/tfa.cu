@@ -19,6 +19,7 @@
 
 #include "../../include/tfa.h"
 #include "tfa_bwd.cuh"
+#include "tfa_first.h"
 #include "tfa_internal.h"
 #include "tfa_kernel.cuh"
 
@@ -43,7 +44,7 @@ struct BwdScratch {
     size_t rows = 0, o_bytes = 0;
 };
 
-constexpr int kVariantsPerD = 18;  // forward kernel variants per head dim (variant_index)
+constexpr int kVariantsPerD = 30;  // forward kernel variants per head dim (variant_index)
 constexpr int kHostStages = 4;     // tfa_prefill_host: most pipeline stages per call (measured best of 4, 8, 16)
 
 struct DeviceState {
@@ -53,7 +54,7 @@ struct DeviceState {
     bool smem_attr[2 * kVariantsPerD] = {};  // per kernel variant: D, layout, key mask, score mode
     std::unordered_map<cudaStream_t, SplitScratch> split;
     std::unordered_map<cudaStream_t, BwdScratch> bwd;
-    bool bwd_attr[4] = {};  // backward kernels prepared, per (D, key mask)
+    bool bwd_attr[8] = {};  // backward kernels prepared, per (first tokens, D, key mask)
     // staging buffers of tfa_prefill_host, and its copy streams and events
     void *h_buf[5] = {nullptr, nullptr, nullptr, nullptr, nullptr};
     size_t h_cap[5] = {0, 0, 0, 0, 0};
@@ -90,22 +91,22 @@ int get_encode_fn() {
 }
 
 // Kernel variants per head dim: dense (packed x key mask x score mode: 12),
-// ring (packed x plain/softcap: 4) and varlen (plain/softcap: 2); ring and
-// varlen take no key mask and write no LSE, varlen is never packed.
+// ring (packed x plain/softcap: 4), varlen (plain/softcap: 2) and first (as dense:
+// 12); ring and varlen take no key mask and write no LSE, varlen is never packed.
 constexpr int variant_index(int D, bool km, int mode, int layout, bool pk) {
     const int sc = mode == tfa::kModeSoftcap ? 1 : 0;
     const int v = layout == tfa::kLayoutDense ? (pk ? 6 : 0) + 2 * mode + (km ? 1 : 0)
                   : layout == tfa::kLayoutRing ? 12 + (pk ? 2 : 0) + sc
-                                               : 16 + sc;
+                  : layout == tfa::kLayoutVarlen ? 16 + sc
+                                                 : 18 + (pk ? 6 : 0) + 2 * mode + (km ? 1 : 0);
     return (D == 128 ? kVariantsPerD : 0) + v;
 }
 
 // Shared-memory opt-in and the register check for one kernel variant, done
 // once per device at first use (never lazily, so a captured call needs neither).
-template <int D, bool KM, int MODE, int LY, bool PK>
-int prepare_kernel(DeviceState &st) {
+template <int D>
+int prepare_kernel(DeviceState &st, const void *kern, bool KM, int MODE, int LY, bool PK) {
     using C = tfa::Cfg<D>;
-    auto kern = tfa::tfa_prefill_kernel<D, KM, MODE, LY, PK>;
     // the largest launch of this variant: with a key mask, or a varlen table
     const int smem = KM ? C::kSmemBytesKeyMask : C::kSmemBytesVarlen;
     const int which = variant_index(D, KM, MODE, LY, PK);
@@ -125,6 +126,11 @@ int prepare_kernel(DeviceState &st) {
     st.smem_attr[which] = true;
     return TFA_OK;
 }
+template <int D, bool KM, int MODE, int LY, bool PK>
+int prepare_kernel(DeviceState &st) {
+    return prepare_kernel<D>(st, reinterpret_cast<const void *>(tfa::tfa_prefill_kernel<D, KM, MODE, LY, PK>), KM, MODE,
+                             LY, PK);
+}
 
 template <int D, bool KM>
 int prepare_bwd_kernels(DeviceState &st) {
@@ -133,7 +139,11 @@ int prepare_bwd_kernels(DeviceState &st) {
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(tfa::bwd::dkv_kernel<D, KM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(backward smem)", e);
+    for (int keys = 0; keys < 2 && e == cudaSuccess; ++keys)
+        e = cudaFuncSetAttribute(tfa::first_backward_kernel(D, KM, keys != 0), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(backward smem, first tokens)", e);
     st.bwd_attr[(D == 128 ? 2 : 0) + (KM ? 1 : 0)] = true;
+    st.bwd_attr[4 + (D == 128 ? 2 : 0) + (KM ? 1 : 0)] = true;
     return TFA_OK;
 }
 
@@ -158,6 +168,11 @@ int prepare_forward_kernels(DeviceState &st) {
     if (!rc) rc = prepare_dense_kernels<D, true>(st);
     if (!rc) rc = prepare_kernel<D, false, kModePlain, kLayoutVarlen, false>(st);
     if (!rc) rc = prepare_kernel<D, false, kModeSoftcap, kLayoutVarlen, false>(st);
+    for (int v = 0; v < 12 && !rc; ++v) {
+        const bool km = (v & 1) != 0, pk = v >= 6;
+        const int mode = (v % 6) >> 1;
+        rc = prepare_kernel<D>(st, first_forward_kernel(D, km, mode, pk), km, mode, kLayoutFirst, pk);
+    }
     return rc;
 }
 
@@ -307,7 +322,8 @@ struct Addressing {
     int ring_rows = 0;  // rotating cache: K/V [B, Hkv, ring_rows, D], key j in row j mod ring_rows
     const int *cu_q = nullptr, *cu_k = nullptr;  // packed variable-length batch (device, [B+1])
     int total_q = 0, total_k = 0;
-    float *lse = nullptr;  // optional per-row log-sum-exp output (dense layout only)
+    float *lse = nullptr;  // optional per-row log-sum-exp output (dense and first layouts only)
+    int first = 0;  // first tokens that stay visible outside the window (dense rows otherwise)
 };
 
 template <int D>
@@ -347,8 +363,10 @@ int launch(DeviceState &st, const void *q, const void *k, const void *v, void *o
     const bool sc = softcap > 0.f;
     if (sc && ad.lse) return TFA_ERR_SOFTCAP;  // no variant computes both (the backward has no softcap)
     const int mode = ad.lse ? tfa::kModeLse : sc ? tfa::kModeSoftcap : tfa::kModePlain;
-    const int layout = varlen ? tfa::kLayoutVarlen : ad.ring_rows ? tfa::kLayoutRing : tfa::kLayoutDense;
-    if (layout != tfa::kLayoutDense && (key_mask || ad.lse)) return TFA_ERR_RING;  // not instantiated
+    const bool first = ad.first > 0;
+    const int layout = varlen ? tfa::kLayoutVarlen : ad.ring_rows ? tfa::kLayoutRing
+                       : first ? tfa::kLayoutFirst : tfa::kLayoutDense;
+    if ((varlen || ad.ring_rows) && (key_mask || ad.lse || first)) return TFA_ERR_RING;  // not instantiated
     if (varlen && packed) return TFA_ERR_RING;  // not instantiated
     using Kern = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const tfa::Params);
     using namespace tfa;
@@ -367,7 +385,8 @@ int launch(DeviceState &st, const void *q, const void *k, const void *v, void *o
          tfa_prefill_kernel<D, false, kModeSoftcap, kLayoutRing, true>}};
     static const Kern vlen[2] = {tfa_prefill_kernel<D, false, kModePlain, kLayoutVarlen, false>,
                                  tfa_prefill_kernel<D, false, kModeSoftcap, kLayoutVarlen, false>};
-    const Kern kern = layout == kLayoutDense ? dense[packed ? 1 : 0][mode][key_mask ? 1 : 0]
+    const Kern kern = first ? reinterpret_cast<Kern>(const_cast<void *>(first_forward_kernel(D, key_mask != nullptr, mode, packed)))
+                      : layout == kLayoutDense ? dense[packed ? 1 : 0][mode][key_mask ? 1 : 0]
                       : layout == kLayoutRing ? ring[packed ? 1 : 0][sc ? 1 : 0]
                                               : vlen[sc ? 1 : 0];
     const int smem = key_mask ? C::kSmemBytesKeyMask : varlen ? C::kSmemBytesVarlen : C::kSmemBytes;
@@ -410,8 +429,13 @@ int launch(DeviceState &st, const void *q, const void *k, const void *v, void *o
     sh.causal = p.causal;
     sh.window = p.window;
     sh.flags = p.flags;
+    sh.first = ad.first;
     sh.n_qp = tfa::shape_n_qp(L);
-    p.W = varlen ? 0 : tfa::total_steps(sh);  // varlen: per-sequence lengths live on the device
+    auto steps_of = [&](const tfa::Shape &x) { return first ? tfa::total_steps<true>(x) : tfa::total_steps(x); };
+    auto makespan = [&](const tfa::Shape &x) {
+        return first ? tfa::makespan_estimate<true>(x, p.W) : tfa::makespan_estimate(x, p.W);
+    };
+    p.W = varlen ? 0 : steps_of(sh);  // varlen: per-sequence lengths live on the device
     // Head pairs for causal calls whose items are short (at most 16 key tiles
     // on average) when a KV group has an even number of query heads: a pair of
     // consecutive query tiles spends one step on the later tile alone (the
@@ -424,7 +448,7 @@ int launch(DeviceState &st, const void *q, const void *k, const void *v, void *o
         sh.hp = 1;
         sh.Hq = Hq / 2;
         sh.n_qp = tfa::shape_n_qp(L, 1);
-        if (!varlen) p.W = tfa::total_steps(sh);
+        if (!varlen) p.W = steps_of(sh);
     }
     const long long n_items = static_cast<long long>(B) * sh.Hq * sh.n_qp;
     // whole-item schedule, and the split one when scratch exists and the
@@ -436,7 +460,7 @@ int launch(DeviceState &st, const void *q, const void *k, const void *v, void *o
         tfa::Shape sp = sh;
         sp.split = 1;
         sp.grid = p.W < st.sm_count ? static_cast<int>(p.W) : st.sm_count;
-        if (force_split || tfa::makespan_estimate(sp, p.W) < tfa::makespan_estimate(sh, p.W)) sh = sp;
+        if (force_split || makespan(sp) < makespan(sh)) sh = sp;
     }
     if (!sh.split) ss = nullptr;
     p.partial = ss ? ss->partial : nullptr;
@@ -638,7 +662,8 @@ template <int D>
 int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void *q, const void *k,
                   const void *v, const void *dout, void *dq, void *dk, void *dv, int B, int Hq,
                   int Hkv, int L, int S, float scale, int causal, int window, const float *key_mask,
-                  cudaStream_t stream, const void *o_saved = nullptr, const float *lse_saved = nullptr) {
+                  cudaStream_t stream, const void *o_saved = nullptr, const float *lse_saved = nullptr,
+                  int first = 0) {
     namespace bw = tfa::bwd;
     const void *o = o_saved;
     const float *lse = lse_saved;
@@ -662,7 +687,7 @@ int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void 
     if (encode_map(&mq, q, L, B * Hq, D) || encode_map(&mdo, dout, L, B * Hq, D) ||
         encode_map(&mk, k, S, B * Hkv, D) || encode_map(&mv, v, S, B * Hkv, D))
         return TFA_ERR_CUDA;
-    if (!st.bwd_attr[(D == 128 ? 2 : 0) + (key_mask ? 1 : 0)]) return drv_fail("backward kernel not prepared", D);
+    if (!st.bwd_attr[(first ? 4 : 0) + (D == 128 ? 2 : 0) + (key_mask ? 1 : 0)]) return drv_fail("backward kernel not prepared", D);
     bw::BwdParams p;
     p.dq = static_cast<__nv_bfloat16 *>(dq);
     p.dk = static_cast<__nv_bfloat16 *>(dk);
@@ -679,18 +704,23 @@ int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void 
     p.G = Hq / Hkv;
     p.causal = causal ? 1 : 0;
     p.window = (causal && window > 0) ? window : 0;
+    p.first = first;
     p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
     const int smem = bw::Cfg<D>::kSmemBytes;
     const long long nq_items = static_cast<long long>(B) * Hq * ((L + tfa::kBlockQ - 1) / tfa::kBlockQ);
     p.n_items = static_cast<int>(nq_items);
-    auto dq_kern = key_mask ? bw::dq_kernel<D, true> : bw::dq_kernel<D, false>;
+    using Kern = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const bw::BwdParams);
+    auto first_kern = [&](bool keys) {
+        return reinterpret_cast<Kern>(const_cast<void *>(tfa::first_backward_kernel(D, key_mask != nullptr, keys)));
+    };
+    const Kern dq_kern = first ? first_kern(false) : key_mask ? Kern(bw::dq_kernel<D, true>) : Kern(bw::dq_kernel<D, false>);
     dq_kern<<<static_cast<int>(nq_items < st.sm_count ? nq_items : st.sm_count), bw::kThreads, smem, stream>>>(
         mq, mdo, mk, mv, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail("dQ kernel launch", e);
     const long long nk_items = static_cast<long long>(B) * Hkv * ((S + tfa::kBlockK - 1) / tfa::kBlockK);
     p.n_items = static_cast<int>(nk_items);
-    auto dkv_kern = key_mask ? bw::dkv_kernel<D, true> : bw::dkv_kernel<D, false>;
+    const Kern dkv_kern = first ? first_kern(true) : key_mask ? Kern(bw::dkv_kernel<D, true>) : Kern(bw::dkv_kernel<D, false>);
     // Programmatic stream serialisation: the dK/dV CTAs start on the SMs the
     // dQ kernel's CTAs leave (the two kernels are independent; dK/dV waits for
     // dQ's completion only before it exits).
@@ -776,6 +806,55 @@ extern "C" int tfa_prefill_backward_saved(const void *q, const void *k, const vo
                                            causal, window, key_mask, s, o, lse)
                       : backward_impl<64>(*st, nullptr, *bs, q, k, v, dout, dq, dk, dv, B, Hq, Hkv, L, S, scale,
                                           causal, window, key_mask, s, o, lse);
+}
+
+extern "C" int tfa_prefill_first(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Hq,
+                                 int Hkv, int L, int S, int D, float scale, int window, int first,
+                                 const float *key_mask, float softcap, const float *sinks, tfa_stream_t stream) {
+    const bool decode = L >= 1 && L <= TFA_MAX_DECODE_ROWS;
+    int rc = validate(q, k, v, o, B, Hq, Hkv, L, S, D, scale, 1, window, key_mask, true, decode);
+    if (rc) return rc;
+    if (window <= 0 || first < 0) return TFA_ERR_WINDOW;
+    if (!std::isfinite(softcap) || softcap < 0.f || (softcap > 0.f && scale == 0.f) || (lse && (softcap > 0.f || sinks)))
+        return TFA_ERR_SOFTCAP;
+    if ((reinterpret_cast<uintptr_t>(sinks) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return TFA_ERR_ALIGN;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    DeviceState *st = nullptr;
+    SplitScratch *ss = nullptr;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    if ((rc = device_state(s, &st)) || (rc = split_scratch(*st, s, &ss))) return rc;
+    Addressing ad;
+    ad.lse = lse;
+    ad.first = first < S ? first : S;
+    return (D == 128) ? launch<128>(*st, q, k, v, o, B, Hq, Hkv, L, S, scale, 1, window, key_mask, s, 0u, ss, false,
+                                    decode, softcap, sinks, ad)
+                      : launch<64>(*st, q, k, v, o, B, Hq, Hkv, L, S, scale, 1, window, key_mask, s, 0u, ss, false,
+                                   decode, softcap, sinks, ad);
+}
+
+extern "C" int tfa_prefill_first_backward(const void *q, const void *k, const void *v, const void *o,
+                                          const float *lse, const void *dout, void *dq, void *dk, void *dv, int B,
+                                          int Hq, int Hkv, int L, int S, int D, float scale, int window, int first,
+                                          const float *key_mask, tfa_stream_t stream) {
+    const bool decode = L >= 1 && L <= TFA_MAX_DECODE_ROWS;
+    int rc = validate(q, k, v, dout, B, Hq, Hkv, L, S, D, scale, 1, window, key_mask, true, decode);
+    if (rc) return rc;
+    if (!o || !lse || !dq || !dk || !dv) return TFA_ERR_NULL;
+    if (window <= 0 || first < 0) return TFA_ERR_WINDOW;
+    auto mis16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; };
+    if (mis16(o) || mis16(dq) || mis16(dk) || mis16(dv) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return TFA_ERR_ALIGN;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    DeviceState *st = nullptr;
+    BwdScratch *bs = nullptr;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    if ((rc = device_state(s, &st)) || (rc = bwd_scratch(*st, s, static_cast<size_t>(B) * Hq * L, D, &bs)))
+        return rc;
+    const int f = first < S ? first : S;
+    return (D == 128) ? backward_impl<128>(*st, nullptr, *bs, q, k, v, dout, dq, dk, dv, B, Hq, Hkv, L, S, scale, 1,
+                                           window, key_mask, s, o, lse, f)
+                      : backward_impl<64>(*st, nullptr, *bs, q, k, v, dout, dq, dk, dv, B, Hq, Hkv, L, S, scale, 1,
+                                          window, key_mask, s, o, lse, f);
 }
 
 extern "C" int tfa_prefill_debug(const void *q, const void *k, const void *v, void *o, int B,

@@ -72,6 +72,7 @@ struct BwdParams {
     const float *key_mask;        // [B,S] or nullptr
     unsigned *status;
     int B, Hq, Hkv, L, S, G, causal, window;
+    int first;  // first tokens that stay visible (kernels instantiated with FIRST)
     float scale, scale_log2;
     int n_items;
 };
@@ -141,8 +142,11 @@ struct ItemIter {
     }
 };
 struct QItem {
-    int b, h, qt, lo, hi;  // key tiles [lo, hi]
+    int b, h, qt, lo, hi;  // key tiles [lo, hi]; with FIRST numbered as visited (key_tile)
+    int fs, gap;
+    __device__ __forceinline__ int key_tile(int j) const { return j < fs ? j : j + gap; }
 };
+template <bool FIRST>
 __device__ __forceinline__ QItem q_item(const BwdParams &p, int item) {
     const int nqt = (p.L + kBlockQ - 1) / kBlockQ;
     const int bh = p.B * p.Hq;
@@ -154,11 +158,20 @@ __device__ __forceinline__ QItem q_item(const BwdParams &p, int item) {
     const KeyRange kr = qtile_key_range(p.L, p.S, p.causal, p.window, it.qt * kBlockQ, 0u);
     it.lo = kr.lo;
     it.hi = kr.hi;
+    it.fs = it.gap = 0;
+    if (FIRST) {
+        const FirstRange fr = first_range(p.first, kr.lo);
+        it.fs = fr.fs;
+        it.gap = fr.gap;
+        it.lo = 0;
+        it.hi -= fr.gap;
+    }
     return it;
 }
 struct KItem {
     int b, g, kt, qlo, qhi, nq, steps;  // per head of the group: query tiles [qlo, qhi]
 };
+template <bool FIRST>
 __device__ __forceinline__ KItem k_item(const BwdParams &p, int item) {
     const int bg = p.B * p.Hkv;
     const int kt = item / bg, rem = item - kt * bg;
@@ -166,7 +179,9 @@ __device__ __forceinline__ KItem k_item(const BwdParams &p, int item) {
     it.kt = kt;
     it.b = rem / p.Hkv;
     it.g = rem - it.b * p.Hkv;
-    const KeyRange qr = ktile_query_range(p.L, p.S, p.causal, p.window, kt);
+    // every later row sees a key among the first tokens
+    const int window = FIRST && kt * kBlockK < p.first ? 0 : p.window;
+    const KeyRange qr = ktile_query_range(p.L, p.S, p.causal, window, kt);
     it.qlo = qr.lo;
     it.qhi = qr.hi;
     it.nq = qr.hi >= qr.lo ? qr.hi - qr.lo + 1 : 0;
@@ -292,7 +307,7 @@ struct KvRing {  // dQ kernel: q_slot holds K_t, do_slot V_t
 };
 
 // ------------------------------------------------------------------ dQ kernel
-template <int D, bool KM>
+template <int D, bool KM, bool FIRST = false>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -315,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int s = 0; s < C::kSlots; ++s) used[s] = 0;
             for (ItemIter ii; ii.item < p.n_items; ii.next()) {
-                const QItem it = q_item(p, ii.item);
+                const QItem it = q_item<FIRST>(p, ii.item);
                 if (fix_use > 0 && !mbar_wait(bar.fix_empty(), (fix_use - 1) & 1, st.abort_flag, p.status))
                     break;
                 mbar_arrive_expect_tx(bar.fix_full(), 2 * C::kTileBytes);
@@ -334,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         mbar_arrive_expect_tx(bar.ring_full(s), C::kTileBytes);
                         load_tile<D>(st.sbase + C::kRingOff + s * C::kTileBytes, which ? &tm_v : &tm_k,
-                                     bar.ring_full(s), j * kBlockK, it.b * p.Hkv + it.h / p.G);
+                                     bar.ring_full(s), (FIRST ? it.key_tile(j) : j) * kBlockK, it.b * p.Hkv + it.h / p.G);
                         ++used[s];
                     }
                 }
@@ -356,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             using R = KvRing<D>;
             uint32_t tb = 0, fix_use = 0, op_cnt = 0, acc_use = 0;
             for (ItemIter ii; ii.item < p.n_items; ii.next()) {
-                const QItem it = q_item(p, ii.item);
+                const QItem it = q_item<FIRST>(p, ii.item);
                 if (!mbar_wait(bar.fix_full(), fix_use & 1, st.abort_flag, p.status)) goto mma_out;
                 ++fix_use;
                 // S_j alternates between two buffers and runs two key tiles
@@ -446,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t mm_cnt = 0, acc_cnt = 0;  // mm_cnt: dP tiles seen
         uint32_t s_even = 0, s_odd = 0;    // S tiles seen per buffer
         for (ItemIter ii; ii.item < p.n_items; ii.next()) {
-            const QItem it = q_item(p, ii.item);
+            const QItem it = q_item<FIRST>(p, ii.item);
             const int q0 = it.qt * kBlockQ;
             const int row = q0 + r;
             const bool valid = row < p.L;
@@ -465,7 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     goto ew_out;
                 tc_fence_after();
                 const uint32_t tS = odd ? tA2 : tA;
-                const bool needs = key_tile_needs_mask(p.L, p.S, p.causal, p.window, KM ? 1 : 0, q0, j, 0u);
+                const int kt = FIRST ? it.key_tile(j) : j;
+                const bool needs = key_tile_needs_mask(p.L, p.S, p.causal, p.window, KM ? 1 : 0, q0, kt, 0u);
                 float pr[64];
 #pragma unroll
                 for (int c2 = 0; c2 < 2; ++c2) {
@@ -476,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 32; ++e) {
                         float pe = ex2(fmaf(__uint_as_float(sv[e]), c, -lse_r));
                         if (needs) {
-                            const int k = j * kBlockK + 32 * ch + e;
-                            const bool al = k >= lo_abs && k <= hi_abs && (!KM || __ldg(km_row + k) > 0.5f);
+                            const int k = kt * kBlockK + 32 * ch + e;
+                            const bool al = (k >= lo_abs || (FIRST && k < p.first)) && k <= hi_abs && (!KM || __ldg(km_row + k) > 0.5f);
                             pe = al ? pe : 0.f;
                         }
                         pr[32 * c2 + e] = pe;
@@ -536,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ----------------------------------------------------------------- dKV kernel
-template <int D, bool KM>
+template <int D, bool KM, bool FIRST = false>
 __global__ void __launch_bounds__(kThreads, 1)
     dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -557,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < C::kSlots; ++s) used[s] = 0;
             bool stop = false;
             for (ItemIter ii; ii.item < p.n_items && !stop; ii.next()) {
-                const KItem it = k_item(p, ii.item);
+                const KItem it = k_item<FIRST>(p, ii.item);
                 if (it.steps == 0) continue;
                 if (fix_use > 0 && !mbar_wait(bar.fix_empty(), (fix_use - 1) & 1, st.abort_flag, p.status))
                     break;
@@ -600,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             using R = KvRing<D>;
             uint32_t n = 0, fix_use = 0, sf_cnt = 0, op_cnt = 0, acc_use = 0;
             for (ItemIter ii; ii.item < p.n_items; ii.next()) {
-                const KItem it = k_item(p, ii.item);
+                const KItem it = k_item<FIRST>(p, ii.item);
                 if (it.steps == 0) continue;
                 if (!mbar_wait(bar.fix_full(), fix_use & 1, st.abort_flag, p.status)) goto mma_out;
                 ++fix_use;
@@ -693,13 +709,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *stage = reinterpret_cast<float *>(st.gbase + C::kStageOff) + warp * 256;
         uint32_t mm_cnt = 0, acc_cnt = 0;
         for (ItemIter ii; ii.item < p.n_items; ii.next()) {
-            const KItem it = k_item(p, ii.item);
+            const KItem it = k_item<FIRST>(p, ii.item);
             const int key = it.kt * kBlockK + r;
             const bool kvalid = key < p.S;
             const bool kept = kvalid && (!KM || __ldg(p.key_mask + static_cast<size_t>(it.b) * p.S + key) > 0.5f);
             // the query rows that see this key: [q_lo, q_hi] (empty when not kept)
             int q_lo = p.causal ? imax(0, key - P) : 0;
             int q_hi = (p.causal && p.window > 0) ? imin(p.L - 1, key - P + p.window - 1) : p.L - 1;
+            if (FIRST && key < p.first) q_hi = p.L - 1;
             if (!kept) q_hi = q_lo - 1;
             const size_t oidx = (static_cast<size_t>(it.b * p.Hkv + it.g) * p.S + key) * D;
             if (it.steps == 0) {  // no row sees this key tile: zero gradients

@@ -205,13 +205,16 @@ __device__ __forceinline__ uint8_t *smem_base() {
 
 // Where K and V rows live, fixed at compile time so that a dense call carries
 // no code for the others: [B*H][rows][D] planes, a rotating cache of ring_rows
-// rows per plane, or packed variable-length sequences [total][H][D].
-enum Layout : int { kLayoutDense = 0, kLayoutRing = 1, kLayoutVarlen = 2 };
+// rows per plane, or packed variable-length sequences [total][H][D].  First:
+// the dense layout with first tokens that stay visible outside the window.
+enum Layout : int { kLayoutDense = 0, kLayoutRing = 1, kLayoutVarlen = 2, kLayoutFirst = 3 };
+template <int LY>
+using SegIterOf = SegIterT<LY == kLayoutFirst>;
 
 // Start the CTA's piece iterator (with the validated sequence table for a
 // packed variable-length call).
 template <int D, int LY>
-__device__ __forceinline__ void iter_init(SegIter &it, const Params &p) {
+__device__ __forceinline__ void iter_init(SegIterOf<LY> &it, const Params &p) {
     it.init(p.shape, p.W, blockIdx.x);
     if constexpr (LY == kLayoutVarlen) {
         const int *tab = reinterpret_cast<const int *>(smem_base() + Cfg<D>::kTableOff);
@@ -234,10 +237,11 @@ struct ItemPlan {
     bool present[2];
     int lo[2], hi[2];
     int jl, jh;
+    int fs, gap;  // first layout: ItemSpan's
 };
 
 // The two query tiles of one piece of work, clipped to the piece's key tiles.
-template <bool PK>
+template <bool PK, int LY>
 __device__ __forceinline__ ItemPlan plan_piece(const Params &p, const Segment &seg) {
     ItemPlan ip;
     ip.b = seg.b;
@@ -250,7 +254,9 @@ __device__ __forceinline__ ItemPlan plan_piece(const Params &p, const Segment &s
     ip.jh = seg.je;
     ip.q_row0 = seg.q_base;
     ip.k_row0 = seg.k_base;
-    const ItemSpan sp = seg_span(p.shape, seg);
+    const ItemSpan sp = seg_span<LY == kLayoutFirst>(p.shape, seg);
+    ip.fs = sp.fs;
+    ip.gap = sp.gap;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const TileRole tr = tile_role(p.shape, seg, sp, t);
@@ -298,7 +304,7 @@ __device__ void load_role(const Params &p, const CUtensorMap *tm_q, const CUtens
     constexpr unsigned lanes = KM ? 0xffffffffu : 1u;
     uint32_t kv_prod = 0;
     uint32_t q_use[2] = {0, 0};
-    SegIter it;
+    SegIterOf<LY> it;
     iter_init<D, LY>(it, p);
     // K/V tiles are read again by the other CTAs of their KV group (and the
     // other query tiles); Q tiles are read once.  Marking them evict-last /
@@ -306,7 +312,7 @@ __device__ void load_role(const Params &p, const CUtensorMap *tm_q, const CUtens
     const uint64_t pol_kv = make_policy_evict_last(), pol_q = make_policy_evict_first();
     Segment seg;
     while (it.next(p.shape, seg)) {
-        const ItemPlan ip = plan_piece<PK>(p, seg);
+        const ItemPlan ip = plan_piece<PK, LY>(p, seg);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             if (!ip.present[t]) continue;
@@ -331,7 +337,8 @@ __device__ void load_role(const Params &p, const CUtensorMap *tm_q, const CUtens
             }
             ++q_use[t];
         }
-        for (int j = ip.jl; j <= ip.jh; ++j) {
+        for (int jj = ip.jl; jj <= ip.jh; ++jj) {
+            const int j = LY == kLayoutFirst && jj >= ip.fs ? jj + ip.gap : jj;
             for (int which = 0; which < 2; ++which) {  // K_j then V_j
                 const uint32_t s = kv_prod % C::kSlots;
                 const uint32_t round = kv_prod / C::kSlots;
@@ -443,7 +450,7 @@ __device__ void mma_role(const Params &p, uint32_t sbase, uint32_t tmem, const B
     uint32_t p_cnt[2] = {0, 0};
     int trace_step = 0;
     (void)trace_step;
-    SegIter it;
+    SegIterOf<LY> it;
     iter_init<D, LY>(it, p);
     Segment seg;
     if constexpr (PK) {
@@ -471,7 +478,7 @@ __device__ void mma_role(const Params &p, uint32_t sbase, uint32_t tmem, const B
                         (accumulate || kk > 0) ? 1u : 0u);
         };
         while (it.next(p.shape, seg)) {
-            const ItemPlan ip = plan_piece<PK>(p, seg);
+            const ItemPlan ip = plan_piece<PK, LY>(p, seg);
             if (ip.jl > ip.jh) continue;  // no key tile: nothing was loaded
             if (!mbar_wait(bar.q_full(0), q_use[0] & 1, abort_flag, p.status, p.wait_limit)) goto out;
             ++q_use[0];
@@ -518,7 +525,7 @@ __device__ void mma_role(const Params &p, uint32_t sbase, uint32_t tmem, const B
         }
     } else {
         while (it.next(p.shape, seg)) {
-            const ItemPlan ip = plan_piece<PK>(p, seg);
+            const ItemPlan ip = plan_piece<PK, LY>(p, seg);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (!ip.present[t]) continue;
@@ -738,11 +745,11 @@ __device__ __forceinline__ void softmax_role(const Params &p, const int t, uint3
     int trace_step = 0;
     (void)trace_step;
 
-    SegIter it;
+    SegIterOf<LY> it;
     iter_init<D, LY>(it, p);
     Segment seg;
     while (it.next(p.shape, seg)) {
-        const ItemSpan sp = seg_span(p.shape, seg);
+        const ItemSpan sp = seg_span<LY == kLayoutFirst>(p.shape, seg);
         const TileRole ip = tile_role(p.shape, seg, sp, t);
         if (!ip.active) continue;
         // query row of this thread (its head too, for a packed tile)
@@ -803,15 +810,18 @@ __device__ __forceinline__ void softmax_role(const Params &p, const int t, uint3
             }
             if (t == 0 && lane == 0) TFA_TR(4 + (r >> 5), trace_step, 0);
 
-            if (key_tile_needs_mask(seg.L, seg.S, p.causal, p.window, 0, q_tile0, j, p.flags)) {
-                const int k0 = j * kBlockK;
+            const int kt = LY == kLayoutFirst ? sp.key_tile(j) : j;
+            if (key_tile_needs_mask(seg.L, seg.S, p.causal, p.window, 0, q_tile0, kt, p.flags)) {
+                const int k0 = kt * kBlockK;
                 const int lo_c = lo_abs - k0;
                 const int hi_c = hi_abs - k0;
+                const int first_c = p.shape.first - k0;  // first layout: columns below it stay
 #pragma unroll
                 for (int cidx = 0; cidx < 128; ++cidx) {
                     // causal / window / key-tail predicate; the key mask arrived
                     // through the bias MMA already
-                    const bool keep = cidx >= lo_c && cidx <= hi_c;
+                    bool keep = cidx >= lo_c && cidx <= hi_c;
+                    if (LY == kLayoutFirst) keep = (cidx >= lo_c || cidx < first_c) && cidx <= hi_c;
                     if (!keep) s[cidx] = 0xff800000u;  // -inf
                 }
             }

@@ -61,6 +61,20 @@ TFA_HD bool key_tile_needs_mask(int L, int S, int causal, int window, int has_ke
     return false;
 }
 
+// With `first` tokens that stay visible outside the window, a range of key tiles
+// that begins at tile lo is preceded by the first tokens' tiles, without those
+// that it holds anyway: fs of them, then a gap of tiles that no row sees.
+struct FirstRange {
+    int fs, gap;
+};
+TFA_HD FirstRange first_range(int first, int lo) {
+    const int keep = (first + kBlockK - 1) / kBlockK;
+    FirstRange r;
+    r.fs = lo > keep ? keep : 0;
+    r.gap = lo > keep ? lo - keep : 0;
+    return r;
+}
+
 // The query tiles that hold a row seeing some key of 128-key tile kt (the
 // transpose of qtile_key_range, for the backward pass that walks key tiles):
 // a row i sees key j iff (causal => j <= P + i) and (window => j > P + i - W).

@@ -56,6 +56,9 @@ struct Shape {
     // the same key tiles; otherwise they are two consecutive query tiles of
     // one head, whose key ranges differ at the causal diagonal and the window.
     int hp = 0;
+    // First tokens that stay visible outside the window (window > 0 only; read
+    // by the functions instantiated with FIRST).
+    int first = 0;
 };
 
 TFA_HD int shape_n_qp(int L, int hp = 0) {
@@ -63,13 +66,20 @@ TFA_HD int shape_n_qp(int L, int hp = 0) {
 }
 
 // Key-tile ranges of the two query tiles of item group qp (a query-tile pair,
-// or with head pairs one query tile of both heads).
+// or with head pairs one query tile of both heads).  With FIRST the item's key
+// tiles are numbered as it visits them: the first `fs` are the tiles of the
+// first tokens, the others lie `gap` further on (key_tile); both query tiles
+// then start at number 0, so the later one of a pair may visit one tile that
+// its window has left (its mask hides it).
 struct ItemSpan {
     int jl, jh;     // union range
     int lo[2], hi[2];
     bool present[2];
+    int fs = 0, gap = 0;
+    TFA_HD int key_tile(int j) const { return j < fs ? j : j + gap; }
 };
 
+template <bool FIRST = false>
 TFA_HD ItemSpan item_span_ls(const Shape &s, int L, int S, int qp) {
     ItemSpan sp;
     sp.jl = 0x7fffffff;
@@ -85,22 +95,36 @@ TFA_HD ItemSpan item_span_ls(const Shape &s, int L, int S, int qp) {
             sp.jh = imax(sp.jh, kr.hi);
         }
     }
+    if (FIRST) {
+        const FirstRange fr = first_range(s.first, sp.jl);
+        sp.fs = fr.fs;
+        sp.gap = fr.gap;
+        sp.jl = 0;
+        sp.jh -= fr.gap;
+        for (int t = 0; t < 2; ++t) {
+            sp.lo[t] = 0;
+            if (sp.present[t]) sp.hi[t] -= fr.gap;
+        }
+    }
     return sp;
 }
 
-TFA_HD ItemSpan item_span(const Shape &s, int qp) { return item_span_ls(s, s.L, s.S, qp); }
+template <bool FIRST = false>
+TFA_HD ItemSpan item_span(const Shape &s, int qp) { return item_span_ls<FIRST>(s, s.L, s.S, qp); }
 
 // Items of group r all have query-tile pair (or query tile) group_qp(r).
 TFA_HD int group_qp(const Shape &s, int r) { return s.causal ? s.n_qp - 1 - r : r; }
 
+template <bool FIRST = false>
 TFA_HD int item_steps(const Shape &s, int qp) {
-    const ItemSpan sp = item_span(s, qp);
+    const ItemSpan sp = item_span<FIRST>(s, qp);
     return sp.jh - sp.jl + 1;
 }
 
+template <bool FIRST = false>
 TFA_HD long long total_steps(const Shape &s) {
     long long w = 0;
-    for (int r = 0; r < s.n_qp; ++r) w += static_cast<long long>(item_steps(s, group_qp(s, r)));
+    for (int r = 0; r < s.n_qp; ++r) w += static_cast<long long>(item_steps<FIRST>(s, group_qp(s, r)));
     return w * s.B * s.Hq;
 }
 
@@ -117,10 +141,12 @@ struct Segment {
 };
 
 // Key-tile ranges of the segment's two tiles, for its own lengths.
-TFA_HD ItemSpan seg_span(const Shape &s, const Segment &seg) { return item_span_ls(s, seg.L, seg.S, seg.qp); }
+template <bool FIRST = false>
+TFA_HD ItemSpan seg_span(const Shape &s, const Segment &seg) { return item_span_ls<FIRST>(s, seg.L, seg.S, seg.qp); }
 
 // Per-CTA iterator over its pieces, identical on every role of the CTA.
-struct SegIter {
+template <bool FIRST = false>
+struct SegIterT {
     long long pos, end;   // split: current / end global step
     long long gstart;     // split: first global step of group r
     int r, gsteps, bh;    // split: current group, steps per item in it, items per group
@@ -144,12 +170,12 @@ struct SegIter {
         end = cta_begin(W, s.grid, c + 1);
         r = 0;
         gstart = 0;
-        gsteps = item_steps(s, group_qp(s, 0));
+        gsteps = item_steps<FIRST>(s, group_qp(s, 0));
         if (s.split) {
             while (r + 1 < s.n_qp && pos >= gstart + static_cast<long long>(bh) * gsteps) {
                 gstart += static_cast<long long>(bh) * gsteps;
                 ++r;
-                gsteps = item_steps(s, group_qp(s, r));
+                gsteps = item_steps<FIRST>(s, group_qp(s, r));
             }
         }
     }
@@ -189,7 +215,7 @@ struct SegIter {
                     seg.k_base = seq.k_start[seg.b];
                     if (seg.qp * (s.hp ? 1 : 2) * kBlockQ >= seg.L) continue;  // no such tile (pair)
                 }
-                const ItemSpan sp = seg_span(s, seg);
+                const ItemSpan sp = seg_span<FIRST>(s, seg);
                 seg.jb = sp.jl;
                 seg.je = sp.jh;
                 seg.x0 = 0;
@@ -200,7 +226,7 @@ struct SegIter {
         while (pos >= gstart + static_cast<long long>(bh) * gsteps) {
             gstart += static_cast<long long>(bh) * gsteps;
             ++r;
-            gsteps = item_steps(s, group_qp(s, r));
+            gsteps = item_steps<FIRST>(s, group_qp(s, r));
         }
         const long long in_group = (pos - gstart) / gsteps;
         const long long x0 = gstart + in_group * gsteps;
@@ -214,7 +240,7 @@ struct SegIter {
         seg.S = s.S;
         seg.q_base = 0;
         seg.k_base = 0;
-        const ItemSpan sp = item_span(s, seg.qp);
+        const ItemSpan sp = item_span<FIRST>(s, seg.qp);
         seg.jb = sp.jl + static_cast<int>(pos - x0);
         seg.je = sp.jl + static_cast<int>(stop - x0) - 1;
         seg.x0 = x0;
@@ -222,6 +248,8 @@ struct SegIter {
         return true;
     }
 };
+
+using SegIter = SegIterT<false>;
 
 // What a piece does for query tile t.
 struct TileRole {
@@ -258,10 +286,11 @@ TFA_HD int last_contributor(long long W, int grid, int c, const Segment &seg,
 // pieces; the whole-item schedule has one piece per item but deals whole items.
 constexpr int kPieceCostSteps = 6;
 
+template <bool FIRST = false>
 inline long long makespan_estimate(Shape s, long long W) {
     long long worst = 0;
     for (int c = 0; c < s.grid; ++c) {
-        SegIter it;
+        SegIterT<FIRST> it;
         it.init(s, W, c);
         Segment seg;
         long long cost = 0;

@@ -141,3 +141,46 @@ def _decode(**over):
 ])
 def test_kv4_decode_refusals(over, code):
     assert _decode(**over) == code
+
+
+# ------------------------------------------- a window with visible first tokens
+def _first(back=False, **over):
+    a = dict(q=A16, k=A16, v=A16, o=A16, lse=None, B=1, Hq=8, Hkv=2, L=33, S=47, D=128, scale=0.1, window=16, first=4,
+             key_mask=None, softcap=0.0, sinks=None, do=A16, dk=A16)
+    if back:
+        a["lse"] = A16
+    a.update(over)
+    sizes = (a["B"], a["Hq"], a["Hkv"], a["L"], a["S"], a["D"], a["scale"], a["window"], a["first"], a["key_mask"])
+    if back:
+        return tb.lib().tfa_prefill_first_backward(a["q"], a["k"], a["v"], a["o"], a["lse"], a["do"], A16, a["dk"], A16,
+                                                   *sizes, None)
+    return tb.lib().tfa_prefill_first(a["q"], a["k"], a["v"], a["o"], a["lse"], *sizes, a["softcap"], a["sinks"], None)
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("over,code", [
+    (dict(q=None), tb.TFA_ERR_NULL),
+    (dict(Hq=7), tb.TFA_ERR_HEADS),
+    (dict(S=32), tb.TFA_ERR_SHAPE),
+    (dict(D=96), tb.TFA_ERR_HEAD_DIM),
+    (dict(window=0), tb.TFA_ERR_WINDOW),
+    (dict(window=-5), tb.TFA_ERR_WINDOW),
+    (dict(first=-1), tb.TFA_ERR_WINDOW),
+    (dict(v=MIS), tb.TFA_ERR_ALIGN),
+    (dict(lse=ctypes.c_void_p(0x10002)), tb.TFA_ERR_ALIGN),
+    (dict(key_mask=ctypes.c_void_p(0x10002)), tb.TFA_ERR_ALIGN),
+    (dict(scale=float("inf")), tb.TFA_ERR_SCALE),
+])
+def test_first_refusals(back, over, code):
+    assert _first(back, **over) == code
+
+
+def test_first_refusals_of_one_direction():
+    assert _first(softcap=-1.0) == tb.TFA_ERR_SOFTCAP
+    assert _first(softcap=3.0, lse=A16) == tb.TFA_ERR_SOFTCAP
+    assert _first(sinks=A16, lse=A16) == tb.TFA_ERR_SOFTCAP
+    assert _first(sinks=ctypes.c_void_p(0x10002)) == tb.TFA_ERR_ALIGN
+    assert _first(True, lse=None) == tb.TFA_ERR_NULL
+    assert _first(True, o=None) == tb.TFA_ERR_NULL
+    assert _first(True, dk=None) == tb.TFA_ERR_NULL
+    assert _first(True, dk=MIS) == tb.TFA_ERR_ALIGN
