@@ -125,6 +125,10 @@ def lib():
             L.tfa_kv4_read.restype = i32
             L.tfa_kv4_decode.argtypes = [P] * 7 + [i32] * 6 + [f32, i32, i32, f32, P, P, P]
             L.tfa_kv4_decode.restype = i32
+            L.tfa_kv4_prefill.argtypes = [P] * 6 + [i32] * 7 + [f32, i32, i32, f32, P, P, P]
+            L.tfa_kv4_prefill.restype = i32
+            L.tfa_kv4_prefill_workspace.argtypes = [i32] * 7
+            L.tfa_kv4_prefill_workspace.restype = ctypes.c_size_t
             L.tfa_kv4_decode_workspace.argtypes = [i32] * 4
             L.tfa_kv4_decode_workspace.restype = ctypes.c_size_t
             L.tfa_qk_norm_rope_workspace.argtypes = [i32]
@@ -803,6 +807,33 @@ def kv4_read(k_codes, k_meta, v_codes, v_meta, *, start=0, rows=None, out=None, 
     return out
 
 
+def _kv4_query(q, B, D, dev, sinks, out):
+    import torch
+
+    _check_on(q, "q", torch.bfloat16, 4, dev)
+    if q.shape[0] != B or q.shape[3] != D:
+        raise ValueError("q and the cache disagree")
+    if sinks is not None:
+        _check_on(sinks, "sinks", torch.float32, 1, dev)
+        if sinks.shape[0] != q.shape[1]:
+            raise ValueError("sinks must hold one logit per query head")
+    if out is not None:
+        _check_on(out, "out", torch.bfloat16, 4, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+
+
+def _kv4_workspace(workspace, need, dev):
+    import torch
+
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    _check_on(workspace, "workspace", torch.uint8, 1, dev)
+    if workspace.shape[0] < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    return workspace
+
+
 def kv4_decode(q, k_codes, k_meta, v_codes, v_meta, lens, *, scale=None, window=0, first=0, softcap=0.0, sinks=None,
                out=None, workspace=None, stream=None):
     """Decoding attention [B,Hq,L,D] (1 <= L <= 8) over the 4-bit cache: lens, int32 [B]
@@ -812,29 +843,15 @@ def kv4_decode(q, k_codes, k_meta, v_codes, v_meta, lens, *, scale=None, window=
     import torch
 
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
-    _check_on(q, "q", torch.bfloat16, 4, dev)
+    _kv4_query(q, B, D, dev, sinks, out)
     _check_on(lens, "lens", torch.int32, 1, dev)
+    if lens.shape[0] != B:
+        raise ValueError("lens must hold one length per sequence")
     Hq, L = q.shape[1], q.shape[2]
-    if q.shape[0] != B or q.shape[3] != D or lens.shape[0] != B:
-        raise ValueError("q, lens and the cache disagree")
-    if sinks is not None:
-        _check_on(sinks, "sinks", torch.float32, 1, dev)
-        if sinks.shape[0] != Hq:
-            raise ValueError("sinks must hold one logit per query head")
     with _scope(dev, stream):
         if out is None:
             out = torch.empty_like(q)
-        else:
-            _check_on(out, "out", torch.bfloat16, 4, dev)
-            if out.shape != q.shape:
-                raise ValueError("out must have q's shape")
-        need = lib().tfa_kv4_decode_workspace(Hq, Hkv, L, D)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        else:
-            _check_on(workspace, "workspace", torch.uint8, 1, dev)
-            if workspace.shape[0] < need:
-                raise ValueError(f"workspace must hold {need} bytes")
+        workspace = _kv4_workspace(workspace, lib().tfa_kv4_decode_workspace(Hq, Hkv, L, D), dev)
         rc = lib().tfa_kv4_decode(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
                                   v_meta.data_ptr(), lens.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, cap, D,
                                   D ** -0.5 if scale is None else scale, window, first, softcap,
@@ -842,4 +859,30 @@ def kv4_decode(q, k_codes, k_meta, v_codes, v_meta, lens, *, scale=None, window=
                                   torch.cuda.current_stream().cuda_stream)
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_kv4_decode")
+    return out
+
+
+def kv4_prefill(q, k_codes, k_meta, v_codes, v_meta, *, S, scale=None, window=0, first=0, softcap=0.0, sinks=None,
+                out=None, workspace=None, stream=None):
+    """Causal attention [B,Hq,L,D] of chunks of any L >= 1 rows over the first S rows of
+    the 4-bit cache (the chunk's own rows last among them); window and first as for
+    kv4_decode.  workspace: uint8 of tfa_kv4_prefill_workspace bytes, by default
+    allocated here."""
+    import torch
+
+    B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
+    _kv4_query(q, B, D, dev, sinks, out)
+    Hq, L = q.shape[1], q.shape[2]
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        need = lib().tfa_kv4_prefill_workspace(B, Hkv, L, S, D, window, first)
+        workspace = _kv4_workspace(workspace, max(need, 16), dev)
+        rc = lib().tfa_kv4_prefill(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
+                                   v_meta.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, S, cap, D,
+                                   D ** -0.5 if scale is None else scale, window, first, softcap,
+                                   sinks.data_ptr() if sinks is not None else None, workspace.data_ptr(),
+                                   torch.cuda.current_stream().cuda_stream)
+    if rc != TFA_OK:
+        raise TfaError(rc, "tfa_kv4_prefill")
     return out

@@ -106,6 +106,7 @@ struct ReadParams {
     const int *start;
     int start0;
     int B, Hkv, rows, cap;
+    int split, skip;  // rows from `split` on lie `skip` cached positions further
     unsigned *status;
 };
 
@@ -129,7 +130,8 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
     const long long bh = row / p.rows;
     const int b = static_cast<int>(bh / p.Hkv);
     const long long first = p.start ? __ldg(p.start + b) : p.start0;
-    const long long at = first + (row - bh * p.rows);
+    const long long i = row - bh * p.rows;
+    const long long at = first + i + (i >= p.split ? p.skip : 0);
     uint4 out = make_uint4(0u, 0u, 0u, 0u);
     if (first >= 0 && at < p.cap) {
         const size_t src = static_cast<size_t>(bh) * p.cap + at;
@@ -157,6 +159,27 @@ int check_cache(const void *kc, const void *km, const void *vc, const void *vm, 
 unsigned row_blocks(long long rows, int D) {
     const long long n = (rows * (D / 8) + 255) / 256;
     return n <= 0x7fffffffll ? static_cast<unsigned>(n) : 0u;
+}
+
+int launch_read(const ReadParams &p, unsigned blocks, int D, cudaStream_t s) {
+    (D == 128 ? read_kernel<128> : read_kernel<64>)<<<dim3(blocks, 2), 256, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TFA_OK : report_cuda("kv4 read launch", e);
+}
+
+// The cached positions that some of the last L rows sees: [0, keep) and [lo, S).
+struct Seen {
+    int keep, lo, rest;  // rest = S - lo
+    long long rows() const { return static_cast<long long>(keep) + rest; }
+};
+Seen seen(int L, int S, int window, int first) {
+    Seen r{0, 0, S};
+    if (window > 0) {
+        const long long lo = static_cast<long long>(S) - L - window + 1;
+        const int keep = first < S ? first : S;
+        if (lo > keep) r = Seen{keep, static_cast<int>(lo), S - static_cast<int>(lo)};
+    }
+    return r;
 }
 
 Cache cache_of(void *kc, void *km, void *vc, void *vm) {
@@ -253,9 +276,8 @@ extern "C" int tfa_kv4_read(const void *k_codes, const void *k_meta, const void 
     p.Hkv = Hkv;
     p.rows = rows;
     p.cap = capacity;
-    (D == 128 ? read_kernel<128> : read_kernel<64>)<<<dim3(blocks, 2), 256, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? TFA_OK : tfa::report_cuda("kv4 read launch", e);
+    p.split = rows;
+    return launch_read(p, blocks, D, s);
 }
 
 extern "C" size_t tfa_kv4_decode_workspace(int Hq, int Hkv, int L, int D) {
@@ -305,4 +327,54 @@ extern "C" int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_
     p.softcap = softcap;
     if (p.rows <= 8) return D == 128 ? launch_decode<128, 1>(p, sms, s) : launch_decode<64, 1>(p, sms, s);
     return D == 128 ? launch_decode<128, 2>(p, sms, s) : launch_decode<64, 2>(p, sms, s);
+}
+
+extern "C" size_t tfa_kv4_prefill_workspace(int B, int Hkv, int L, int S, int D, int window, int first) {
+    if (B < 1 || Hkv < 1 || L < 1 || S < L || D < 1 || first < 0) return 0;
+    return static_cast<size_t>(B) * Hkv * seen(L, S, window, first).rows() * D * 4;
+}
+
+// A chunk's products are the tensor core's to bound, so K and V are brought back
+// to bf16 once, next to which they would be read by every query tile, and the
+// dense kernel runs on them.  Only positions that some row sees are brought back;
+// leaving the others out shifts rows and window alike.
+extern "C" int tfa_kv4_prefill(const void *q, const void *k_codes, const void *k_meta, const void *v_codes,
+                               const void *v_meta, void *o, int B, int Hq, int Hkv, int L, int S, int capacity, int D,
+                               float scale, int window, int first, float softcap, const float *sinks, void *workspace,
+                               tfa_stream_t stream) {
+    if (!q || !o || !workspace) return TFA_ERR_NULL;
+    if (int rc = check_cache(k_codes, k_meta, v_codes, v_meta, B, Hkv, capacity, D)) return rc;
+    if (Hq < 1 || Hq % Hkv != 0) return TFA_ERR_HEADS;
+    if (L < 1 || S < L || static_cast<long long>(B) * Hq * L > (1ll << 31) - 1) return TFA_ERR_SHAPE;
+    if (S > capacity) return TFA_ERR_CACHE;
+    if (first < 0 || (first > 0 && window <= 0)) return TFA_ERR_WINDOW;
+    if (!std::isfinite(scale)) return TFA_ERR_SCALE;
+    if (!std::isfinite(softcap) || softcap < 0.f || (softcap > 0.f && scale == 0.f)) return TFA_ERR_SOFTCAP;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(sinks, 4) || !aligned(workspace, 16)) return TFA_ERR_ALIGN;
+    const Seen sn = seen(L, S, window, first);
+    const int rows = static_cast<int>(sn.rows());
+    const long long all = static_cast<long long>(B) * Hkv * rows;
+    const unsigned blocks = row_blocks(all, D);
+    if (all > (1ll << 31) - 1 || !blocks ||
+        static_cast<long long>(B) * Hq * ((L + 255) / 256) > (1ll << 30))  // the dense kernel's own limits
+        return TFA_ERR_SHAPE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    ReadParams p = {};
+    int sms = 0;
+    if (int rc = tfa::device_info(s, &p.status, &sms)) return rc;
+    p.c = cache_of(const_cast<void *>(k_codes), const_cast<void *>(k_meta), const_cast<void *>(v_codes),
+                   const_cast<void *>(v_meta));
+    p.k = static_cast<__nv_bfloat16 *>(workspace);
+    p.v = p.k + static_cast<size_t>(all) * D;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.rows = rows;
+    p.cap = capacity;
+    p.split = sn.lo > 0 ? sn.keep : rows;
+    p.skip = sn.lo - sn.keep;
+    if (int rc = launch_read(p, blocks, D, s)) return rc;
+    if (window > 0 && first > 0)
+        return tfa_prefill_first(q, p.k, p.v, o, nullptr, B, Hq, Hkv, L, rows, D, scale, window, first, nullptr, softcap,
+                                 sinks, stream);
+    return tfa_attention_ex(q, p.k, p.v, o, B, Hq, Hkv, L, rows, D, scale, 1, window, nullptr, softcap, sinks, stream);
 }

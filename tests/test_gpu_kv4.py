@@ -354,3 +354,93 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+PREFILL = [
+    # B, Hq, Hkv, L, S, D, cap, window, first
+    (1, 4, 2, 1, 1, 128, 1, 0, 0),
+    (2, 14, 2, 9, 300, 128, 333, 0, 0),
+    (1, 8, 8, 129, 129, 64, 140, 0, 0),
+    (2, 4, 2, 200, 1000, 128, 1000, 100, 0),
+    (2, 4, 2, 200, 1000, 128, 1001, 100, 4),
+    (1, 6, 2, 70, 900, 64, 1000, 65, 300),
+    (1, 4, 1, 300, 700, 128, 700, 128, 600),
+    (3, 4, 4, 5, 2000, 128, 2048, 1024, 64),
+    (1, 2, 1, 40, 500, 64, 500, 2 ** 31 - 1, 9),
+]
+
+
+@pytest.mark.parametrize("c", PREFILL, ids=["-".join(map(str, c)) for c in PREFILL])
+def test_prefill(c):
+    """K and V are rounded to bf16 once more (2^-8 of each value), and P and the
+    output once: the scores move by delta = scale 2^-8 sum_d |q_d k_jd|, at random
+    signs; the bound takes half of the largest delta of a row, |err| <= 2^-8 (2 sum w |v| + |o|)
+    + 2 delta' sum_j w_j |v_j - o|."""
+    B, Hq, Hkv, L, S, D, cap, window, first = c
+    gen = _gen(20)
+    cache = cache_of(_randn(gen, B, Hkv, S, D).bfloat16(), _randn(gen, B, Hkv, S, D).bfloat16(), cap)
+    q = _randn(gen, B, Hq, L, D).bfloat16()
+    got = tb.kv4_prefill(q, *cache, S=S, window=window, first=first)
+    tb.check_status()
+    ref, _ = reference(q, cache, [S] * B, D ** -0.5, window, first)
+    for b in range(B):
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            k, v = (sum(parts(cache[i][b, g, :S], cache[i + 1][b, g, :S])) for i in (0, 2))
+            x = q[b, h].double()
+            pos = S - L + torch.arange(L, device="cuda")[:, None]
+            j = torch.arange(S, device="cuda")
+            see = (j <= pos) & ((j > pos - window) | (j < first)) if window > 0 else j <= pos
+            w = torch.softmax((x @ k.T * D ** -0.5).masked_fill(~see, -math.inf), 1)
+            delta = D ** -0.5 * 2 ** -8 * (x.abs() @ k.abs().T).masked_fill(~see, 0).amax(1, keepdim=True)
+            spread = w @ v.abs() + ref[b, h].abs()
+            bound = 2 ** -8 * (2 * (w @ v.abs()) + ref[b, h].abs()) + delta * spread
+            assert ((got[b, h].double() - ref[b, h]).abs() <= bound).all()
+
+
+def test_prefill_is_the_dense_attention_of_the_values_read_back():
+    gen = _gen(21)
+    cache = cache_of(_randn(gen, 2, 2, 600, 128).bfloat16(), _randn(gen, 2, 2, 600, 128).bfloat16(), 640)
+    q = _randn(gen, 2, 8, 50, 128).bfloat16()
+    k, v = tb.kv4_read(*cache, rows=600)
+    sinks = _randn(gen, 8)
+    a = dict(softcap=20.0, sinks=sinks)
+    assert torch.equal(tb.kv4_prefill(q, *cache, S=600), tb.prefill(q, k, v))
+    assert torch.equal(tb.kv4_prefill(q, *cache, S=600, **a), tb.prefill(q, k, v, **a))
+    # without the positions that no row sees, the tiles fall elsewhere: two outputs' roundings apart
+    x = tb.kv4_prefill(q, *cache, S=600, window=70, first=5, **a).double()
+    y = tb.prefill(q, k, v, window=70, first=5, **a).double()
+    assert ((x - y).abs() <= 2 ** -7 * (y.abs() + v.abs().max().double())).all()
+
+
+def test_a_chunk_then_decoding():
+    """A prompt chunk written and attended to, then tokens one by one, against the
+    whole sequence at once."""
+    B, Hq, Hkv, D, cap, n = 2, 8, 2, 128, 100, 90
+    gen = _gen(22)
+    k, v = (_randn(gen, B, Hkv, n, D).bfloat16() for _ in range(2))
+    q = _randn(gen, B, Hq, n, D).bfloat16()
+    cache = tb.kv4_cache(B, Hkv, cap, D)
+    tb.kv4_append(k[:, :, :80], v[:, :, :80], *cache, start=0)
+    outs = [tb.kv4_prefill(q[:, :, :80].contiguous(), *cache, S=80, window=40, first=4)]
+    for i in range(80, n):
+        lens = torch.full((B,), i, dtype=torch.int32, device="cuda")
+        tb.kv4_append(k[:, :, i:i + 1], v[:, :, i:i + 1], *cache, start=lens)
+        outs.append(tb.kv4_decode(q[:, :, i:i + 1].contiguous(), *cache, lens + 1, window=40, first=4))
+    whole = tb.kv4_prefill(q, *cache, S=n, window=40, first=4)
+    ref, bound = reference(q, cache, [n] * B, D ** -0.5, 40, 4)
+    got = torch.cat(outs, 2)
+    assert ((got[:, :, 80:].double() - ref[:, :, 80:]).abs() <= bound[:, :, 80:]).all()
+    assert ((got.double() - whole.double()).abs() <= 2 ** -5 * (1 + whole.double().abs())).all()
+
+
+def test_prefill_workspace_is_used_within_its_size():
+    gen = _gen(23)
+    cache = cache_of(_randn(gen, 1, 2, 400, 64).bfloat16(), _randn(gen, 1, 2, 400, 64).bfloat16(), 400)
+    q = _randn(gen, 1, 4, 20, 64).bfloat16()
+    need = tb.lib().tfa_kv4_prefill_workspace(1, 2, 20, 400, 64, 30, 4)
+    ws = torch.full((need + 64,), 77, dtype=torch.uint8, device="cuda")
+    got = tb.kv4_prefill(q, *cache, S=400, window=30, first=4, workspace=ws)
+    assert torch.equal(got, tb.kv4_prefill(q, *cache, S=400, window=30, first=4)) and (ws[need:] == 77).all()
+    with pytest.raises(ValueError):
+        tb.kv4_prefill(q, *cache, S=400, workspace=ws)

@@ -184,3 +184,42 @@ def test_first_refusals_of_one_direction():
     assert _first(True, o=None) == tb.TFA_ERR_NULL
     assert _first(True, dk=None) == tb.TFA_ERR_NULL
     assert _first(True, dk=MIS) == tb.TFA_ERR_ALIGN
+
+
+def _chunk(**over):
+    a = dict(q=A16, kc=A16, km=A16, vc=A16, vm=A16, o=A16, B=2, Hq=8, Hkv=2, L=20, S=60, cap=64, D=128, scale=0.1,
+             window=0, first=0, softcap=0.0, sinks=None, ws=A16)
+    a.update(over)
+    return tb.lib().tfa_kv4_prefill(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(q=None), tb.TFA_ERR_NULL),
+    (dict(km=None), tb.TFA_ERR_NULL),
+    (dict(ws=None), tb.TFA_ERR_NULL),
+    (dict(Hq=7), tb.TFA_ERR_HEADS),
+    (dict(L=0), tb.TFA_ERR_SHAPE),
+    (dict(L=61), tb.TFA_ERR_SHAPE),
+    (dict(S=65), tb.TFA_ERR_CACHE),
+    (dict(D=96), tb.TFA_ERR_HEAD_DIM),
+    (dict(first=4), tb.TFA_ERR_WINDOW),
+    (dict(first=-1, window=3), tb.TFA_ERR_WINDOW),
+    (dict(scale=float("inf")), tb.TFA_ERR_SCALE),
+    (dict(softcap=float("nan")), tb.TFA_ERR_SOFTCAP),
+    (dict(q=MIS), tb.TFA_ERR_ALIGN),
+    (dict(ws=MIS), tb.TFA_ERR_ALIGN),
+    (dict(B=1 << 10, Hkv=1 << 10, Hq=1 << 10, L=1, S=1 << 20, cap=1 << 20), tb.TFA_ERR_SHAPE),
+])
+def test_kv4_prefill_refusals(over, code):
+    assert _chunk(**over) == code
+
+
+def test_kv4_workspaces():
+    size = tb.lib().tfa_kv4_prefill_workspace
+    assert size(2, 4, 10, 100, 128, 0, 0) == 2 * 4 * 100 * 128 * 4
+    assert size(2, 4, 10, 100, 64, 20, 5) == 2 * 4 * (5 + 29) * 64 * 4
+    assert size(1, 1, 10, 100, 64, 20, 71) == 100 * 64 * 4  # the first tokens meet the window
+    assert size(1, 1, 10, 9, 64, 20, 0) == 0
+    assert size(1, 1, 10, 100, 64, 2 ** 31 - 1, 2 ** 31 - 1) == 100 * 64 * 4
+    assert tb.lib().tfa_kv4_decode_workspace(8, 2, 1, 128) < tb.lib().tfa_kv4_decode_workspace(8, 2, 8, 128)
+    assert tb.lib().tfa_kv4_decode_workspace(8, 0, 1, 128) == 0
