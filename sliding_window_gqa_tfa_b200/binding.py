@@ -14,7 +14,10 @@ import ctypes
 import math
 import os
 import re
+import struct
 import threading
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libtfa.so")
@@ -110,7 +113,7 @@ def lib():
             L.tfa_plan_pieces.argtypes = [i32] * 9 + [P, i32, ctypes.POINTER(i32),
                                                       ctypes.POINTER(ctypes.c_longlong)]
             L.tfa_plan_pieces.restype = i32
-            LL, dims = ctypes.POINTER(ctypes.c_longlong), [i32] * 7
+            LL, dims = ctypes.c_char_p, [i32] * 7  # LL: host array of int64, packed
             L.tfa_qk_norm_rope.argtypes = [P] * 4 + [LL, P, P, P, P, i32, i32] + dims + [f32, f32, P]
             L.tfa_qk_norm_rope.restype = i32
             L.tfa_qk_norm_rope_backward.argtypes = [P] * 8 + [LL, P, P, P, P, i32, i32] + dims + [f32, f32, P, P]
@@ -538,25 +541,31 @@ def prefill_host(q, k, v, *, scale=None, causal=True, window=0, key_mask=None, o
 
 # ------------------------------------------- norms and rotary positions of q and k
 _NO_SCOPE = contextlib.nullcontext()
+_BF16, _F32, _F64, _I32, _U8 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.uint8
 
 
-def _scope(device, stream):
-    """Makes `device` current for a call, and `stream` where one is given, so that
-    what the call allocates belongs to the stream that uses it."""
-    import torch
-
+def _scope(index, stream):
+    """Makes device `index` current for a call, and `stream` where one is given, so
+    that what the call allocates belongs to the stream that uses it."""
     if stream is not None:
-        if stream.device != device:
+        if stream.device.index != index:
             raise ValueError("stream belongs to another device than the tensors")
         return torch.cuda.stream(stream)
-    return _NO_SCOPE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _NO_SCOPE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
-def _check_on(t, name, dtype, ndim, device=None, rows=False):
-    """Checks a CUDA tensor's type, dimensions and device; rows: any strides, as
-    long as the last dimension is contiguous (else all of it must be)."""
-    import torch
+# the current stream's handle without the Stream object around it (1.5 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+
+def _check_on(t, name, dtype, ndim, index=None, rows=False):
+    """Checks a CUDA tensor's type, dimensions and device (`index`, or any); rows: any
+    strides, as long as the last dimension is contiguous (else all of it must be)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim
+            and (t.get_device() == index if index is not None else t.is_cuda)
+            and (t.is_contiguous() or (rows and (t.stride(-1) == 1 or t.shape[-1] == 1)))):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -565,13 +574,9 @@ def _check_on(t, name, dtype, ndim, device=None, rows=False):
         raise ValueError(f"{name} must have {ndim} dimensions")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if rows:
-        if t.shape[-1] != 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name} must have a contiguous last dimension")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    raise ValueError(f"{name} must have a contiguous last dimension" if rows else f"{name} must be contiguous")
 
 
 def rope_inv_freq(rot, base=10000.0, *, scaling=None, factor=1.0, original=8192, device=None):
@@ -581,8 +586,6 @@ def rope_inv_freq(rot, base=10000.0, *, scaling=None, factor=1.0, original=8192,
     "yarn" (pairs that turn less than once in the `original` positions are divided
     by factor, those that turn more than 4, or 32, times are kept, between them a
     linear ramp over the turns; yarn's mscale is 0.1 ln(factor) + 1)."""
-    import torch
-
     if rot < 0 or rot % 2:
         raise ValueError("rot must be even and >= 0")
     if not (factor > 0 and original > 0 and base > 0):
@@ -604,26 +607,24 @@ def rope_inv_freq(rot, base=10000.0, *, scaling=None, factor=1.0, original=8192,
 
 def _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight):
     """Checks shared by the pass and its gradient; the C call's middle arguments."""
-    import torch
-
-    dev = q.device
-    _check_on(k, "k", torch.bfloat16, 4, dev, rows=True)
+    dev = q.get_device()
+    _check_on(k, "k", _BF16, 4, dev, rows=True)
     B, L, Hq, D = q.shape
     if k.shape[0] != B or k.shape[1] != L or k.shape[3] != D:
         raise ValueError("q and k disagree on batch, tokens or head dimension")
-    _check_on(inv_freq, "inv_freq", torch.float64, 1, dev)
+    _check_on(inv_freq, "inv_freq", _F64, 1, dev)
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight must be given together")
     if q_weight is not None:
         for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            _check_on(t, n, torch.bfloat16, 1, dev)
+            _check_on(t, n, _BF16, 1, dev)
             if t.shape[0] != D:
                 raise ValueError(f"{n} must hold one weight per channel")
     per_row, first, ptr = 0, 0, None
     if isinstance(positions, int):
         first = positions
     else:
-        _check_on(positions, "positions", torch.int32, positions.dim() if isinstance(positions, torch.Tensor) else 1, dev)
+        _check_on(positions, "positions", _I32, positions.dim() if isinstance(positions, torch.Tensor) else 1, dev)
         per_row = int(positions.dim() == 2)
         if tuple(positions.shape) != ((B, L) if per_row else (B,)):
             raise ValueError("positions must be an int, [B] or [B, L]")
@@ -633,13 +634,25 @@ def _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight):
             first), (B, L, Hq, k.shape[2], D, 2 * inv_freq.shape[0])
 
 
-def _strides(*tensors):
-    """(batch, token, head) element strides of (tensor, token axis) pairs."""
-    s = []
-    for t, axis in tensors:
-        a = t.stride()
-        s += (a[0], a[axis], a[3 - axis])
-    return (ctypes.c_longlong * len(s))(*s)
+_PACK6, _PACK12, _PACK18 = (struct.Struct(f"{n}q").pack for n in (6, 12, 18))
+
+
+def _tokens(t):
+    """(batch, token, head) element strides of a [B, L, H, D] tensor."""
+    a = t.stride()
+    return a[0], a[1], a[2]
+
+
+def _heads(t):
+    """(batch, token, head) element strides of a [B, H, L, D] tensor."""
+    a = t.stride()
+    return a[0], a[2], a[1]
+
+
+def _check_rows(t, name, shape, dev):
+    _check_on(t, name, _BF16, 4, dev, rows=True)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
 
 
 def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, mscale=1.0,
@@ -652,23 +665,23 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     an int.  inv_freq: fp64 [rot/2] on the device (rope_inv_freq), rot a multiple of
     16 up to D, the other channels pass through.  q_out and k_out may be views, e.g.
     a key cache's rows, in [B,H,L,D] order.  Raises TfaError on a nonzero status."""
-    import torch
-
-    _check_on(q, "q", torch.bfloat16, 4, rows=True)
+    _check_on(q, "q", _BF16, 4, rows=True)
     mid, dims = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight)
     B, L, Hq, Hkv, D, rot = dims
-    with _scope(q.device, stream):
+    dev = q.get_device()
+    with _scope(dev, stream):
         if q_out is None:
-            q_out = torch.empty((B, Hq, L, D), dtype=torch.bfloat16, device=q.device)
+            q_out = q.new_empty((B, Hq, L, D))
+        else:
+            _check_rows(q_out, "q_out", (B, Hq, L, D), dev)
         if k_out is None:
-            k_out = torch.empty((B, Hkv, L, D), dtype=torch.bfloat16, device=q.device)
-        for t, n, h in ((q_out, "q_out", Hq), (k_out, "k_out", Hkv)):
-            _check_on(t, n, torch.bfloat16, 4, q.device, rows=True)
-            if t.shape != (B, h, L, D):
-                raise ValueError(f"{n} must be [B, H, L, D]")
-        rc = lib().tfa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-                                    _strides((q, 1), (k, 1), (q_out, 2), (k_out, 2)), *mid, *dims, int(interleaved),
-                                    eps, mscale, torch.cuda.current_stream().cuda_stream)
+            k_out = k.new_empty((B, Hkv, L, D))
+        else:
+            _check_rows(k_out, "k_out", (B, Hkv, L, D), dev)
+        rc = (_lib or lib()).tfa_qk_norm_rope(
+            q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+            _PACK12(*_tokens(q), *_tokens(k), *_heads(q_out), *_heads(k_out)), *mid, *dims, interleaved, eps, mscale,
+            _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_qk_norm_rope")
     return q_out, k_out
@@ -680,34 +693,29 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
     dq_out [B,Hq,L,D] and dk_out [B,Hkv,L,D] (bf16, any strides with contiguous
     channels).  dq [B,L,Hq,D] and dk [B,L,Hkv,D] are bf16 (views in `out` are fine);
     the weights' are fp32 [D], None without weights."""
-    import torch
-
-    _check_on(dq_out, "dq_out", torch.bfloat16, 4, rows=True)
-    _check_on(q, "q", torch.bfloat16, 4, dq_out.device, rows=True)
+    _check_on(q, "q", _BF16, 4, rows=True)
     mid, dims = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight)
     B, L, Hq, Hkv, D, rot = dims
-    _check_on(dk_out, "dk_out", torch.bfloat16, 4, q.device, rows=True)
-    if dq_out.shape != (B, Hq, L, D) or dk_out.shape != (B, Hkv, L, D):
-        raise ValueError("dq_out and dk_out must be [B, H, L, D]")
-    with _scope(q.device, stream):
+    dev = q.get_device()
+    _check_rows(dq_out, "dq_out", (B, Hq, L, D), dev)
+    _check_rows(dk_out, "dk_out", (B, Hkv, L, D), dev)
+    with _scope(dev, stream):
         if out is None:
-            out = (torch.empty((B, L, Hq, D), dtype=torch.bfloat16, device=q.device),
-                   torch.empty((B, L, Hkv, D), dtype=torch.bfloat16, device=q.device))
-        dq, dk = out
-        for t, n, ref in ((dq, "dq", q), (dk, "dk", k)):
-            _check_on(t, n, torch.bfloat16, 4, q.device, rows=True)
-            if t.shape != ref.shape:
-                raise ValueError(f"{n} has the wrong shape")
-        dwq = dwk = ws = None
+            dq, dk = q.new_empty((B, L, Hq, D)), k.new_empty((B, L, Hkv, D))
+        else:
+            dq, dk = out
+            _check_rows(dq, "dq", (B, L, Hq, D), dev)
+            _check_rows(dk, "dk", (B, L, Hkv, D), dev)
+        L_ = _lib or lib()
+        dwq = dwk = ws = pq = pk = pw = None
         if q_weight is not None:
-            dw = torch.empty((2, D), dtype=torch.float32, device=q.device)
-            dwq, dwk = dw[0], dw[1]
-            ws = torch.empty(lib().tfa_qk_norm_rope_workspace(D), dtype=torch.uint8, device=q.device)
-        rc = lib().tfa_qk_norm_rope_backward(
-            dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-            dwq.data_ptr() if ws is not None else None, dwk.data_ptr() if ws is not None else None,
-            _strides((dq_out, 2), (dk_out, 2), (q, 1), (k, 1), (dq, 1), (dk, 1)), *mid, *dims, int(interleaved), eps,
-            mscale, ws.data_ptr() if ws is not None else None, torch.cuda.current_stream().cuda_stream)
+            dwq, dwk = torch.empty((2, D), dtype=_F32, device=q.device).unbind(0)
+            ws = torch.empty(L_.tfa_qk_norm_rope_workspace(D), dtype=_U8, device=q.device)
+            pq, pk, pw = dwq.data_ptr(), dwk.data_ptr(), ws.data_ptr()
+        rc = L_.tfa_qk_norm_rope_backward(
+            dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(), dk.data_ptr(), pq, pk,
+            _PACK18(*_heads(dq_out), *_heads(dk_out), *_tokens(q), *_tokens(k), *_tokens(dq), *_tokens(dk)), *mid,
+            *dims, interleaved, eps, mscale, pw, _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_qk_norm_rope_backward")
     return dq, dk, dwq, dwk
@@ -719,8 +727,6 @@ KV4_GROUP = 32
 
 def kv4_cache(B, Hkv, capacity, D, device=None):
     """(k_codes, k_meta, v_codes, v_meta): an empty 4-bit cache (every value 0)."""
-    import torch
-
     if D not in (64, 128):
         raise ValueError("head dimension must be 64 or 128")
     dev = "cuda" if device is None else device
@@ -732,16 +738,14 @@ def kv4_cache(B, Hkv, capacity, D, device=None):
 
 
 def _kv4_check(k_codes, k_meta, v_codes, v_meta):
-    """Checks a cache's tensors; (B, Hkv, capacity, D, device)."""
-    import torch
-
-    _check_on(k_codes, "k_codes", torch.uint8, 4)
-    dev = k_codes.device
+    """Checks a cache's tensors; (B, Hkv, capacity, D, device index)."""
+    _check_on(k_codes, "k_codes", _U8, 4)
+    dev = k_codes.get_device()
     B, Hkv, cap, half = k_codes.shape
     meta = (B, Hkv, cap, half // (KV4_GROUP // 2), 2)
-    _check_on(v_codes, "v_codes", torch.uint8, 4, dev)
-    _check_on(k_meta, "k_meta", torch.bfloat16, 5, dev)
-    _check_on(v_meta, "v_meta", torch.bfloat16, 5, dev)
+    _check_on(v_codes, "v_codes", _U8, 4, dev)
+    _check_on(k_meta, "k_meta", _BF16, 5, dev)
+    _check_on(v_meta, "v_meta", _BF16, 5, dev)
     if v_codes.shape != k_codes.shape or k_meta.shape != meta or v_meta.shape != meta:
         raise ValueError("a 4-bit cache is codes [B,Hkv,capacity,D/2] and meta [B,Hkv,capacity,D/32,2], twice")
     return B, Hkv, cap, 2 * half, dev
@@ -749,11 +753,9 @@ def _kv4_check(k_codes, k_meta, v_codes, v_meta):
 
 def _kv4_start(start, B, dev):
     """(device pointer or None, first row) of an int or int32 [B]."""
-    import torch
-
     if isinstance(start, int):
         return None, start
-    _check_on(start, "start", torch.int32, 1, dev)
+    _check_on(start, "start", _I32, 1, dev)
     if start.shape[0] != B:
         raise ValueError("start must hold one row per sequence")
     return start.data_ptr(), 0
@@ -763,19 +765,17 @@ def kv4_append(k, v, k_codes, k_meta, v_codes, v_meta, *, start, stream=None):
     """Writes k, v (bf16 [B,Hkv,L,D], any strides with contiguous channels) into the
     4-bit cache: row i of sequence b at cache row start[b] + i.  start: int32 [B] on
     the device (negative: nothing for that sequence), or an int for all."""
-    import torch
-
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
-    _check_on(k, "k", torch.bfloat16, 4, dev, rows=True)
-    _check_on(v, "v", torch.bfloat16, 4, dev, rows=True)
+    _check_on(k, "k", _BF16, 4, dev, rows=True)
+    _check_on(v, "v", _BF16, 4, dev, rows=True)
     if k.shape != v.shape or k.shape[0] != B or k.shape[1] != Hkv or k.shape[3] != D:
         raise ValueError("k and v must be [B,Hkv,L,D] of the cache's B, Hkv and D")
     ptr, first = _kv4_start(start, B, dev)
-    strides = (ctypes.c_longlong * 6)(*k.stride()[:3], *v.stride()[:3])
+    strides = _PACK6(*k.stride()[:3], *v.stride()[:3])
     with _scope(dev, stream):
-        rc = lib().tfa_kv4_append(k.data_ptr(), v.data_ptr(), strides, k_codes.data_ptr(), k_meta.data_ptr(),
+        rc = (_lib or lib()).tfa_kv4_append(k.data_ptr(), v.data_ptr(), strides, k_codes.data_ptr(), k_meta.data_ptr(),
                                   v_codes.data_ptr(), v_meta.data_ptr(), ptr, first, B, Hkv, k.shape[2], cap, D,
-                                  torch.cuda.current_stream().cuda_stream)
+                                  _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_kv4_append")
 
@@ -783,8 +783,6 @@ def kv4_append(k, v, k_codes, k_meta, v_codes, v_meta, *, start, stream=None):
 def kv4_read(k_codes, k_meta, v_codes, v_meta, *, start=0, rows=None, out=None, stream=None):
     """(k, v) bf16 [B,Hkv,rows,D]: the values of cached rows start[b] .. start[b] + rows - 1
     (start: int32 [B] on the device, or an int; rows: by default all from start on)."""
-    import torch
-
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
     ptr, first = _kv4_start(start, B, dev)
     if rows is None:
@@ -793,42 +791,38 @@ def kv4_read(k_codes, k_meta, v_codes, v_meta, *, start=0, rows=None, out=None, 
         rows = cap - first
     with _scope(dev, stream):
         if out is None:
-            out = (torch.empty((B, Hkv, rows, D), dtype=torch.bfloat16, device=dev),
-                   torch.empty((B, Hkv, rows, D), dtype=torch.bfloat16, device=dev))
-        for t, n in zip(out, ("k", "v")):
-            _check_on(t, n, torch.bfloat16, 4, dev)
-            if t.shape != (B, Hkv, rows, D):
-                raise ValueError(f"{n} must be [B,Hkv,rows,D]")
-        rc = lib().tfa_kv4_read(k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(), v_meta.data_ptr(),
+            out = k_meta.new_empty((B, Hkv, rows, D)), k_meta.new_empty((B, Hkv, rows, D))
+        else:
+            for t, n in zip(out, ("k", "v")):
+                _check_on(t, n, _BF16, 4, dev)
+                if t.shape != (B, Hkv, rows, D):
+                    raise ValueError(f"{n} must be [B,Hkv,rows,D]")
+        rc = (_lib or lib()).tfa_kv4_read(k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(), v_meta.data_ptr(),
                                 out[0].data_ptr(), out[1].data_ptr(), ptr, first, B, Hkv, rows, cap, D,
-                                torch.cuda.current_stream().cuda_stream)
+                                _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_kv4_read")
     return out
 
 
 def _kv4_query(q, B, D, dev, sinks, out):
-    import torch
-
-    _check_on(q, "q", torch.bfloat16, 4, dev)
+    _check_on(q, "q", _BF16, 4, dev)
     if q.shape[0] != B or q.shape[3] != D:
         raise ValueError("q and the cache disagree")
     if sinks is not None:
-        _check_on(sinks, "sinks", torch.float32, 1, dev)
+        _check_on(sinks, "sinks", _F32, 1, dev)
         if sinks.shape[0] != q.shape[1]:
             raise ValueError("sinks must hold one logit per query head")
     if out is not None:
-        _check_on(out, "out", torch.bfloat16, 4, dev)
+        _check_on(out, "out", _BF16, 4, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
 
 
-def _kv4_workspace(workspace, need, dev):
-    import torch
-
+def _kv4_workspace(workspace, need, dev, like):
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    _check_on(workspace, "workspace", torch.uint8, 1, dev)
+        return like.new_empty(need)
+    _check_on(workspace, "workspace", _U8, 1, dev)
     if workspace.shape[0] < need:
         raise ValueError(f"workspace must hold {need} bytes")
     return workspace
@@ -840,23 +834,21 @@ def kv4_decode(q, k_codes, k_meta, v_codes, v_meta, lens, *, scale=None, window=
     on the device, holds each sequence's cached positions, its L new rows last among
     them.  window > 0: the last `window` positions and the `first` first ones.
     workspace: uint8 of tfa_kv4_decode_workspace bytes, by default allocated here."""
-    import torch
-
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
     _kv4_query(q, B, D, dev, sinks, out)
-    _check_on(lens, "lens", torch.int32, 1, dev)
+    _check_on(lens, "lens", _I32, 1, dev)
     if lens.shape[0] != B:
         raise ValueError("lens must hold one length per sequence")
     Hq, L = q.shape[1], q.shape[2]
     with _scope(dev, stream):
         if out is None:
             out = torch.empty_like(q)
-        workspace = _kv4_workspace(workspace, lib().tfa_kv4_decode_workspace(Hq, Hkv, L, D), dev)
-        rc = lib().tfa_kv4_decode(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
+        workspace = _kv4_workspace(workspace, (_lib or lib()).tfa_kv4_decode_workspace(Hq, Hkv, L, D), dev, k_codes)
+        rc = (_lib or lib()).tfa_kv4_decode(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
                                   v_meta.data_ptr(), lens.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, cap, D,
                                   D ** -0.5 if scale is None else scale, window, first, softcap,
                                   sinks.data_ptr() if sinks is not None else None, workspace.data_ptr(),
-                                  torch.cuda.current_stream().cuda_stream)
+                                  _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_kv4_decode")
     return out
@@ -868,21 +860,19 @@ def kv4_prefill(q, k_codes, k_meta, v_codes, v_meta, *, S, scale=None, window=0,
     the 4-bit cache (the chunk's own rows last among them); window and first as for
     kv4_decode.  workspace: uint8 of tfa_kv4_prefill_workspace bytes, by default
     allocated here."""
-    import torch
-
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
     _kv4_query(q, B, D, dev, sinks, out)
     Hq, L = q.shape[1], q.shape[2]
     with _scope(dev, stream):
         if out is None:
             out = torch.empty_like(q)
-        need = lib().tfa_kv4_prefill_workspace(B, Hkv, L, S, D, window, first)
-        workspace = _kv4_workspace(workspace, max(need, 16), dev)
-        rc = lib().tfa_kv4_prefill(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
+        need = (_lib or lib()).tfa_kv4_prefill_workspace(B, Hkv, L, S, D, window, first)
+        workspace = _kv4_workspace(workspace, max(need, 16), dev, k_codes)
+        rc = (_lib or lib()).tfa_kv4_prefill(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
                                    v_meta.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, S, cap, D,
                                    D ** -0.5 if scale is None else scale, window, first, softcap,
                                    sinks.data_ptr() if sinks is not None else None, workspace.data_ptr(),
-                                   torch.cuda.current_stream().cuda_stream)
+                                   _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_kv4_prefill")
     return out

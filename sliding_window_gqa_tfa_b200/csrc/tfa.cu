@@ -25,7 +25,7 @@
 
 namespace {
 
-constexpr int kMaxDevices = 64;
+using tfa::kMaxDevices;
 
 // Scratch of the split schedule, one set per (device, stream) so that calls on
 // different streams never share it: a partial slot and a ready flag per

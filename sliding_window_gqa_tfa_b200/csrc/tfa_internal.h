@@ -6,6 +6,8 @@
 
 namespace tfa {
 
+constexpr int kMaxDevices = 64;  // device_info refuses others
+
 // Record which CUDA call failed (readable through tfa_last_error); TFA_ERR_CUDA.
 int report_cuda(const char *what, cudaError_t e);
 

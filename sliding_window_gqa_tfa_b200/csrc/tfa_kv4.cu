@@ -7,6 +7,7 @@
 // i channel 2i (low half) and 2i + 1; steps and minima: one 32-bit word per
 // group, s in the low half.  A group that holds a value that is not finite (or
 // whose range is not) has s = m = NaN: it reads back as NaN.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -36,26 +37,41 @@ struct AppendParams {
     Cache c;
     const int *start;  // first cache row of each sequence; NULL: start0
     int start0;
-    int B, Hkv, L, cap;
+    unsigned n_rows, L, Hkv;  // n_rows = B Hkv L
+    int cap;
     unsigned *status;
 };
+
+// round((x - lo) / step) of a quotient in [0, 15.1], ties to even as the division's
+// would be: the product with the reciprocal may fall on the wrong side of a half,
+// the remainder x - lo - r step (exact: r step has 12 bits) says which side it was.
+__device__ __forceinline__ uint32_t code_of(float d, float step, float below, float inv) {
+    const float u = fmaf(d, inv, 8388608.f);  // rounds to a whole number in its low bits
+    const uint32_t r = __float_as_uint(u) - 0x4b000000u;
+    const float twice = 2.f * fmaf(-(u - 8388608.f), step, d);
+    const float edge = (r & 1u) ? below : step;  // an odd r yields at a tie: twice >= step
+    const uint32_t q = r + (twice > edge ? 1u : 0u) - (twice < -edge ? 1u : 0u);
+    return q < 15u ? q : 15u;
+}
 
 // One row of one tensor is D / 8 lanes of 16 bytes; four lanes share a group.
 // Bound by the bytes moved: 2 in, 0.625 out a channel.
 template <int D>
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int LPR = D / 8;
-    const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;
+    // 32-bit indexes: the 64-bit divisions took longer than the rest of the kernel
+    const unsigned row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
     const int lane8 = threadIdx.x % LPR;
-    const long long n_rows = static_cast<long long>(p.B) * p.Hkv * p.L;
     const bool is_v = blockIdx.y != 0;
-    const bool in = row < n_rows;
-    const long long bh = in ? row / p.L : 0;
-    const int i = in ? static_cast<int>(row - bh * p.L) : 0;
-    const int b = static_cast<int>(bh / p.Hkv), h = static_cast<int>(bh - static_cast<long long>(b) * p.Hkv);
+    const bool in = row < p.n_rows;
+    const unsigned bh = in ? row / p.L : 0u, i = in ? row - bh * p.L : 0u;
+    const unsigned b = bh / p.Hkv, h = bh - b * p.Hkv;
     const long long *s = is_v ? p.sv : p.sk;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (in) raw = *reinterpret_cast<const uint4 *>((is_v ? p.v : p.k) + b * s[0] + h * s[1] + i * s[2] + lane8 * 8);
+    if (in)
+        raw = *reinterpret_cast<const uint4 *>((is_v ? p.v : p.k) + static_cast<long long>(b) * s[0] +
+                                               static_cast<long long>(h) * s[1] + static_cast<long long>(i) * s[2] +
+                                               lane8 * 8);
     const long long first = p.start ? __ldg(p.start + b) : p.start0;
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     float x[8];
@@ -80,12 +96,14 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     const float step = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(hi - lo, 15.f)));
     const bool fine = odd == 0.f && step <= 3.3895314e38f;  // finite values and a finite step
     uint32_t code = 0u;
-    if (fine && step > 0.f) {
+    if (fine && step >= 0x1p-100f && step <= 0x1p100f) {
+        const float below = __uint_as_float(__float_as_uint(step) - 1u), inv = __frcp_rn(step);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float q = rintf(__fdiv_rn(x[e] - lo, step));
-            code |= static_cast<uint32_t>(fminf(fmaxf(q, 0.f), 15.f)) << (4 * e);
-        }
+        for (int e = 0; e < 8; ++e) code |= code_of(x[e] - lo, step, below, inv) << (4 * e);
+    } else if (fine && step > 0.f) {  // where reciprocal or remainder could leave the range
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            code |= static_cast<uint32_t>(fminf(rintf(__fdiv_rn(x[e] - lo, step)), 15.f)) << (4 * e);
     }
     if (!in || first < 0) return;  // a sequence without a place takes nothing
     const long long at = first + i;
@@ -105,7 +123,8 @@ struct ReadParams {
     __nv_bfloat16 *k, *v;  // [B, Hkv, rows, D]
     const int *start;
     int start0;
-    int B, Hkv, rows, cap;
+    unsigned n_rows, rows, Hkv;  // n_rows = B Hkv rows
+    int cap;
     int split, skip;  // rows from `split` on lie `skip` cached positions further
     unsigned *status;
 };
@@ -123,14 +142,13 @@ __device__ __forceinline__ uint4 values8(uint32_t code, uint32_t meta) {
 template <int D>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
     constexpr int LPR = D / 8;
-    const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;
+    const unsigned row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
     const int lane8 = threadIdx.x % LPR;
-    if (row >= static_cast<long long>(p.B) * p.Hkv * p.rows) return;
+    if (row >= p.n_rows) return;
     const bool is_v = blockIdx.y != 0;
-    const long long bh = row / p.rows;
-    const int b = static_cast<int>(bh / p.Hkv);
+    const unsigned bh = row / p.rows, b = bh / p.Hkv;
+    const int i = static_cast<int>(row - bh * p.rows);
     const long long first = p.start ? __ldg(p.start + b) : p.start0;
-    const long long i = row - bh * p.rows;
     const long long at = first + i + (i >= p.split ? p.skip : 0);
     uint4 out = make_uint4(0u, 0u, 0u, 0u);
     if (first >= 0 && at < p.cap) {
@@ -155,10 +173,9 @@ int check_cache(const void *kc, const void *km, const void *vc, const void *vm, 
     return TFA_OK;
 }
 
-// Blocks of 256 threads for `rows` rows of D / 8 lanes; 0 if the grid cannot hold them.
+// Blocks of 256 threads for `rows` rows of D / 8 lanes; 0 if there are more than 2^31 - 1 rows.
 unsigned row_blocks(long long rows, int D) {
-    const long long n = (rows * (D / 8) + 255) / 256;
-    return n <= 0x7fffffffll ? static_cast<unsigned>(n) : 0u;
+    return rows <= 0x7fffffffll ? static_cast<unsigned>((rows * (D / 8) + 255) / 256) : 0u;
 }
 
 int launch_read(const ReadParams &p, unsigned blocks, int D, cudaStream_t s) {
@@ -194,9 +211,15 @@ template <int D, int NB>
 int launch_decode(DecodeParams &p, int sms, cudaStream_t stream) {
     using C = Cfg<D, NB>;
     p.chunks = (p.rows + C::kRows - 1) / C::kRows;
-    // cheap next to the launch, and the attribute holds for the current device only
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-    if (e != cudaSuccess) return report_cuda("cudaFuncSetAttribute(kv4 decode smem)", e);
+    static std::atomic<bool> prepared[kMaxDevices];  // the attribute holds for one device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return report_cuda("cudaGetDevice", e);
+    if (!prepared[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(decode_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        if (e != cudaSuccess) return report_cuda("cudaFuncSetAttribute(kv4 decode smem)", e);
+        prepared[dev].store(true, std::memory_order_release);
+    }
     const int grid = sms * C::kCtasPerSm < kMaxCtas ? sms * C::kCtasPerSm : kMaxCtas;
     decode_kernel<D, NB><<<grid, 32 * kWarps, C::kSmemBytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda("kv4 decode launch", e);
@@ -243,7 +266,7 @@ extern "C" int tfa_kv4_append(const void *k, const void *v, const long long *str
     p.c = cache_of(k_codes, k_meta, v_codes, v_meta);
     p.start = start;
     p.start0 = first_row;
-    p.B = B;
+    p.n_rows = static_cast<unsigned>(B) * Hkv * L;
     p.Hkv = Hkv;
     p.L = L;
     p.cap = capacity;
@@ -272,7 +295,7 @@ extern "C" int tfa_kv4_read(const void *k_codes, const void *k_meta, const void 
     p.v = static_cast<__nv_bfloat16 *>(v);
     p.start = start;
     p.start0 = first_row;
-    p.B = B;
+    p.n_rows = static_cast<unsigned>(B) * Hkv * rows;
     p.Hkv = Hkv;
     p.rows = rows;
     p.cap = capacity;
@@ -366,7 +389,7 @@ extern "C" int tfa_kv4_prefill(const void *q, const void *k_codes, const void *k
                    const_cast<void *>(v_meta));
     p.k = static_cast<__nv_bfloat16 *>(workspace);
     p.v = p.k + static_cast<size_t>(all) * D;
-    p.B = B;
+    p.n_rows = static_cast<unsigned>(B) * Hkv * rows;
     p.Hkv = Hkv;
     p.rows = rows;
     p.cap = capacity;

@@ -3,13 +3,24 @@
 // For a query row q of a KV group and cached position j, with s and m the step
 // and minimum of a group of 32 channels and c its codes:
 //   q.k_j = sum_groups [ s (sum_d q_d c_d) + m (sum_d q_d) ],
-//   o     = sum_j p_j v_j = sum_j [ (p_j s) (c_d - 8) + p_j (m + 8 s) ]   per channel d,
-// so the tensor core multiplies q and p s with the codes themselves, exact as
-// bf16, and K and V are never rounded.  (c - 8: p s is rounded to bf16, so its
-// factor should have no mean; against c the error was 0.0040 of the output
-// instead of 0.0023.)  A code becomes bf16 by one logical operation: 0x4300 | c
-// is 128 + c; the 128 comes off K's sums as part of m (m - 128 s), and 136 off
-// V's codes by one subtraction for two.
+//   o     = sum_j p_j v_j = sum_j [ (p_j s) c_d + p_j m ]   per channel d,
+// so the tensor core multiplies q and p s with the codes themselves, and K and V
+// are never rounded.  A code in the low four bits of a 16-bit word is the
+// subnormal c 2^-24 of fp16, one in the next four c 2^-20, both exact: a pair of
+// codes costs one logical operation, and no offset has to come off again.  (As
+// bf16, 0x4300 | c = 128 + c, the loop took 370 instructions for 16 positions
+// instead of 250 and was bound by issuing them: 39 us for 16 sequences of at most
+// 8192 positions; p s rounded to bf16 left an error of 0.0024 of the output
+// instead of 0.0017.)
+// fp16 needs its range kept:
+//   q   is scaled by a power of two for each row, its largest magnitude just below
+//       2^15: exact but for channels 2^-28 and more below the largest;
+//   p   is taken against a reference r (in log2 units) with p s < 2^15, so r follows
+//       the scores and the steps: terms down to 2^-30 of the largest survive the
+//       rounding, 2^-11 relative above 2^-20.  r, not the maximum, is what pieces
+//       are joined by.  Steps are taken to lie in [2^-40, 2^80] there.
+// The minima's part of the scores is one more product, of the (s, m) words as they
+// lie in the cache with (0, sum q), the sum split into two bf16.
 //
 // What bounds it is reading the cache (1.25 D bytes a position and head) as long
 // as a group's rows are few, so the products are transposed: positions (K) and
@@ -23,7 +34,7 @@
 // The steps of all (sequence, KV head, chunk of rows) segments are cut into equal
 // ranges, one per CTA; lengths are read on the device.  A segment that lies in
 // one CTA is finished there; the pieces of a cut one go to a workspace and are
-// joined by a second kernel (m* = max m, l* = sum 2^(m - m*) l, likewise O).
+// joined by a second kernel (r* = max r, l* = sum 2^(r - r*) l, likewise O).
 #pragma once
 
 #include <cstdint>
@@ -123,11 +134,24 @@ __device__ __forceinline__ int ctas_used(long long W, int grid) {
 __device__ __forceinline__ long long range_begin(long long W, int used, int c) { return W * c / used; }
 
 // -------------------------------------------------------------- instructions
+// d = a b + d, a b (d from zero), fp16; a b, bf16.
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
+__device__ __forceinline__ void mma0_bf16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
 }
 // Transpose of an 8 x 8 matrix of 16-bit words, a row's two words per lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -135,17 +159,16 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// Codes i and i + 4 of a word (bits 4 i and 16 + 4 i) as the bf16 pair 128 + c.
+// Codes i and i + 4 of a word (bits 4 i and 16 + 4 i) as an fp16 pair: c 2^-24 for
+// even i, c 2^-20 for odd.
 template <int I>
-__device__ __forceinline__ uint32_t pair128(uint32_t w) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w >> (4 * I)), "r"(0x000f000fu), "r"(0x43004300u));
-    return r;
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+    return (w >> (I & 2 ? 8 : 0)) & (I & 1 ? 0x00f000f0u : 0x000f000fu);
 }
-__device__ __forceinline__ uint32_t minus136(uint32_t x) {
-    const __nv_bfloat162 c = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
-    __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&x), c);
-    return *reinterpret_cast<uint32_t *>(&v);
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool in) {
@@ -163,6 +186,14 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
+}
+// A row's words of steps and minima.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+    else
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
 }
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
     unsigned short v;
@@ -196,21 +227,14 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
 // then t, t + 4 and t + 8, t + 12, whose banks differ across t.
 __device__ __forceinline__ int row_of(int s) { return (s & 8) + ((s & 7) >> 1) + 4 * (s & 1); }
 
-// O += P V for one 16-row tile.  SAFE: a position that a row does not see adds
-// nothing even where its step or minimum is not finite.
+// O += P V for one 16-row tile, its rows' words of steps and minima (rows g and
+// g + 8 of the scores' layout) in m0 and m1.  SAFE: a position that a row does not
+// see adds nothing even where its step or minimum is not finite.
 template <int D, int NB, bool SAFE>
 __device__ __forceinline__ void add_values(float (&o)[D / 16][NB][4], float (&om)[D / 32][NB][2],
-                                           const float (&pr)[NB][4], uint32_t vcodes, uint32_t vmeta, int tile, int g,
-                                           int t) {
+                                           const float (&pr)[NB][4], uint32_t vcodes, const uint32_t (&m0)[D / 32],
+                                           const uint32_t (&m1)[D / 32], int tile, int g, int t) {
     using C = Cfg<D, NB>;
-    // steps and minima of the tile's rows g and g + 8 (as the scores' layout has them)
-    const int r0 = tile * 16 + row_of(g), r1 = tile * 16 + row_of(g + 8);
-    uint32_t m0[C::kGroups], m1[C::kGroups];
-#pragma unroll
-    for (int gr = 0; gr < C::kGroups; ++gr) {
-        m0[gr] = lds32(vmeta + r0 * C::kMetaBytes + gr * 4);
-        m1[gr] = lds32(vmeta + r1 * C::kMetaBytes + gr * 4);
-    }
 #pragma unroll
     for (int gr = 0; gr < C::kGroups; ++gr) {
         // codes of channels 32 gr + 4 g .. + 3 of rows t, t + 4, t + 8, t + 12
@@ -220,21 +244,17 @@ __device__ __forceinline__ void add_values(float (&o)[D / 16][NB][4], float (&om
             const int r = tile * 16 + t + 4 * k;
             w[k] = lds16(vcodes + r * C::kRowBytes + chunk_at<D>(r, gr) * 16 + g * 2);
         }
-        const uint32_t wa = w[0] | (w[1] << 16), wb = w[2] | (w[3] << 16);
-        const uint32_t a0[4] = {minus136(pair128<0>(wa)), minus136(pair128<1>(wa)), minus136(pair128<0>(wb)),
-                                minus136(pair128<1>(wb))};
-        const uint32_t a1[4] = {minus136(pair128<2>(wa)), minus136(pair128<3>(wa)), minus136(pair128<2>(wb)),
-                                minus136(pair128<3>(wb))};
-        const float s0 = __uint_as_float(m0[gr] << 16), s1 = __uint_as_float(m1[gr] << 16);
-        const float n0 = fmaf(8.f, s0, __uint_as_float(m0[gr] & 0xffff0000u));
-        const float n1 = fmaf(8.f, s1, __uint_as_float(m1[gr] & 0xffff0000u));
+        const uint32_t wa = __byte_perm(w[0], w[1], 0x5410), wb = __byte_perm(w[2], w[3], 0x5410);
+        const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
+        const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
+        const float s0 = __uint_as_float(m0[gr] << 16), n0 = __uint_as_float(m0[gr] & 0xffff0000u);
+        const float s1 = __uint_as_float(m1[gr] << 16), n1 = __uint_as_float(m1[gr] & 0xffff0000u);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             const float *q = pr[nb];
             auto times = [](float a, float b) { return SAFE && a == 0.f ? 0.f : a * b; };
-            // p s is rounded to bf16 here: 2^-9 of each term, as P is in the dense kernels
-            const uint32_t b[2] = {transpose8(pack_bf16(times(q[0], s0), times(q[1], s0))),
-                                   transpose8(pack_bf16(times(q[2], s1), times(q[3], s1)))};
+            const uint32_t b[2] = {transpose8(pack_f16(times(q[0], s0), times(q[1], s0))),
+                                   transpose8(pack_f16(times(q[2], s1), times(q[3], s1)))};
             mma(o[2 * gr][nb], a0, b);
             mma(o[2 * gr + 1][nb], a1, b);
             om[gr][nb][0] += times(q[0], n0) + times(q[2], n1);
@@ -307,29 +327,59 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
         }
 
         // the query rows as B fragments: lane (g, t) holds row g's channels 32 gr + 8 t ..
-        // + 7, paired as the codes are (i, i + 4); qs: sums over a group for rows 2 t, 2 t + 1
-        uint32_t bq[NB][C::kGroups][2][2];
-        float qs[NB][C::kGroups][2];
+        // + 7, paired as the codes are (i, i + 4), those of odd i scaled by 2^-4 against
+        // the codes' 2^4; bs: (0, sum of the group's q) of group t, split in two bf16;
+        // unit: what scores are multiplied by, for rows 2 t and 2 t + 1
+        uint32_t bq[NB][C::kGroups][2][2], bs[NB][2];
+        float unit[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+            uint4 v[C::kGroups];
+            float top = 0.f, sum[C::kGroups];
 #pragma unroll
             for (int gr = 0; gr < C::kGroups; ++gr) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                v[gr] = make_uint4(0u, 0u, 0u, 0u);
                 if (8 * nb + g < n_rows)
-                    v = __ldg(reinterpret_cast<const uint4 *>(p.q + (qrow + 8 * nb + g) * D + 32 * gr + 8 * t));
-                bq[nb][gr][0][0] = __byte_perm(v.x, v.z, 0x5410);
-                bq[nb][gr][0][1] = __byte_perm(v.x, v.z, 0x7632);
-                bq[nb][gr][1][0] = __byte_perm(v.y, v.w, 0x5410);
-                bq[nb][gr][1][1] = __byte_perm(v.y, v.w, 0x7632);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                float s = 0.f;
+                    v[gr] = __ldg(reinterpret_cast<const uint4 *>(p.q + (qrow + 8 * nb + g) * D + 32 * gr + 8 * t));
+                const uint32_t w[4] = {v[gr].x, v[gr].y, v[gr].z, v[gr].w};
+                sum[gr] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xffff0000u);
-                s += __shfl_xor_sync(0xffffffffu, s, 1);
-                s += __shfl_xor_sync(0xffffffffu, s, 2);
-                qs[nb][gr][0] = __shfl_sync(0xffffffffu, s, 8 * t);
-                qs[nb][gr][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4);
+                for (int e = 0; e < 4; ++e) {
+                    const float x = __uint_as_float(w[e] << 16), y = __uint_as_float(w[e] & 0xffff0000u);
+                    top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+                    sum[gr] += x + y;
+                }
+                sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
+                sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
             }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // rho = 2^(14 - e), 2^e the power of two at or below the row's largest
+            const int e = max(-86, static_cast<int>(__float_as_uint(top) >> 23) - 127);
+            const float rho = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+#pragma unroll
+            for (int gr = 0; gr < C::kGroups; ++gr) {
+                const uint32_t w[4] = {v[gr].x, v[gr].y, v[gr].z, v[gr].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // channels i and i + 4
+                    const uint32_t lo = w[i >> 1], hi = w[2 + (i >> 1)];
+                    const float f = i & 1 ? rho * 0.0625f : rho;
+                    const float x = __uint_as_float(i & 1 ? lo & 0xffff0000u : lo << 16);
+                    const float y = __uint_as_float(i & 1 ? hi & 0xffff0000u : hi << 16);
+                    bq[nb][gr][i >> 1][i & 1] = pack_f16(x * f, y * f);
+                }
+            }
+            float mine = 0.f;
+#pragma unroll
+            for (int gr = 0; gr < C::kGroups; ++gr) mine = t == gr ? sum[gr] : mine;
+            mine *= rho * 0x1p-24f;  // the codes' unit
+            const float head = __bfloat162float(__float2bfloat16_rn(mine));
+            bs[nb][0] = pack_bf16(0.f, mine);
+            bs[nb][1] = pack_bf16(0.f, mine - head);
+            const float un = 0x1p24f / rho;
+            unit[nb][0] = __shfl_sync(0xffffffffu, un, 8 * t);
+            unit[nb][1] = __shfl_sync(0xffffffffu, un, 8 * t + 4);
+            if (p.softcap == 0.f) unit[nb][0] *= p.scale_log2, unit[nb][1] *= p.scale_log2;
         }
 
         float o[D / 16][NB][4], om[C::kGroups][NB][2], m[NB][2], l[NB][2];
@@ -357,36 +407,39 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
             st = st + 1 == C::kStages ? 0 : st + 1;
             const int key0 = (j < sp.fs ? j : j + sp.gap) * kStep;
 
-            // scores: [tile][nb][(row g, rows 2t, 2t + 1), (row g + 8, ..)], log2 units
+            // scores: [tile][nb][(row g, rows 2t, 2t + 1), (row g + 8, ..)]
             float sc[2][NB][4];
 #pragma unroll
             for (int tile = 0; tile < 2; ++tile) {
                 const int r0 = tile * 16 + row_of(g), r1 = tile * 16 + row_of(g + 8);
+                {
+                    // minima: the (s, m) word of group t as it lies there, twice
+                    const bool in = t < C::kGroups;
+                    const uint32_t x0 = in ? lds32(kmeta + r0 * C::kMetaBytes + t * 4) : 0u;
+                    const uint32_t x1 = in ? lds32(kmeta + r1 * C::kMetaBytes + t * 4) : 0u;
+                    const uint32_t a[4] = {x0, x1, x0, x1};
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[tile][nb][e] = 0.f;
+                    for (int nb = 0; nb < NB; ++nb) mma0_bf16(sc[tile][nb], a, bs[nb]);
+                }
+                uint32_t k0[C::kGroups], k1[C::kGroups];
+                lds_words(kmeta + r0 * C::kMetaBytes, k0);
+                lds_words(kmeta + r1 * C::kMetaBytes, k1);
 #pragma unroll
                 for (int gr = 0; gr < C::kGroups; ++gr) {
                     const uint32_t w0 = lds32(kcodes + r0 * C::kRowBytes + chunk_at<D>(r0, gr) * 16 + t * 4);
                     const uint32_t w1 = lds32(kcodes + r1 * C::kRowBytes + chunk_at<D>(r1, gr) * 16 + t * 4);
-                    const uint32_t k0 = lds32(kmeta + r0 * C::kMetaBytes + gr * 4);
-                    const uint32_t k1 = lds32(kmeta + r1 * C::kMetaBytes + gr * 4);
-                    const uint32_t a0[4] = {pair128<0>(w0), pair128<0>(w1), pair128<1>(w0), pair128<1>(w1)};
-                    const uint32_t a1[4] = {pair128<2>(w0), pair128<2>(w1), pair128<3>(w0), pair128<3>(w1)};
-                    const float s0 = __uint_as_float(k0 << 16), s1 = __uint_as_float(k1 << 16);
-                    // the minimum, less what the 128 in every code adds
-                    const float n0 = fmaf(-128.f, s0, __uint_as_float(k0 & 0xffff0000u));
-                    const float n1 = fmaf(-128.f, s1, __uint_as_float(k1 & 0xffff0000u));
+                    const uint32_t a0[4] = {code_pair<0>(w0), code_pair<0>(w1), code_pair<1>(w0), code_pair<1>(w1)};
+                    const uint32_t a1[4] = {code_pair<2>(w0), code_pair<2>(w1), code_pair<3>(w0), code_pair<3>(w1)};
+                    const float s0 = __uint_as_float(k0[gr] << 16), s1 = __uint_as_float(k1[gr] << 16);
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma(acc, a0, bq[nb][gr][0]);
+                        float acc[4];
+                        mma0(acc, a0, bq[nb][gr][0]);
                         mma(acc, a1, bq[nb][gr][1]);
-                        sc[tile][nb][0] = fmaf(s0, acc[0], fmaf(n0, qs[nb][gr][0], sc[tile][nb][0]));
-                        sc[tile][nb][1] = fmaf(s0, acc[1], fmaf(n0, qs[nb][gr][1], sc[tile][nb][1]));
-                        sc[tile][nb][2] = fmaf(s1, acc[2], fmaf(n1, qs[nb][gr][0], sc[tile][nb][2]));
-                        sc[tile][nb][3] = fmaf(s1, acc[3], fmaf(n1, qs[nb][gr][1], sc[tile][nb][3]));
+                        sc[tile][nb][0] = fmaf(s0, acc[0], sc[tile][nb][0]);
+                        sc[tile][nb][1] = fmaf(s0, acc[1], sc[tile][nb][1]);
+                        sc[tile][nb][2] = fmaf(s1, acc[2], sc[tile][nb][2]);
+                        sc[tile][nb][3] = fmaf(s1, acc[3], sc[tile][nb][3]);
                     }
                 }
             }
@@ -397,14 +450,14 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[tile][nb][e] = cap2 * tanhf(sc[tile][nb][e] * u);
+                        for (int e = 0; e < 4; ++e) sc[tile][nb][e] = cap2 * tanhf(sc[tile][nb][e] * unit[nb][e & 1] * u);
             } else {
 #pragma unroll
                 for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[tile][nb][e] *= p.scale_log2;
+                        for (int e = 0; e < 4; ++e) sc[tile][nb][e] *= unit[nb][e & 1];
             }
             // only steps at the causal edge, the tail or the window's edge hold hidden pairs
             const int p0 = sp.n - p.L;  // position of a sequence's first new row
@@ -428,15 +481,28 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                     }
             }
 
-            // running maximum, kept until a score exceeds it by more than 2^8
+            // V's steps and minima, and a power of two above this lane's steps
+            uint32_t v0[2][C::kGroups], v1[2][C::kGroups];
+            float high = 0.f;
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                lds_words(vmeta + (tile * 16 + row_of(g)) * C::kMetaBytes, v0[tile]);
+                lds_words(vmeta + (tile * 16 + row_of(g + 8)) * C::kMetaBytes, v1[tile]);
+#pragma unroll
+                for (int gr = 0; gr < C::kGroups; ++gr)
+                    high = fmax3(high, __uint_as_float(v0[tile][gr] << 16), __uint_as_float(v1[tile][gr] << 16));
+            }
+            const float es = static_cast<float>(
+                min(80, max(-40, static_cast<int>(__float_as_uint(high) >> 23) - 126)));  // step < 2^es
+            // the reference r of a row: moved up when 2^(score - r) 2^es would pass 2^15
             bool grow = false;
             float top[NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    top[nb][e] = fmaxf(fmaxf(sc[0][nb][e], sc[0][nb][2 + e]), fmaxf(sc[1][nb][e], sc[1][nb][2 + e]));
-                    grow |= top[nb][e] - m[nb][e] > 8.f;  // (false where both are -inf)
+                    top[nb][e] = fmaxf(fmaxf(sc[0][nb][e], sc[0][nb][2 + e]), fmaxf(sc[1][nb][e], sc[1][nb][2 + e])) + es;
+                    grow |= top[nb][e] - m[nb][e] > 15.f;  // (false where both are -inf)
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -447,7 +513,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        x = fmaxf(x, m[nb][e]);
+                        x = fmaxf(x - 7.f, m[nb][e]);
                         const float f = m[nb][e] == -CUDART_INF_F ? 0.f : ex2(m[nb][e] - x);
                         m[nb][e] = x;
                         l[nb][e] *= f;
@@ -473,11 +539,11 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                     }
                 }
             if (edge) {
-                add_values<D, NB, true>(o, om, sc[0], vcodes, vmeta, 0, g, t);
-                add_values<D, NB, true>(o, om, sc[1], vcodes, vmeta, 1, g, t);
+                add_values<D, NB, true>(o, om, sc[0], vcodes, v0[0], v1[0], 0, g, t);
+                add_values<D, NB, true>(o, om, sc[1], vcodes, v0[1], v1[1], 1, g, t);
             } else {
-                add_values<D, NB, false>(o, om, sc[0], vcodes, vmeta, 0, g, t);
-                add_values<D, NB, false>(o, om, sc[1], vcodes, vmeta, 1, g, t);
+                add_values<D, NB, false>(o, om, sc[0], vcodes, v0[0], v1[0], 0, g, t);
+                add_values<D, NB, false>(o, om, sc[1], vcodes, v0[1], v1[1], 1, g, t);
             }
             __syncwarp();  // every lane has read the stage that the next copies fill
         }
@@ -505,9 +571,11 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                 float *dst = jo + (warp * C::kRows + row) * C::kOutStride;
 #pragma unroll
                 for (int gr = 0; gr < C::kGroups; ++gr)
-                    *reinterpret_cast<float4 *>(dst + 32 * gr + 4 * g) =
-                        make_float4(o[2 * gr][nb][e] + om[gr][nb][e], o[2 * gr][nb][2 + e] + om[gr][nb][e],
-                                    o[2 * gr + 1][nb][e] + om[gr][nb][e], o[2 * gr + 1][nb][2 + e] + om[gr][nb][e]);
+                    *reinterpret_cast<float4 *>(dst + 32 * gr + 4 * g) =  // out of the codes' units
+                        make_float4(fmaf(o[2 * gr][nb][e], 0x1p24f, om[gr][nb][e]),
+                                    fmaf(o[2 * gr][nb][2 + e], 0x1p20f, om[gr][nb][e]),
+                                    fmaf(o[2 * gr + 1][nb][e], 0x1p24f, om[gr][nb][e]),
+                                    fmaf(o[2 * gr + 1][nb][2 + e], 0x1p20f, om[gr][nb][e]));
                 if (g == 0) {
                     jm[warp * C::kRows + row] = m[nb][e];
                     jl[warp * C::kRows + row] = l[nb][e];
