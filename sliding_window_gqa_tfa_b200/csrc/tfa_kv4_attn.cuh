@@ -171,6 +171,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool in) {
     const int n = in ? BYTES : 0;  // 0: the destination is filled with zeros
     if constexpr (BYTES == 16)
@@ -227,23 +234,41 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
 // then t, t + 4 and t + 8, t + 12, whose banks differ across t.
 __device__ __forceinline__ int row_of(int s) { return (s & 8) + ((s & 7) >> 1) + 4 * (s & 1); }
 
+// Byte offsets of what a lane reads of a step, from the start of K's or V's codes
+// (steps and minima), for the first tile; rows 8 and tiles 16 rows further have the
+// same chunk order, so they lie a constant further.
+template <int D>
+struct LaneOffsets {
+    uint32_t k[D / 32];  // word t of group gr of row row_of(g)
+    uint32_t v[D / 32];  // halfword g of group gr of row t; of row t + 4 the one of group gr ^ kFlip
+    uint32_t m;          // the words of row row_of(g)
+    static constexpr int kFlip = D == 128 ? 2 : 1;
+    __device__ __forceinline__ LaneOffsets(int g, int t) {
+        const int r = row_of(g);
+#pragma unroll
+        for (int gr = 0; gr < D / 32; ++gr) {
+            k[gr] = r * (D / 2) + chunk_at<D>(r, gr) * 16 + t * 4;
+            v[gr] = t * (D / 2) + chunk_at<D>(t, gr) * 16 + g * 2;
+        }
+        m = r * (D / 8);
+    }
+};
+
 // O += P V for one 16-row tile, its rows' words of steps and minima (rows g and
 // g + 8 of the scores' layout) in m0 and m1.  SAFE: a position that a row does not
 // see adds nothing even where its step or minimum is not finite.
 template <int D, int NB, bool SAFE>
 __device__ __forceinline__ void add_values(float (&o)[D / 16][NB][4], float (&om)[D / 32][NB][2],
-                                           const float (&pr)[NB][4], uint32_t vcodes, const uint32_t (&m0)[D / 32],
-                                           const uint32_t (&m1)[D / 32], int tile, int g, int t) {
+                                           const float (&pr)[NB][4], uint32_t vcodes, const LaneOffsets<D> &at,
+                                           const uint32_t (&m0)[D / 32], const uint32_t (&m1)[D / 32]) {
     using C = Cfg<D, NB>;
 #pragma unroll
     for (int gr = 0; gr < C::kGroups; ++gr) {
         // codes of channels 32 gr + 4 g .. + 3 of rows t, t + 4, t + 8, t + 12
         uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = tile * 16 + t + 4 * k;
-            w[k] = lds16(vcodes + r * C::kRowBytes + chunk_at<D>(r, gr) * 16 + g * 2);
-        }
+        for (int k = 0; k < 4; ++k)
+            w[k] = lds16(vcodes + at.v[k & 1 ? gr ^ LaneOffsets<D>::kFlip : gr] + 4 * k * C::kRowBytes);
         const uint32_t wa = __byte_perm(w[0], w[1], 0x5410), wb = __byte_perm(w[2], w[3], 0x5410);
         const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
         const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
@@ -278,6 +303,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t pipe = smem_addr(smem) + warp * C::kStages * 2 * C::kHalfStage;
+    const LaneOffsets<D> at(g, t);
+    // chunk `lane` of a step's codes: row lane / (chunks a row), in that row's order
+    const uint32_t copy_to = (lane / (C::kRowBytes / 16)) * C::kRowBytes +
+                             chunk_at<D>(lane / (C::kRowBytes / 16), lane % (C::kRowBytes / 16)) * 16;
     float *jo = reinterpret_cast<float *>(smem);                      // [warp][row][kOutStride]
     float *jm = jo + kWarps * C::kRows * C::kOutStride, *jl = jm + kWarps * C::kRows;  // [warp][row]
 
@@ -298,31 +327,39 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
         const size_t plane = (static_cast<size_t>(b) * p.Hkv + h) * p.cap;
         const size_t qrow = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.L + row0;
 
-        // copies of step j into stage st: codes in 16-byte chunks, steps and minima row by row
-        auto issue = [&](int j, int st) {
+        // copies of step j into stage st: codes in 16-byte chunks, steps and minima row by
+        // row.  A lane's chunks lie 512 bytes apart on both sides (their rows' chunk
+        // orders agree), so a whole step takes one address a tensor.
+        const uint8_t *kc = p.kc + plane * C::kRowBytes + lane * 16, *vc = p.vc + plane * C::kRowBytes + lane * 16;
+        const uint32_t *km = p.km + (plane + lane) * C::kGroups, *vm = p.vm + (plane + lane) * C::kGroups;
+        auto issue = [&](int j, uint32_t base) {
             const int key0 = (j < sp.fs ? j : j + sp.gap) * kStep;
-            const uint32_t base = pipe + st * 2 * C::kHalfStage;
+            constexpr int kChunks = C::kRowBytes / 16, kCopies = kStep * kChunks / 32;
+            const size_t co = static_cast<size_t>(key0) * C::kRowBytes, mo = static_cast<size_t>(key0) * C::kGroups;
+            const uint32_t dst = base + copy_to, mdst = base + kStep * C::kRowBytes + lane * C::kMetaBytes;
+            if (key0 + kStep <= sp.n) {
 #pragma unroll
-            for (int which = 0; which < 2; ++which) {
-                const uint8_t *codes = which ? p.vc : p.kc;
-                const uint32_t *meta = which ? p.vm : p.km;
-                const uint32_t dst = base + which * C::kHalfStage;
-                constexpr int kChunks = C::kRowBytes / 16;
-#pragma unroll
-                for (int i = 0; i < kStep * kChunks / 32; ++i) {
-                    const int r = (i * 32 + lane) / kChunks, c = (i * 32 + lane) % kChunks;
-                    const bool in = key0 + r < sp.n;
-                    cp_async<16>(dst + r * C::kRowBytes + chunk_at<D>(r, c) * 16,
-                                 codes + (plane + (in ? key0 + r : 0)) * C::kRowBytes + c * 16, in);
+                for (int i = 0; i < kCopies; ++i) {
+                    cp_async<16>(dst + i * 512, kc + co + i * 512);
+                    cp_async<16>(dst + C::kHalfStage + i * 512, vc + co + i * 512);
                 }
-                const bool in = key0 + lane < sp.n;
-                cp_async<C::kMetaBytes>(dst + kStep * C::kRowBytes + lane * C::kMetaBytes,
-                                        meta + (plane + (in ? key0 + lane : 0)) * C::kGroups, in);
+                cp_async<C::kMetaBytes>(mdst, km + mo);
+                cp_async<C::kMetaBytes>(mdst + C::kHalfStage, vm + mo);
+            } else {  // the last step: rows past the end are filled with zeros, nothing is read
+                const int left = sp.n - key0;
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    const bool in = (i * 32 + lane) / kChunks < left;
+                    cp_async<16>(dst + i * 512, kc + (in ? co + i * 512 : 0), in);
+                    cp_async<16>(dst + C::kHalfStage + i * 512, vc + (in ? co + i * 512 : 0), in);
+                }
+                cp_async<C::kMetaBytes>(mdst, km + (lane < left ? mo : 0), lane < left);
+                cp_async<C::kMetaBytes>(mdst + C::kHalfStage, vm + (lane < left ? mo : 0), lane < left);
             }
         };
 #pragma unroll
         for (int st = 0; st < C::kStages - 1; ++st) {
-            if (j0 + warp + st * kWarps < j1) issue(j0 + warp + st * kWarps, st);
+            if (j0 + warp + st * kWarps < j1) issue(j0 + warp + st * kWarps, pipe + st * 2 * C::kHalfStage);
             cp_commit();
         }
 
@@ -395,39 +432,42 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
             l[nb][0] = l[nb][1] = 0.f;
         }
 
-        int st = 0;
+        constexpr uint32_t kStageBytes = 2 * C::kHalfStage, kPipe = C::kStages * kStageBytes;
+        uint32_t here = 0, fill = kPipe - kStageBytes;  // the stage read now, the one filled now
         for (int j = j0 + warp; j < j1; j += kWarps) {
             const int ahead = j + (C::kStages - 1) * kWarps;
-            if (ahead < j1) issue(ahead, st == 0 ? C::kStages - 1 : st - 1);
+            if (ahead < j1) issue(ahead, pipe + fill);
             cp_commit();
             cp_wait<C::kStages - 1>();
             __syncwarp();
-            const uint32_t kcodes = pipe + st * 2 * C::kHalfStage, kmeta = kcodes + kStep * C::kRowBytes;
+            const uint32_t kcodes = pipe + here, kmeta = kcodes + kStep * C::kRowBytes;
             const uint32_t vcodes = kcodes + C::kHalfStage, vmeta = vcodes + kStep * C::kRowBytes;
-            st = st + 1 == C::kStages ? 0 : st + 1;
+            fill = here;
+            here = here + kStageBytes == kPipe ? 0 : here + kStageBytes;
             const int key0 = (j < sp.fs ? j : j + sp.gap) * kStep;
 
             // scores: [tile][nb][(row g, rows 2t, 2t + 1), (row g + 8, ..)]
             float sc[2][NB][4];
 #pragma unroll
             for (int tile = 0; tile < 2; ++tile) {
-                const int r0 = tile * 16 + row_of(g), r1 = tile * 16 + row_of(g + 8);
+                constexpr int kTileMeta = 16 * C::kMetaBytes, kTileCodes = 16 * C::kRowBytes;
+                const uint32_t ma = kmeta + at.m + tile * kTileMeta;
                 {
                     // minima: the (s, m) word of group t as it lies there, twice
                     const bool in = t < C::kGroups;
-                    const uint32_t x0 = in ? lds32(kmeta + r0 * C::kMetaBytes + t * 4) : 0u;
-                    const uint32_t x1 = in ? lds32(kmeta + r1 * C::kMetaBytes + t * 4) : 0u;
+                    const uint32_t x0 = in ? lds32(ma + t * 4) : 0u;
+                    const uint32_t x1 = in ? lds32(ma + t * 4 + 8 * C::kMetaBytes) : 0u;
                     const uint32_t a[4] = {x0, x1, x0, x1};
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) mma0_bf16(sc[tile][nb], a, bs[nb]);
                 }
                 uint32_t k0[C::kGroups], k1[C::kGroups];
-                lds_words(kmeta + r0 * C::kMetaBytes, k0);
-                lds_words(kmeta + r1 * C::kMetaBytes, k1);
+                lds_words(ma, k0);
+                lds_words(ma + 8 * C::kMetaBytes, k1);
 #pragma unroll
                 for (int gr = 0; gr < C::kGroups; ++gr) {
-                    const uint32_t w0 = lds32(kcodes + r0 * C::kRowBytes + chunk_at<D>(r0, gr) * 16 + t * 4);
-                    const uint32_t w1 = lds32(kcodes + r1 * C::kRowBytes + chunk_at<D>(r1, gr) * 16 + t * 4);
+                    const uint32_t w0 = lds32(kcodes + at.k[gr] + tile * kTileCodes);
+                    const uint32_t w1 = lds32(kcodes + at.k[gr] + tile * kTileCodes + 8 * C::kRowBytes);
                     const uint32_t a0[4] = {code_pair<0>(w0), code_pair<0>(w1), code_pair<1>(w0), code_pair<1>(w1)};
                     const uint32_t a1[4] = {code_pair<2>(w0), code_pair<2>(w1), code_pair<3>(w0), code_pair<3>(w1)};
                     const float s0 = __uint_as_float(k0[gr] << 16), s1 = __uint_as_float(k1[gr] << 16);
@@ -486,8 +526,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
             float high = 0.f;
 #pragma unroll
             for (int tile = 0; tile < 2; ++tile) {
-                lds_words(vmeta + (tile * 16 + row_of(g)) * C::kMetaBytes, v0[tile]);
-                lds_words(vmeta + (tile * 16 + row_of(g + 8)) * C::kMetaBytes, v1[tile]);
+                lds_words(vmeta + at.m + tile * 16 * C::kMetaBytes, v0[tile]);
+                lds_words(vmeta + at.m + (tile * 16 + 8) * C::kMetaBytes, v1[tile]);
 #pragma unroll
                 for (int gr = 0; gr < C::kGroups; ++gr)
                     high = fmax3(high, __uint_as_float(v0[tile][gr] << 16), __uint_as_float(v1[tile][gr] << 16));
@@ -539,11 +579,11 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                     }
                 }
             if (edge) {
-                add_values<D, NB, true>(o, om, sc[0], vcodes, v0[0], v1[0], 0, g, t);
-                add_values<D, NB, true>(o, om, sc[1], vcodes, v0[1], v1[1], 1, g, t);
+                add_values<D, NB, true>(o, om, sc[0], vcodes, at, v0[0], v1[0]);
+                add_values<D, NB, true>(o, om, sc[1], vcodes + 16 * C::kRowBytes, at, v0[1], v1[1]);
             } else {
-                add_values<D, NB, false>(o, om, sc[0], vcodes, v0[0], v1[0], 0, g, t);
-                add_values<D, NB, false>(o, om, sc[1], vcodes, v0[1], v1[1], 1, g, t);
+                add_values<D, NB, false>(o, om, sc[0], vcodes, at, v0[0], v1[0]);
+                add_values<D, NB, false>(o, om, sc[1], vcodes + 16 * C::kRowBytes, at, v0[1], v1[1]);
             }
             __syncwarp();  // every lane has read the stage that the next copies fill
         }

@@ -50,6 +50,7 @@ struct Params {
     int conj;   // rotate back (a gradient)
     int inter;  // pairs of neighbouring channels (2i, 2i + 1)
     float *partial;  // gradient: [blocks][2][D]
+    int q_slots, rounds;  // gradient: slots that take query rows, rounds of a token
 };
 
 __device__ __forceinline__ int position(const Params &p, int b, int l) {
@@ -197,96 +198,99 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
 // Gradient with norms: blocks walk the tokens, so that the weights' gradients
 // gather in registers over all of a block's rows; one partial sum per block,
 // added up in block order by the second kernel (the same order every time).
+// A slot (the lanes of a row) takes query rows only or key rows only, in
+// proportion: it keeps one weight and one sum, and no selection in the loop
+// (with both in every slot the loop took 62 instructions a channel, not 20).
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const __grid_constant__ Params p) {
     constexpr int LPR = D / 8, kSlots = kThreads / LPR;
     __shared__ float2 tab[2][D / 2];
     __shared__ float red[kSlots][D + 4];
     const int lane8 = threadIdx.x % LPR, slot = threadIdx.x / LPR;
-    const int n_rows = p.Hq + p.Hkv, n_tokens = p.B * p.L;
-    float wq[8], wk[8], gq[8], gk[8];
-    unpack(*reinterpret_cast<const uint4 *>(p.wq + lane8 * 8), wq);
-    unpack(*reinterpret_cast<const uint4 *>(p.wk + lane8 * 8), wk);
+    const int n_tokens = p.B * p.L;
+    const int q_slots = p.q_slots;
+    const bool isq = slot < q_slots;
+    const int first = isq ? slot : slot - q_slots, step = isq ? q_slots : kSlots - q_slots;
+    const int heads = isq ? p.Hq : p.Hkv;
+    const int rounds = p.rounds;  // the block's: the larger of the two kinds'
+    const Strides sx = isq ? p.sq : p.sk, sg = isq ? p.sdq : p.sdk, so = isq ? p.sqo : p.sko;
+    const __nv_bfloat16 *xb = (isq ? p.q : p.k) + lane8 * 8 + first * sx.h;
+    const __nv_bfloat16 *gb = (isq ? p.dq : p.dk) + lane8 * 8 + first * sg.h;
+    __nv_bfloat16 *ob = (isq ? p.qo : p.ko) + lane8 * 8 + first * so.h;
+    const long long hx = step * sx.h, hg = step * sg.h, ho = step * so.h;  // a round further
+    float w[8], acc[8];
+    unpack(*reinterpret_cast<const uint4 *>((isq ? p.wq : p.wk) + lane8 * 8), w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) gq[e] = gk[e] = 0.f;
-    // The loads of a round (kSlots rows of a token) are issued while the round
-    // before is computed, and the next token's angles while this one's rows are:
-    // with both in line the kernel waited for memory, 94 us against 33 us for
-    // 4 x 2047 tokens of 24 heads (151 MB).
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    // The loads of a round are issued while the round before is computed, and the
+    // next token's angles while this one's rows are: with both in line the kernel
+    // waited for memory.
     uint4 xv, gv;
-    auto load = [&](int token, int row) {
+    const __nv_bfloat16 *xp, *gp;
+    auto load = [&](bool in) {
         xv = gv = make_uint4(0u, 0u, 0u, 0u);
-        if (token >= n_tokens || row >= n_rows) return;
-        const int b = token / p.L, l = token - b * p.L;
-        const bool isq = row < p.Hq;
-        const int h = isq ? row : row - p.Hq;
-        const __nv_bfloat16 *xp = isq ? p.q + b * p.sq.b + l * p.sq.l + h * p.sq.h
-                                      : p.k + b * p.sk.b + l * p.sk.l + h * p.sk.h;
-        const __nv_bfloat16 *gp = isq ? p.dq + b * p.sdq.b + l * p.sdq.l + h * p.sdq.h
-                                      : p.dk + b * p.sdk.b + l * p.sdk.l + h * p.sdk.h;
-        xv = *reinterpret_cast<const uint4 *>(xp + lane8 * 8);
-        gv = *reinterpret_cast<const uint4 *>(gp + lane8 * 8);
+        if (in) {
+            xv = *reinterpret_cast<const uint4 *>(xp);
+            gv = *reinterpret_cast<const uint4 *>(gp);
+        }
     };
     int which = 0;
-    load(blockIdx.x, slot);
-    fill_table(p, position(p, blockIdx.x / p.L, blockIdx.x % p.L), tab[0]);
+    int b = blockIdx.x / p.L, l = blockIdx.x - b * p.L;
+    xp = xb + b * sx.b + l * sx.l;
+    gp = gb + b * sg.b + l * sg.l;
+    load(first < heads);
+    fill_table(p, position(p, b, l), tab[0]);
     __syncthreads();
     for (int token = blockIdx.x; token < n_tokens; token += gridDim.x, which ^= 1) {
-        const int b = token / p.L, l = token - b * p.L;
-        const int next = token + gridDim.x;
+        __nv_bfloat16 *op = ob + b * so.b + l * so.l;
         Factors<INTER> f;
         f.load(tab[which], lane8, p.rot);
-        if (next < n_tokens) fill_table(p, position(p, next / p.L, next % p.L), tab[which ^ 1]);
-        for (int base = 0; base < n_rows; base += kSlots) {
-            const int row = base + slot;
-            const bool isq = row < p.Hq, in = row < n_rows;
+        const int next = token + gridDim.x;
+        b = next / p.L;
+        l = next - b * p.L;
+        if (next < n_tokens) fill_table(p, position(p, b, l), tab[which ^ 1]);
+        int h = first;
+        for (int i = 0; i < rounds; ++i, h += step, op += ho) {
             float x[8], g[8];
             unpack(xv, x);
             unpack(gv, g);
-            if (base + kSlots < n_rows) load(token, row + kSlots);
-            else load(next, slot);
+            const bool in = h < heads;
+            if (i + 1 < rounds) {
+                xp += hx;
+                gp += hg;
+                load(h + step < heads);
+            } else {
+                xp = xb + b * sx.b + l * sx.l;
+                gp = gb + b * sg.b + l * sg.l;
+                load(next < n_tokens && first < heads);
+            }
             f.rotate(g, lane8, p.rot);
             float ss = 0.f, dot = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ss = fmaf(x[e], x[e], ss);
-                dot = fmaf(g[e] * (isq ? wq[e] : wk[e]), x[e], dot);
-            }
-            ss = row_sum<LPR>(ss);
-            dot = row_sum<LPR>(dot);
-            const float r = rsqrtf(ss * (1.f / D) + p.eps);
-            const float m = dot * r * r * (1.f / D);  // h mean(w g h) = x m
-            float o[8];
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+            const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float gx = g[e] * x[e] * r;
-                if (in) {
-                    if (isq) gq[e] += gx;
-                    else gk[e] += gx;
-                }
-                o[e] = r * fmaf(-x[e], m, g[e] * (isq ? wq[e] : wk[e]));
+                const float gx = g[e] * x[e];
+                dot = fmaf(gx, w[e], dot);
+                if (in) acc[e] = fmaf(gx, r, acc[e]);  // (a row past the last holds zeros, but eps may be 0)
             }
-            if (in) {
-                const int h = isq ? row : row - p.Hq;
-                __nv_bfloat16 *op = isq ? p.qo + b * p.sqo.b + l * p.sqo.l + h * p.sqo.h
-                                        : p.ko + b * p.sko.b + l * p.sko.l + h * p.sko.h;
-                *reinterpret_cast<uint4 *>(op + lane8 * 8) = pack(o);
-            }
+            dot = row_sum<LPR>(dot);
+            const float m = -dot * r * r * (1.f / D);  // dx = r (w g - x r^2 mean(w g x))
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = r * fmaf(x[e], m, g[e] * w[e]);
+            if (in) *reinterpret_cast<uint4 *>(op) = pack(g);
         }
         __syncthreads();  // this table may be overwritten, the next one is there
     }
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) red[slot][lane8 * 8 + e] = t ? gk[e] : gq[e];
-        __syncthreads();
-        if (threadIdx.x < D) {
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < kSlots; ++i) s += red[i][threadIdx.x];
-            p.partial[(static_cast<size_t>(blockIdx.x) * 2 + t) * D + threadIdx.x] = s;
-        }
+    for (int e = 0; e < 8; ++e) red[slot][lane8 * 8 + e] = acc[e];
+    __syncthreads();
+    if (threadIdx.x < 2 * D) {
+        const int t = threadIdx.x / D, c = threadIdx.x % D;
+        float s = 0.f;
+        for (int i = t ? q_slots : 0; i < (t ? kSlots : q_slots); ++i) s += red[i][c];
+        p.partial[(static_cast<size_t>(blockIdx.x) * 2 + t) * D + c] = s;
     }
 }
 
@@ -350,6 +354,16 @@ int launch_forward(Params &p, int D, cudaStream_t stream) {
 int launch_backward(Params &p, int D, float *dwq, float *dwk, cudaStream_t stream) {
     const int tokens = p.B * p.L;
     const int blocks = tokens < kBwdBlocks ? tokens : kBwdBlocks;
+    // the split of the slots with the fewest rounds, the proportional one or a neighbour
+    const int slots = kThreads / (D / 8);
+    p.rounds = 0x7fffffff;
+    for (int n = 1; n < slots; ++n) {
+        const int a = (p.Hq + n - 1) / n, b = (p.Hkv + slots - n - 1) / (slots - n);
+        if ((a > b ? a : b) < p.rounds) {
+            p.rounds = a > b ? a : b;
+            p.q_slots = n;
+        }
+    }
     using Kern = void (*)(Params);
     const Kern kern = D == 128 ? (p.inter ? backward_kernel<128, true> : backward_kernel<128, false>)
                                : (p.inter ? backward_kernel<64, true> : backward_kernel<64, false>);
