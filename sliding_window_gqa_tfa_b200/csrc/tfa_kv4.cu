@@ -253,8 +253,8 @@ int launch_decode(DecodeParams &p, int sms, cudaStream_t stream) {
     decode_kernel<D, NB><<<grid, 32 * kWarps, C::kSmemBytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda("kv4 decode launch", e);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.chunks));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.chunks * (C::kRows / kJoinRows)));
+    cfg.blockDim = dim3(32 * kJoinRows);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

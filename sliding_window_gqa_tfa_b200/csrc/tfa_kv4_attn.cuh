@@ -76,10 +76,9 @@ struct Span {
     int steps;  // in all
     int fs, gap;
 };
-__device__ __forceinline__ Span span_of(const DecodeParams &p, int b) {
+__device__ __forceinline__ Span span_of(const DecodeParams &p, int n) {
     Span s;
-    s.n = __ldg(p.lens + b);
-    if (s.n < 0 || s.n > p.cap) s.n = 0;
+    s.n = n < 0 || n > p.cap ? 0 : n;
     s.fs = s.gap = s.steps = 0;
     if (s.n == 0) return s;
     s.steps = (s.n + kStep - 1) / kStep;
@@ -97,41 +96,100 @@ __device__ __forceinline__ Span span_of(const DecodeParams &p, int b) {
     return s;
 }
 
-// Prefix sums of the sequences' steps, by the block's threads: pre[b] for b in [0, B].
-__device__ __forceinline__ void prefix_steps(const DecodeParams &p, long long *pre, bool report) {
-    __shared__ int steps[kMaxSeqs];
-    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-        const int n = __ldg(p.lens + b);
-        if (report && (n < 0 || n > p.cap)) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
-        steps[b] = span_of(p, b).steps;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x, per = (p.B + 31) / 32;
-        const int a0 = min(lane * per, p.B), a1 = min(a0 + per, p.B);
-        long long sum = 0;
-        for (int i = a0; i < a1; ++i) sum += steps[i];
-        long long incl = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += y;
-        }
-        long long run = incl - sum;
-        for (int i = a0; i < a1; ++i) {
-            pre[i] = run;
-            run += steps[i];
-        }
-        if (a1 == p.B) pre[p.B] = incl;  // (lanes without a share hold the total too)
-    }
-    __syncthreads();
-}
+// Where the sequences' steps lie in the order that is cut into ranges: sequence b's
+// segments (HC of them) begin at step begin(b) HC.  Up to 32 sequences are held one
+// per lane, the same in every warp, without a word to the others; more of them in
+// shared memory.  Every lane of a warp calls the members together.
+struct Order {
+    int HC, B, lane;
+    int n, steps, before;   // B <= 32: the lane's sequence, the steps before it
+    long long *pre;         // B > 32: steps before each, [B + 1]
+    long long total;        // of all sequences, for one segment each
 
-__device__ __forceinline__ int ctas_used(long long W, int grid) {
-    const long long n = (W + kCtaMinSteps - 1) / kCtaMinSteps;
-    return n < grid ? static_cast<int>(n) : grid;
-}
-__device__ __forceinline__ long long range_begin(long long W, int used, int c) { return W * c / used; }
+    __device__ __forceinline__ Order(const DecodeParams &p, long long *pre_, bool report)
+        : HC(p.Hkv * p.chunks), B(p.B), lane(threadIdx.x & 31), n(0), steps(0), before(0), pre(pre_) {
+        if (B <= 32) {
+            if (lane < B) n = __ldg(p.lens + lane);
+            if (report && threadIdx.x < 32 && (n < 0 || n > p.cap)) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
+            steps = span_of(p, n).steps;
+            int incl = steps;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += y;
+            }
+            before = incl - steps;
+            total = __shfl_sync(0xffffffffu, incl, 31);
+            return;
+        }
+        for (int b = threadIdx.x; b < B; b += blockDim.x) {
+            const int len = __ldg(p.lens + b);
+            if (report && (len < 0 || len > p.cap)) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
+            pre[b] = span_of(p, len).steps;
+        }
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            const int per = (B + 31) / 32, a0 = min(lane * per, B), a1 = min(a0 + per, B);
+            long long sum = 0;
+            for (int i = a0; i < a1; ++i) sum += pre[i];
+            long long incl = sum;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += y;
+            }
+            long long run = incl - sum;
+            for (int i = a0; i < a1; ++i) {
+                const long long mine = pre[i];
+                pre[i] = run;
+                run += mine;
+            }
+            if (lane == 31) pre[B] = incl;
+        }
+        __syncthreads();
+        total = pre[B];
+    }
+    // The sequence that holds step x < total HC: the last that begins at or before it.
+    __device__ __forceinline__ int find(long long x) const {
+        if (B <= 32) {
+            const unsigned at = __ballot_sync(0xffffffffu, lane < B && static_cast<long long>(before) * HC <= x);
+            return 31 - __clz(at);
+        }
+        int lo = 0, hi = B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (pre[mid] * HC <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    }
+    __device__ __forceinline__ long long begin(int b) const {
+        return (B <= 32 ? static_cast<long long>(__shfl_sync(0xffffffffu, before, b)) : pre[b]) * HC;
+    }
+    __device__ __forceinline__ int length(const DecodeParams &p, int b) const {
+        return B <= 32 ? __shfl_sync(0xffffffffu, n, b) : __ldg(p.lens + b);
+    }
+};
+
+// The ranges of W steps: `used` CTAs take q steps each, the first r of them one more.
+struct Ranges {
+    int used;
+    long long q, r;
+    __device__ __forceinline__ Ranges(long long W, int grid) {
+        used = W < static_cast<long long>(grid) * kCtaMinSteps ? static_cast<int>((W + kCtaMinSteps - 1) / kCtaMinSteps) : grid;
+        q = used ? quotient(W, used) : 0;
+        r = W - q * used;
+    }
+    __device__ __forceinline__ long long begin(int c) const { return q * c + (c < r ? c : r); }
+    __device__ __forceinline__ int cta_of(long long x) const {
+        const long long head = r * (q + 1);
+        return static_cast<int>(x < head ? quotient(x, q + 1) : r + quotient(x - head, q));
+    }
+    // (64-bit divisions take some 150 instructions)
+    __device__ __forceinline__ static long long quotient(long long a, long long b) {
+        return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b)) : a / b;
+    }
+};
 
 // -------------------------------------------------------------- instructions
 // d = a b + d, a b (d from zero), fp16; a b, bf16.
@@ -254,14 +312,16 @@ struct LaneOffsets {
     }
 };
 
-// O += P V for one 16-row tile, its rows' words of steps and minima (rows g and
-// g + 8 of the scores' layout) in m0 and m1.  SAFE: a position that a row does not
-// see adds nothing even where its step or minimum is not finite.
+// O += P V for one 16-row tile.  SAFE: a position that a row does not see adds
+// nothing even where its step or minimum is not finite.
 template <int D, int NB, bool SAFE>
 __device__ __forceinline__ void add_values(float (&o)[D / 16][NB][4], float (&om)[D / 32][NB][2],
-                                           const float (&pr)[NB][4], uint32_t vcodes, const LaneOffsets<D> &at,
-                                           const uint32_t (&m0)[D / 32], const uint32_t (&m1)[D / 32]) {
+                                           const float (&pr)[NB][4], uint32_t vcodes, uint32_t vmeta,
+                                           const LaneOffsets<D> &at) {
     using C = Cfg<D, NB>;
+    uint32_t m0[C::kGroups], m1[C::kGroups];  // rows g and g + 8 of the scores' layout
+    lds_words(vmeta + at.m, m0);
+    lds_words(vmeta + at.m + 8 * C::kMetaBytes, m1);
 #pragma unroll
     for (int gr = 0; gr < C::kGroups; ++gr) {
         // codes of channels 32 gr + 4 g .. + 3 of rows t, t + 4, t + 8, t + 12
@@ -294,12 +354,11 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long pre[kMaxSeqs + 1];
     grid_dep_launch();  // the joining kernel may be set up meanwhile; it waits for this one's end
-    prefix_steps(p, pre, blockIdx.x == 0);
-    const int HC = p.Hkv * p.chunks;
-    const long long W = pre[p.B] * HC;
-    const int used = ctas_used(W, gridDim.x);
-    if (static_cast<int>(blockIdx.x) >= used) return;
-    const long long begin = range_begin(W, used, blockIdx.x), end = range_begin(W, used, blockIdx.x + 1);
+    const Order order(p, pre, blockIdx.x == 0);
+    const long long W = order.total * order.HC;
+    const Ranges ranges(W, gridDim.x);
+    if (static_cast<int>(blockIdx.x) >= ranges.used) return;
+    const long long begin = ranges.begin(blockIdx.x), end = ranges.begin(blockIdx.x + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t pipe = smem_addr(smem) + warp * C::kStages * 2 * C::kHalfStage;
@@ -311,16 +370,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
     float *jm = jo + kWarps * C::kRows * C::kOutStride, *jl = jm + kWarps * C::kRows;  // [warp][row]
 
     for (long long pos = begin; pos < end;) {
-        int lo = 0, hi = p.B - 1;  // the sequence that holds step `pos`: the last that begins at or before it
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (pre[mid] * HC <= pos) lo = mid;
-            else hi = mid - 1;
-        }
-        const int b = lo;
-        const Span sp = span_of(p, b);
-        const long long rel = pos - pre[b] * HC;
-        const int hc = static_cast<int>(rel / sp.steps), j0 = static_cast<int>(rel - static_cast<long long>(hc) * sp.steps);
+        const int b = order.find(pos);
+        const Span sp = span_of(p, order.length(p, b));
+        const long long rel = pos - order.begin(b);
+        const int hc = static_cast<int>(Ranges::quotient(rel, sp.steps)), j0 = static_cast<int>(rel - static_cast<long long>(hc) * sp.steps);
         const int j1 = static_cast<int>(min(static_cast<long long>(sp.steps), j0 + (end - pos)));
         const int h = hc / p.chunks, row0 = (hc - h * p.chunks) * C::kRows;
         const int n_rows = min(C::kRows, p.rows - row0);
@@ -521,19 +574,16 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                     }
             }
 
-            // V's steps and minima, and a power of two above this lane's steps
-            uint32_t v0[2][C::kGroups], v1[2][C::kGroups];
-            float high = 0.f;
+            // a power of two above the steps of V's rows, a row a lane
+            float es;
+            {
+                uint32_t w[C::kGroups], high = 0u;
+                lds_words(vmeta + lane * C::kMetaBytes, w);
 #pragma unroll
-            for (int tile = 0; tile < 2; ++tile) {
-                lds_words(vmeta + at.m + tile * 16 * C::kMetaBytes, v0[tile]);
-                lds_words(vmeta + at.m + (tile * 16 + 8) * C::kMetaBytes, v1[tile]);
-#pragma unroll
-                for (int gr = 0; gr < C::kGroups; ++gr)
-                    high = fmax3(high, __uint_as_float(v0[tile][gr] << 16), __uint_as_float(v1[tile][gr] << 16));
+                for (int gr = 0; gr < C::kGroups; ++gr) high = max(high, (w[gr] & 0x7fffu) < 0x7f80u ? w[gr] & 0x7fffu : 0u);
+                high = __reduce_max_sync(0xffffffffu, high);  // bf16 patterns: ordered like their values
+                es = static_cast<float>(min(80, max(-40, static_cast<int>(high >> 7) - 126)));  // step < 2^es
             }
-            const float es = static_cast<float>(
-                min(80, max(-40, static_cast<int>(__float_as_uint(high) >> 23) - 126)));  // step < 2^es
             // the reference r of a row: moved up when 2^(score - r) 2^es would pass 2^15
             bool grow = false;
             float top[NB][2];
@@ -579,11 +629,11 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                     }
                 }
             if (edge) {
-                add_values<D, NB, true>(o, om, sc[0], vcodes, at, v0[0], v1[0]);
-                add_values<D, NB, true>(o, om, sc[1], vcodes + 16 * C::kRowBytes, at, v0[1], v1[1]);
+                add_values<D, NB, true>(o, om, sc[0], vcodes, vmeta, at);
+                add_values<D, NB, true>(o, om, sc[1], vcodes + 16 * C::kRowBytes, vmeta + 16 * C::kMetaBytes, at);
             } else {
-                add_values<D, NB, false>(o, om, sc[0], vcodes, at, v0[0], v1[0]);
-                add_values<D, NB, false>(o, om, sc[1], vcodes + 16 * C::kRowBytes, at, v0[1], v1[1]);
+                add_values<D, NB, false>(o, om, sc[0], vcodes, vmeta, at);
+                add_values<D, NB, false>(o, om, sc[1], vcodes + 16 * C::kRowBytes, vmeta + 16 * C::kMetaBytes, at);
             }
             __syncwarp();  // every lane has read the stage that the next copies fill
         }
@@ -660,75 +710,73 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
 }
 
 // Joins the pieces of the segments that were cut, and writes zeros for a sequence
-// without a position.  One block per segment.
+// without a position.  A warp takes one row of a segment, a lane D / 32 channels of
+// it; up to 16 pieces' loads are in flight together, as there may be as many pieces
+// as CTAs.  (One block for a segment's rows, eight pieces at a time and the ranges
+// divided out anew for each took 23 us for 8 segments of 37 pieces.)
+constexpr int kJoinRows = 4;  // warps of a block
+
 template <int D, int NB>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeParams p, int grid) {
+__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const __grid_constant__ DecodeParams p, int grid) {
     using C = Cfg<D, NB>;
     __shared__ long long pre[kMaxSeqs + 1];
-    prefix_steps(p, pre, false);  // the lengths are the caller's: no need to wait for them
-    const int HC = p.Hkv * p.chunks;
-    const int b = blockIdx.x / HC, hc = blockIdx.x - b * HC;
+    constexpr int kRowBlocks = C::kRows / kJoinRows, kVec = D / 32;
+    const Order order(p, pre, false);  // the lengths are the caller's: no need to wait for them
+    const int HC = order.HC;
+    const int segment = blockIdx.x / kRowBlocks, b = segment / HC, hc = segment - b * HC;
     const int h = hc / p.chunks, row0 = (hc - h * p.chunks) * C::kRows;
-    const int n_rows = min(C::kRows, p.rows - row0);
+    const int row = (blockIdx.x % kRowBlocks) * kJoinRows + (threadIdx.x >> 5);
     const size_t qrow = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.L + row0;
-    const long long W = pre[p.B] * HC;
-    const int steps = static_cast<int>(pre[b + 1] - pre[b]);
-    if (steps == 0) {
-        grid_dep_wait();
-        for (int i = threadIdx.x; i < n_rows * (D / 4); i += 128)
-            *reinterpret_cast<uint2 *>(p.o + (qrow + i / (D / 4)) * D + 4 * (i % (D / 4))) = make_uint2(0u, 0u);
-        return;
-    }
-    const int used = ctas_used(W, grid);
-    const long long x0 = pre[b] * HC + static_cast<long long>(hc) * steps, x1 = x0 + steps;
-    auto cta_of = [&](long long x) {  // the CTA whose range holds step x
-        int c = static_cast<int>(x * used / W);
-        while (c + 1 < used && range_begin(W, used, c + 1) <= x) ++c;
-        while (range_begin(W, used, c) > x) --c;
-        return c;
-    };
-    const int c0 = cta_of(x0), c1 = cta_of(x1 - 1);
+    const int steps = span_of(p, order.length(p, b)).steps;
+    const Ranges ranges(order.total * HC, grid);
+    const long long x0 = order.begin(b) + static_cast<long long>(hc) * steps;
+    const int c0 = steps ? ranges.cta_of(x0) : 0, c1 = steps ? ranges.cta_of(x0 + steps - 1) : 0;
+    const bool first_is_second = steps && ranges.begin(c0) < x0;  // c0's slot: its second piece
     grid_dep_wait();
-    if (c0 == c1) return;  // it was finished where it was computed
-    auto slot_of = [&](int c) {
-        return p.part + static_cast<size_t>(2 * c + (c == c0 && range_begin(W, used, c) < x0 ? 1 : 0)) * C::kSlotFloats;
-    };
-    for (int i = threadIdx.x; i < n_rows * (D / 4); i += 128) {
-        const int row = i / (D / 4), c4 = i % (D / 4);
-        float mx = -CUDART_INF_F, sum = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kBatch = 8;  // pieces whose loads are in flight together
-        for (int k0 = c0; k0 <= c1; k0 += kBatch) {
-            float mk[kBatch], lk[kBatch];
-            float4 v[kBatch];
+    if (row0 + row >= p.rows || (steps && c0 == c1)) return;  // (one CTA: finished where it was computed)
+    float mx = -CUDART_INF_F, sum = 0.f, a[kVec];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const bool in = k0 + u <= c1;
-                const float *s = slot_of(in ? k0 + u : k0);
-                mk[u] = in ? __ldcg(s + C::kRows * D + row) : -CUDART_INF_F;
-                lk[u] = __ldcg(s + C::kRows * (D + 1) + row);
-                v[u] = __ldcg(reinterpret_cast<const float4 *>(s + row * D + 4 * c4));
+    for (int i = 0; i < kVec; ++i) a[i] = 0.f;
+    constexpr int kBatch = 16;
+    for (int k0 = c0; k0 <= c1 && steps; k0 += kBatch) {
+        float mk[kBatch], lk[kBatch], v[kBatch][kVec];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int c = min(k0 + u, c1);
+            const float *s = p.part + static_cast<size_t>(2 * c + (c == c0 && first_is_second ? 1 : 0)) * C::kSlotFloats;
+            mk[u] = k0 + u <= c1 ? __ldcg(s + C::kRows * D + row) : -CUDART_INF_F;
+            lk[u] = __ldcg(s + C::kRows * (D + 1) + row);
+            const float *src = s + row * D + (threadIdx.x & 31) * kVec;
+            if constexpr (kVec == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                v[u][0] = x.x, v[u][1] = x.y;
             }
-            float mn = mx;
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, mk[u]);
-            const float f0 = mx == -CUDART_INF_F ? 0.f : ex2(mx - mn);
-            sum *= f0, a.x *= f0, a.y *= f0, a.z *= f0, a.w *= f0;
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                if (mk[u] == -CUDART_INF_F) continue;
-                const float f = ex2(mk[u] - mn);
-                sum = fmaf(f, lk[u], sum);
-                a.x = fmaf(f, v[u].x, a.x), a.y = fmaf(f, v[u].y, a.y);
-                a.z = fmaf(f, v[u].z, a.z), a.w = fmaf(f, v[u].w, a.w);
-            }
-            mx = mn;
         }
-        if (p.sinks && mx > -CUDART_INF_F) sum += ex2(fmaf(__ldg(p.sinks + h * p.G + (row0 + row) / p.L), kLog2e, -mx));
-        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-        *reinterpret_cast<uint2 *>(p.o + (qrow + row) * D + 4 * c4) =
-            make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+        float mn = mx;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, mk[u]);
+        const float f0 = mx == -CUDART_INF_F ? 0.f : ex2(mx - mn);
+        sum *= f0;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) a[i] *= f0;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (mk[u] == -CUDART_INF_F) continue;
+            const float f = ex2(mk[u] - mn);
+            sum = fmaf(f, lk[u], sum);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) a[i] = fmaf(f, v[u][i], a[i]);
+        }
+        mx = mn;
     }
+    if (p.sinks && mx > -CUDART_INF_F) sum += ex2(fmaf(__ldg(p.sinks + h * p.G + (row0 + row) / p.L), kLog2e, -mx));
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + (qrow + row) * D) + (threadIdx.x & 31) * (kVec / 2);
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i) dst[i] = pack_bf16(a[2 * i] * inv, a[2 * i + 1] * inv);
 }
 
 }  // namespace kv4

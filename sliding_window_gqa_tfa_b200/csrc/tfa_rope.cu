@@ -49,8 +49,8 @@ struct Params {
     float eps, mscale;
     int conj;   // rotate back (a gradient)
     int inter;  // pairs of neighbouring channels (2i, 2i + 1)
-    float *partial;  // gradient: [blocks][2][D]
-    int q_slots, rounds;  // gradient: slots that take query rows, rounds of a token
+    float *partial;  // gradient: [blocks][D]
+    int q_blocks;    // gradient: blocks that take query rows, the first ones
 };
 
 __device__ __forceinline__ int position(const Params &p, int b, int l) {
@@ -58,17 +58,14 @@ __device__ __forceinline__ int position(const Params &p, int b, int l) {
     return p.pos_per_row ? __ldg(p.pos + static_cast<long long>(b) * p.L + l) : __ldg(p.pos + b) + l;
 }
 
-// cos and sin (times mscale) of the rot / 2 angles of one position, by the
-// block's first threads.
-__device__ __forceinline__ void fill_table(const Params &p, int pos, float2 *tab) {
-    if (threadIdx.x < static_cast<unsigned>(p.rot >> 1)) {
-        constexpr double kInv2Pi = 0.15915494309189533577;
-        double turns = static_cast<double>(pos) * p.inv_freq[threadIdx.x] * kInv2Pi;
-        turns -= rint(turns);
-        float s, c;
-        sincospif(2.f * static_cast<float>(turns), &s, &c);
-        tab[threadIdx.x] = make_float2(c * p.mscale, (p.conj ? -s : s) * p.mscale);
-    }
+// cos and sin (times mscale) of pair i's angle at a position.
+__device__ __forceinline__ float2 angle(const Params &p, int pos, int i) {
+    constexpr double kInv2Pi = 0.15915494309189533577;
+    double turns = static_cast<double>(pos) * p.inv_freq[i] * kInv2Pi;
+    turns -= rint(turns);
+    float s, c;
+    sincospif(2.f * static_cast<float>(turns), &s, &c);
+    return make_float2(c * p.mscale, (p.conj ? -s : s) * p.mscale);
 }
 
 __device__ __forceinline__ void unpack(const uint4 &v, float (&x)[8]) {
@@ -163,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
         }
     };
     load(row0);
-    fill_table(p, position(p, b, l), tab);
+    if (threadIdx.x < static_cast<unsigned>(p.rot >> 1)) tab[threadIdx.x] = angle(p, position(p, b, l), threadIdx.x);
     float wq[8], wk[8];
     if constexpr (NORM) {
         unpack(*reinterpret_cast<const uint4 *>(p.wq + lane8 * 8), wq);
@@ -195,127 +192,159 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
     }
 }
 
-// Gradient with norms: blocks walk the tokens, so that the weights' gradients
-// gather in registers over all of a block's rows; one partial sum per block,
-// added up in block order by the second kernel (the same order every time).
-// A slot (the lanes of a row) takes query rows only or key rows only, in
-// proportion: it keeps one weight and one sum, and no selection in the loop
-// (with both in every slot the loop took 62 instructions a channel, not 20).
+// Gradient with norms: blocks walk groups of tokens, so that the weight's gradient
+// gathers in registers over all of a block's rows; one partial sum per block, added
+// up in block order by the second kernel (the same order every time).
+// A block takes query rows only or key rows only, in proportion to their heads: the
+// strides and the tensors are then the same for all its threads, and a thread keeps
+// one weight and one sum (with both kinds in a block the loop spilled and took 39
+// instructions a channel).  With few heads a round holds several tokens' rows.
+// The loads of a round are issued while the round before is computed, and the next
+// tokens' angles while these ones' rows are.
+constexpr int kMaxTokens = 4;  // tokens of a group
+
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const __grid_constant__ Params p) {
     constexpr int LPR = D / 8, kSlots = kThreads / LPR;
-    __shared__ float2 tab[2][D / 2];
+    __shared__ float2 tab[2][kMaxTokens][D / 2];
     __shared__ float red[kSlots][D + 4];
-    const int lane8 = threadIdx.x % LPR, slot = threadIdx.x / LPR;
-    const int n_tokens = p.B * p.L;
-    const int q_slots = p.q_slots;
-    const bool isq = slot < q_slots;
-    const int first = isq ? slot : slot - q_slots, step = isq ? q_slots : kSlots - q_slots;
+    const bool isq = static_cast<int>(blockIdx.x) < p.q_blocks;  // the block's kind
+    const int block = isq ? blockIdx.x : blockIdx.x - p.q_blocks;
+    const int blocks = isq ? p.q_blocks : static_cast<int>(gridDim.x) - p.q_blocks;
     const int heads = isq ? p.Hq : p.Hkv;
-    const int rounds = p.rounds;  // the block's: the larger of the two kinds'
+    const __nv_bfloat16 *xs = isq ? p.q : p.k, *gs = isq ? p.dq : p.dk;
+    __nv_bfloat16 *os = isq ? p.qo : p.ko;
     const Strides sx = isq ? p.sq : p.sk, sg = isq ? p.sdq : p.sdk, so = isq ? p.sqo : p.sko;
-    const __nv_bfloat16 *xb = (isq ? p.q : p.k) + lane8 * 8 + first * sx.h;
-    const __nv_bfloat16 *gb = (isq ? p.dq : p.dk) + lane8 * 8 + first * sg.h;
-    __nv_bfloat16 *ob = (isq ? p.qo : p.ko) + lane8 * 8 + first * so.h;
-    const long long hx = step * sx.h, hg = step * sg.h, ho = step * so.h;  // a round further
+    const int n_tokens = p.B * p.L;
+    const int per = heads < kSlots ? min(kMaxTokens, kSlots / heads) : 1;  // tokens of a group
+    const int rounds = (heads + kSlots - 1) / kSlots;
+    const int n_groups = (n_tokens + per - 1) / per;
+    const int lane8 = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+    const int sub = per > 1 ? slot / heads : 0, h0 = per > 1 ? slot - sub * heads : slot;  // (sub may be past the group)
     float w[8], acc[8];
     unpack(*reinterpret_cast<const uint4 *>((isq ? p.wq : p.wk) + lane8 * 8), w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    // The loads of a round are issued while the round before is computed, and the
-    // next token's angles while this one's rows are: with both in line the kernel
-    // waited for memory.
+    // Every thread's token moves by the same number of tokens from group to group:
+    // db sequences and dl rows, and where that leaves the sequence one more sequence
+    // and L rows back.  Pointers move by the same, without a product or a division.
+    const int stride = blocks * per, db = stride / p.L, dl = stride - db * p.L;
+    struct Place {
+        int t, b, l;
+    };
+    auto place = [&](int t) { return Place{t, t / p.L, t - t / p.L * p.L}; };
+    auto move = [&](Place &c) {  // whether it left its sequence
+        c.t += stride;
+        c.b += db;
+        c.l += dl;
+        const bool wrap = c.l >= p.L;
+        if (wrap) c.b += 1, c.l -= p.L;
+        return wrap;
+    };
+    // the angles of a group's tokens, D / 2 threads a token
+    Place at = place(block * per + threadIdx.x / (D / 2));
+    const int pair = threadIdx.x % (D / 2);
+    const bool fills = static_cast<int>(threadIdx.x) / (D / 2) < per && pair < (p.rot >> 1);
+    auto angles = [&](int buf) {
+        if (fills && at.t < n_tokens) tab[buf][threadIdx.x / (D / 2)][pair] = angle(p, position(p, at.b, at.l), pair);
+        move(at);
+    };
+    const bool has = sub < per && h0 < heads;  // the slot has a row in a group's first round
+    Place c = place(block * per + sub);
+    const __nv_bfloat16 *xp = xs + c.b * sx.b + c.l * sx.l + h0 * sx.h + lane8 * 8;
+    const __nv_bfloat16 *gp = gs + c.b * sg.b + c.l * sg.l + h0 * sg.h + lane8 * 8;
+    __nv_bfloat16 *op = os + c.b * so.b + c.l * so.l + h0 * so.h + lane8 * 8;
+    const long long mx = db * sx.b + dl * sx.l, mg = db * sg.b + dl * sg.l, mo = db * so.b + dl * so.l;
+    const long long wx = sx.b - p.L * sx.l, wg = sg.b - p.L * sg.l, wo = so.b - p.L * so.l;
     uint4 xv, gv;
-    const __nv_bfloat16 *xp, *gp;
-    auto load = [&](bool in) {
+    auto load = [&](bool in, long long x_off, long long g_off) {
         xv = gv = make_uint4(0u, 0u, 0u, 0u);
         if (in) {
-            xv = *reinterpret_cast<const uint4 *>(xp);
-            gv = *reinterpret_cast<const uint4 *>(gp);
+            xv = *reinterpret_cast<const uint4 *>(xp + x_off);
+            gv = *reinterpret_cast<const uint4 *>(gp + g_off);
         }
     };
     int which = 0;
-    int b = blockIdx.x / p.L, l = blockIdx.x - b * p.L;
-    xp = xb + b * sx.b + l * sx.l;
-    gp = gb + b * sg.b + l * sg.l;
-    load(first < heads);
-    fill_table(p, position(p, b, l), tab[0]);
+    bool live = has && c.t < n_tokens;
+    load(live, 0, 0);
+    angles(0);
     __syncthreads();
-    for (int token = blockIdx.x; token < n_tokens; token += gridDim.x, which ^= 1) {
-        __nv_bfloat16 *op = ob + b * so.b + l * so.l;
+    for (int group = block; group < n_groups; group += blocks, which ^= 1) {
         Factors<INTER> f;
-        f.load(tab[which], lane8, p.rot);
-        const int next = token + gridDim.x;
-        b = next / p.L;
-        l = next - b * p.L;
-        if (next < n_tokens) fill_table(p, position(p, b, l), tab[which ^ 1]);
-        int h = first;
-        for (int i = 0; i < rounds; ++i, h += step, op += ho) {
+        f.load(tab[which][sub < per ? sub : 0], lane8, p.rot);
+        angles(which ^ 1);
+        __nv_bfloat16 *orow = op;
+        int h = h0;
+        for (int i = 0; i < rounds; ++i, h += kSlots, orow += kSlots * so.h) {
             float x[8], g[8];
             unpack(xv, x);
             unpack(gv, g);
-            const bool in = h < heads;
+            const bool in = live;
             if (i + 1 < rounds) {
-                xp += hx;
-                gp += hg;
-                load(h + step < heads);
+                live = in && h + kSlots < heads;
+                load(live, (i + 1) * kSlots * sx.h, (i + 1) * kSlots * sg.h);
             } else {
-                xp = xb + b * sx.b + l * sx.l;
-                gp = gb + b * sg.b + l * sg.l;
-                load(next < n_tokens && first < heads);
+                const bool wrap = move(c);
+                xp += mx + (wrap ? wx : 0);
+                gp += mg + (wrap ? wg : 0);
+                op += mo + (wrap ? wo : 0);
+                live = has && c.t < n_tokens;
+                load(live, 0, 0);
             }
             f.rotate(g, lane8, p.rot);
             float ss = 0.f, dot = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
             const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+            const float rr = in ? r : 0.f;  // (a row past the last holds zeros, but eps may be 0)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float gx = g[e] * x[e];
                 dot = fmaf(gx, w[e], dot);
-                if (in) acc[e] = fmaf(gx, r, acc[e]);  // (a row past the last holds zeros, but eps may be 0)
+                acc[e] = fmaf(gx, rr, acc[e]);
             }
             dot = row_sum<LPR>(dot);
             const float m = -dot * r * r * (1.f / D);  // dx = r (w g - x r^2 mean(w g x))
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] = r * fmaf(x[e], m, g[e] * w[e]);
-            if (in) *reinterpret_cast<uint4 *>(op) = pack(g);
+            if (in) *reinterpret_cast<uint4 *>(orow) = pack(g);
         }
         __syncthreads();  // this table may be overwritten, the next one is there
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) red[slot][lane8 * 8 + e] = acc[e];
     __syncthreads();
-    if (threadIdx.x < 2 * D) {
-        const int t = threadIdx.x / D, c = threadIdx.x % D;
+    if (threadIdx.x < D) {
         float s = 0.f;
-        for (int i = t ? q_slots : 0; i < (t ? kSlots : q_slots); ++i) s += red[i][c];
-        p.partial[(static_cast<size_t>(blockIdx.x) * 2 + t) * D + c] = s;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) s += red[i][threadIdx.x];
+        p.partial[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = s;
     }
 }
 
-// dw[2][D] = sum over blocks of partial[block][2][D]: 32 columns a block, 8
-// threads a column, always in the same order.
-__global__ void __launch_bounds__(256) weight_kernel(const float *partial, int blocks, int cols, float *dwq,
+// The weights' gradients: dwq sums partial[block][D] over the first q_blocks blocks,
+// dwk over the others; 32 columns a block, 8 threads a column, always in the same order.
+__global__ void __launch_bounds__(256) weight_kernel(const float *partial, int q_blocks, int blocks, int D, float *dwq,
                                                      float *dwk) {
     __shared__ float red[8][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), s = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), s = threadIdx.x >> 5;
+    const bool isq = col < D;
+    const int c = isq ? col : col - D, end = isq ? q_blocks : blocks;
     float sum = 0.f;
-    for (int i = s; i < blocks; i += 8) sum += partial[static_cast<size_t>(i) * cols + c];
+#pragma unroll 4
+    for (int i = (isq ? 0 : q_blocks) + s; i < end; i += 8) sum += partial[static_cast<size_t>(i) * D + c];
     red[s][threadIdx.x & 31] = sum;
     __syncthreads();
     if (s == 0) {
 #pragma unroll
         for (int i = 1; i < 8; ++i) sum += red[i][threadIdx.x & 31];
-        const int half = cols >> 1;
-        if (c < half) dwq[c] = sum;
-        else dwk[c - half] = sum;
+        (isq ? dwq : dwk)[c] = sum;
     }
 }
 
 int check(const Params &p, int D) {
     if (p.Hq < 1 || p.Hkv < 1) return TFA_ERR_HEADS;
-    if (p.B < 1 || p.L < 1 || static_cast<long long>(p.B) * p.L > 0x7fffffffll - 1024 || p.Hq > (1 << 20) ||
+    if (p.B < 1 || p.L < 1 || static_cast<long long>(p.B) * p.L > (1ll << 30) || p.Hq > (1 << 20) ||
         p.Hkv > (1 << 20))
         return TFA_ERR_SHAPE;
     if (D != 64 && D != 128) return TFA_ERR_HEAD_DIM;
@@ -353,24 +382,20 @@ int launch_forward(Params &p, int D, cudaStream_t stream) {
 
 int launch_backward(Params &p, int D, float *dwq, float *dwk, cudaStream_t stream) {
     const int tokens = p.B * p.L;
-    const int blocks = tokens < kBwdBlocks ? tokens : kBwdBlocks;
-    // the split of the slots with the fewest rounds, the proportional one or a neighbour
-    const int slots = kThreads / (D / 8);
-    p.rounds = 0x7fffffff;
-    for (int n = 1; n < slots; ++n) {
-        const int a = (p.Hq + n - 1) / n, b = (p.Hkv + slots - n - 1) / (slots - n);
-        if ((a > b ? a : b) < p.rounds) {
-            p.rounds = a > b ? a : b;
-            p.q_slots = n;
-        }
-    }
+    // blocks in proportion to the heads, one of each kind at least, none without a token
+    p.q_blocks = static_cast<int>(static_cast<long long>(kBwdBlocks) * p.Hq / (p.Hq + p.Hkv));
+    p.q_blocks = p.q_blocks < 1 ? 1 : p.q_blocks > kBwdBlocks - 1 ? kBwdBlocks - 1 : p.q_blocks;
+    int k_blocks = kBwdBlocks - p.q_blocks;
+    if (p.q_blocks > tokens) p.q_blocks = tokens;
+    if (k_blocks > tokens) k_blocks = tokens;
+    const int blocks = p.q_blocks + k_blocks;
     using Kern = void (*)(Params);
     const Kern kern = D == 128 ? (p.inter ? backward_kernel<128, true> : backward_kernel<128, false>)
                                : (p.inter ? backward_kernel<64, true> : backward_kernel<64, false>);
     kern<<<blocks, kThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return report_cuda("qk_norm_rope gradient launch", e);
-    weight_kernel<<<2 * D / 32, 256, 0, stream>>>(p.partial, blocks, 2 * D, dwq, dwk);
+    weight_kernel<<<2 * D / 32, 256, 0, stream>>>(p.partial, p.q_blocks, blocks, D, dwq, dwk);
     e = cudaGetLastError();
     return e == cudaSuccess ? TFA_OK : report_cuda("norm weight gradient launch", e);
 }
@@ -419,7 +444,7 @@ extern "C" int tfa_qk_norm_rope(const void *q, const void *k, void *q_out, void 
 }
 
 extern "C" size_t tfa_qk_norm_rope_workspace(int D) {
-    return static_cast<size_t>(tfa::rope::kBwdBlocks) * 2 * (D < 0 ? 0 : D) * sizeof(float);
+    return static_cast<size_t>(tfa::rope::kBwdBlocks) * (D < 0 ? 0 : D) * sizeof(float);
 }
 
 extern "C" int tfa_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void *q, const void *k,
