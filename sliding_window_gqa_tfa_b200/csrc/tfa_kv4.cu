@@ -234,7 +234,7 @@ Cache cache_of(void *kc, void *km, void *vc, void *vm) {
 }
 
 // ------------------------------------------------------------------- decoding
-constexpr int kMaxCtas = 320;  // bounds the workspace whatever the device
+constexpr int kMaxCtas = 640;  // of NB = 1, half of it of NB = 2: bounds the workspace whatever the device
 
 template <int D, int NB>
 int launch_decode(DecodeParams &p, int sms, cudaStream_t stream) {
@@ -249,7 +249,7 @@ int launch_decode(DecodeParams &p, int sms, cudaStream_t stream) {
         if (e != cudaSuccess) return report_cuda("cudaFuncSetAttribute(kv4 decode smem)", e);
         prepared[dev].store(true, std::memory_order_release);
     }
-    const int grid = sms * C::kCtasPerSm < kMaxCtas ? sms * C::kCtasPerSm : kMaxCtas;
+    const int grid = sms * C::kCtasPerSm < kMaxCtas / NB ? sms * C::kCtasPerSm : kMaxCtas / NB;
     decode_kernel<D, NB><<<grid, 32 * kWarps, C::kSmemBytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda("kv4 decode launch", e);
     cudaLaunchConfig_t cfg = {};
@@ -334,8 +334,8 @@ extern "C" int tfa_kv4_read(const void *k_codes, const void *k_meta, const void 
 
 extern "C" size_t tfa_kv4_decode_workspace(int Hq, int Hkv, int L, int D) {
     if (Hkv < 1 || Hq < 1 || L < 1 || D < 1) return 0;
-    const int nb = static_cast<long long>(Hq / Hkv) * L <= 8 ? 1 : 2;
-    return static_cast<size_t>(2 * kMaxCtas) * 8 * nb * (D + 2) * sizeof(float);
+    // a slot of 8 rows (NB = 1; 16 and half as many CTAs for NB = 2) for each piece of a cut segment
+    return static_cast<size_t>(kMaxRounds) * kMaxCtas * 8 * (D + 2) * sizeof(float);
 }
 
 extern "C" int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_meta, const void *v_codes,
@@ -345,7 +345,7 @@ extern "C" int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_
     if (!q || !o || !lens || !workspace) return TFA_ERR_NULL;
     if (int rc = check_cache(k_codes, k_meta, v_codes, v_meta, B, Hkv, capacity, D)) return rc;
     if (Hq < 1 || Hq % Hkv != 0) return TFA_ERR_HEADS;
-    if (B > kMaxSeqs || L < 1 || L > TFA_MAX_DECODE_ROWS || static_cast<long long>(B) * Hq * L > (1ll << 30))
+    if (B > kMaxSeqs || L < 1 || L > TFA_MAX_DECODE_ROWS || static_cast<long long>(B) * Hq * L > (1ll << 26))
         return TFA_ERR_SHAPE;
     if (first < 0 || (first > 0 && window <= 0)) return TFA_ERR_WINDOW;
     if (!std::isfinite(scale)) return TFA_ERR_SCALE;

@@ -31,9 +31,12 @@
 // come straight from the codes: a lane's word of 8 codes gives four bf16 pairs,
 // in an order of channels that q is laid out in once.
 //
-// The steps of all (sequence, KV head, chunk of rows) segments are cut into equal
-// ranges, one per CTA; lengths are read on the device.  A segment that lies in
-// one CTA is finished there; the pieces of a cut one go to a workspace and are
+// A segment is a sequence's KV head and a chunk of its rows.  Lengths are read on
+// the device, where every CTA works out the same deal (Deal): longer sequences'
+// segments are cut into more pieces, about as many pieces in all as there are
+// CTAs, and a piece lies in one segment, since to start one (queries, first
+// copies, the join of its warps) costs as much as some 25 steps.  A segment in one
+// piece is finished there; the pieces of a cut one go to a workspace and are
 // joined by a second kernel (r* = max r, l* = sum 2^(r - r*) l, likewise O).
 #pragma once
 
@@ -49,9 +52,9 @@ namespace kv4 {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kStep = 32;      // positions of a warp's step
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;      // of a CTA
 constexpr int kMaxSeqs = 1024;  // sequences of a call
-constexpr int kCtaMinSteps = kWarps;  // steps that a CTA takes at least
+constexpr int kMaxRounds = 4;   // pieces of a CTA that cut segments may ask for
 
 struct DecodeParams {
     const __nv_bfloat16 *q;  // [B, Hq, L, D]
@@ -60,7 +63,7 @@ struct DecodeParams {
     const uint32_t *km, *vm;  // [B, Hkv, cap, D / 32]
     const int *lens;          // [B]
     const float *sinks;       // [Hq] or nullptr
-    float *part;              // workspace: [2 CTAs][rows (D + 2)]
+    float *part;              // workspace: [kMaxRounds CTAs][rows (D + 2)], a slot a piece
     unsigned *status;
     int B, Hq, Hkv, L, G, cap;
     int rows;                 // G L: query rows of a KV head
@@ -96,98 +99,113 @@ __device__ __forceinline__ Span span_of(const DecodeParams &p, int n) {
     return s;
 }
 
-// Where the sequences' steps lie in the order that is cut into ranges: sequence b's
-// segments (HC of them) begin at step begin(b) HC.  Up to 32 sequences are held one
-// per lane, the same in every warp, without a word to the others; more of them in
-// shared memory.  Every lane of a warp calls the members together.
-struct Order {
-    int HC, B, lane;
-    int n, steps, before;   // B <= 32: the lane's sequence, the steps before it
-    long long *pre;         // B > 32: steps before each, [B + 1]
-    long long total;        // of all sequences, for one segment each
+// How the segments are cut: each segment of a sequence of n steps into
+// k = ceil(n / T) pieces, T the least (about) for which the pieces do not pass the
+// CTAs (or a small multiple of them, if the segments do; from kMaxRounds of them on
+// nothing is cut).  Pieces are numbered by sequence, segment and place; CTA c takes
+// c, c + grid, ..  Up to 32 sequences are held one per lane, the same in every warp;
+// more in shared memory.  Every lane of a warp calls the members together.
+struct Deal {
+    int HC, B, lane;   // segments of a sequence
+    int n, k, before;  // B <= 32: the lane's sequence: length, pieces of a segment, those of the sequences before
+    int *first;        // B > 32: pieces of a segment before each sequence, [B + 1]
+    int total;         // of all sequences, for one segment each
+    float inv_t;
 
-    __device__ __forceinline__ Order(const DecodeParams &p, long long *pre_, bool report)
-        : HC(p.Hkv * p.chunks), B(p.B), lane(threadIdx.x & 31), n(0), steps(0), before(0), pre(pre_) {
+    __device__ __forceinline__ int pieces(int steps) const {
+        return steps == 0 ? 0 : max(1, static_cast<int>(ceilf(steps * inv_t)));
+    }
+    __device__ __forceinline__ Deal(const DecodeParams &p, int grid, int *shared, bool report)
+        : HC(p.Hkv * p.chunks), B(p.B), lane(threadIdx.x & 31), n(0), k(0), before(0), first(shared) {
+        int *steps_of = shared + kMaxSeqs + 1;
+        int mine = 0;
+        float all = 0.f;
+        int count = 0;
         if (B <= 32) {
             if (lane < B) n = __ldg(p.lens + lane);
             if (report && threadIdx.x < 32 && (n < 0 || n > p.cap)) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
-            steps = span_of(p, n).steps;
-            int incl = steps;
+            mine = span_of(p, n).steps;
+            count = __popc(__ballot_sync(0xffffffffu, mine > 0));
+            all = static_cast<float>(mine);
+        } else {
+            for (int b = threadIdx.x; b < B; b += blockDim.x) {
+                const int len = __ldg(p.lens + b);
+                if (report && (len < 0 || len > p.cap)) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
+                steps_of[b] = span_of(p, len).steps;
+            }
+            __syncthreads();
+            for (int b = lane; b < B; b += 32) {
+                all += static_cast<float>(steps_of[b]);
+                count += steps_of[b] > 0;
+            }
+            count = __reduce_add_sync(0xffffffffu, count);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+        const int rounds = min(kMaxRounds, max(1, (count * HC + grid - 1) / grid));
+        const int most = max(count, rounds * grid / HC);  // pieces for one segment each
+        float T = fmaxf(all / static_cast<float>(max(most, 1)), static_cast<float>(kWarps));
+        for (int tries = 0; ; ++tries) {
+            inv_t = tries < 16 ? 1.f / T : 0.f;  // (0: one piece a segment)
+            int sum = 0;
+            if (B <= 32) {
+                k = pieces(mine);
+                sum = k;
+            } else {
+                for (int b = lane; b < B; b += 32) sum += pieces(steps_of[b]);
+            }
+            total = __reduce_add_sync(0xffffffffu, sum);
+            if (total <= most) break;
+            T *= fmaxf(1.02f, static_cast<float>(total) / static_cast<float>(most));
+        }
+        if (B <= 32) {
+            int incl = k;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, incl, d);
                 if (lane >= d) incl += y;
             }
-            before = incl - steps;
-            total = __shfl_sync(0xffffffffu, incl, 31);
+            before = incl - k;
             return;
         }
-        for (int b = threadIdx.x; b < B; b += blockDim.x) {
-            const int len = __ldg(p.lens + b);
-            if (report && (len < 0 || len > p.cap)) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
-            pre[b] = span_of(p, len).steps;
-        }
-        __syncthreads();
         if (threadIdx.x < 32) {
             const int per = (B + 31) / 32, a0 = min(lane * per, B), a1 = min(a0 + per, B);
-            long long sum = 0;
-            for (int i = a0; i < a1; ++i) sum += pre[i];
-            long long incl = sum;
+            int sum = 0;
+            for (int i = a0; i < a1; ++i) sum += pieces(steps_of[i]);
+            int incl = sum;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+                const int y = __shfl_up_sync(0xffffffffu, incl, d);
                 if (lane >= d) incl += y;
             }
-            long long run = incl - sum;
+            int run = incl - sum;
             for (int i = a0; i < a1; ++i) {
-                const long long mine = pre[i];
-                pre[i] = run;
-                run += mine;
+                first[i] = run;
+                run += pieces(steps_of[i]);
             }
-            if (lane == 31) pre[B] = incl;
+            if (lane == 31) first[B] = incl;
         }
         __syncthreads();
-        total = pre[B];
     }
-    // The sequence that holds step x < total HC: the last that begins at or before it.
-    __device__ __forceinline__ int find(long long x) const {
-        if (B <= 32) {
-            const unsigned at = __ballot_sync(0xffffffffu, lane < B && static_cast<long long>(before) * HC <= x);
-            return 31 - __clz(at);
-        }
+    // The sequence that holds piece x < total HC: the last that begins at or before it.
+    __device__ __forceinline__ int find(int x) const {
+        if (B <= 32) return 31 - __clz(__ballot_sync(0xffffffffu, lane < B && before * HC <= x));
         int lo = 0, hi = B - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (pre[mid] * HC <= x) lo = mid;
+            if (first[mid] * HC <= x) lo = mid;
             else hi = mid - 1;
         }
         return lo;
     }
-    __device__ __forceinline__ long long begin(int b) const {
-        return (B <= 32 ? static_cast<long long>(__shfl_sync(0xffffffffu, before, b)) : pre[b]) * HC;
+    __device__ __forceinline__ int begin(int b) const {
+        return (B <= 32 ? __shfl_sync(0xffffffffu, before, b) : first[b]) * HC;
+    }
+    __device__ __forceinline__ int pieces_of(int b) const {
+        return B <= 32 ? __shfl_sync(0xffffffffu, k, b) : first[b + 1] - first[b];
     }
     __device__ __forceinline__ int length(const DecodeParams &p, int b) const {
         return B <= 32 ? __shfl_sync(0xffffffffu, n, b) : __ldg(p.lens + b);
-    }
-};
-
-// The ranges of W steps: `used` CTAs take q steps each, the first r of them one more.
-struct Ranges {
-    int used;
-    long long q, r;
-    __device__ __forceinline__ Ranges(long long W, int grid) {
-        used = W < static_cast<long long>(grid) * kCtaMinSteps ? static_cast<int>((W + kCtaMinSteps - 1) / kCtaMinSteps) : grid;
-        q = used ? quotient(W, used) : 0;
-        r = W - q * used;
-    }
-    __device__ __forceinline__ long long begin(int c) const { return q * c + (c < r ? c : r); }
-    __device__ __forceinline__ int cta_of(long long x) const {
-        const long long head = r * (q + 1);
-        return static_cast<int>(x < head ? quotient(x, q + 1) : r + quotient(x - head, q));
-    }
-    // (64-bit divisions take some 150 instructions)
-    __device__ __forceinline__ static long long quotient(long long a, long long b) {
-        return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b)) : a / b;
     }
 };
 
@@ -260,10 +278,16 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
     else
         asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    unsigned short v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-    return v;
+// Four 8 x 8 matrices of 16-bit words, a row's address from each lane: lane (g, t)
+// gets words 2 t, 2 t + 1 of row g (TRANS: of column g) of each.
+template <bool TRANS>
+__device__ __forceinline__ void load_matrices(uint32_t a, uint32_t (&w)[4]) {
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
 }
 
 template <int D, int NB>
@@ -271,7 +295,7 @@ struct Cfg {
     static constexpr int kGroups = D / 32;
     static constexpr int kRowBytes = D / 2, kMetaBytes = D / 8;
     static constexpr int kRows = 8 * NB;
-    static constexpr int kCtasPerSm = NB == 1 ? 2 : 1;
+    static constexpr int kCtasPerSm = NB == 1 ? 4 : 2;  // the register file
     static constexpr int kStages = (NB == 1 && D == 128) ? 2 : 4;  // what shared memory holds
     static constexpr int kHalfStage = kStep * (kRowBytes + kMetaBytes);  // K or V of a step
     static constexpr int kPipeBytes = kWarps * kStages * 2 * kHalfStage;
@@ -282,68 +306,57 @@ struct Cfg {
     static constexpr int kSlotFloats = kRows * (D + 2);
 };
 
-// Position of 16-byte chunk c of row r: rows two (D = 128) or four (D = 64) apart
-// would meet in the same banks.
+// Position of 16-byte chunk c (a group's codes) of row r: the chunks of eight rows
+// then lie in different banks.
 template <int D>
 __device__ __forceinline__ int chunk_at(int r, int c) {
     return D == 128 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1);
 }
-// Row of a 16-row tile that matrix row `s` holds: a lane's two pairs of V rows are
-// then t, t + 4 and t + 8, t + 12, whose banks differ across t.
-__device__ __forceinline__ int row_of(int s) { return (s & 8) + ((s & 7) >> 1) + 4 * (s & 1); }
 
-// Byte offsets of what a lane reads of a step, from the start of K's or V's codes
-// (steps and minima), for the first tile; rows 8 and tiles 16 rows further have the
-// same chunk order, so they lie a constant further.
-template <int D>
-struct LaneOffsets {
-    uint32_t k[D / 32];  // word t of group gr of row row_of(g)
-    uint32_t v[D / 32];  // halfword g of group gr of row t; of row t + 4 the one of group gr ^ kFlip
-    uint32_t m;          // the words of row row_of(g)
-    static constexpr int kFlip = D == 128 ? 2 : 1;
-    __device__ __forceinline__ LaneOffsets(int g, int t) {
-        const int r = row_of(g);
-#pragma unroll
-        for (int gr = 0; gr < D / 32; ++gr) {
-            k[gr] = r * (D / 2) + chunk_at<D>(r, gr) * 16 + t * 4;
-            v[gr] = t * (D / 2) + chunk_at<D>(t, gr) * 16 + g * 2;
-        }
-        m = r * (D / 8);
-    }
-};
-
-// O += P V for one 16-row tile.  SAFE: a position that a row does not see adds
-// nothing even where its step or minimum is not finite.
+// O += P V for a step's two 16-row tiles.  A group's 16 bytes are eight 16-bit words
+// of four channels each: the transposing load hands lane (g, t) word g of rows 2 t and
+// 2 t + 1, channels 32 gr + 4 g .. + 3 of two positions, as the product's A side takes
+// them.  SAFE: a position that a row does not see adds nothing even where its step or
+// minimum is not finite.
 template <int D, int NB, bool SAFE>
 __device__ __forceinline__ void add_values(float (&o)[D / 16][NB][4], float (&om)[D / 32][NB][2],
-                                           const float (&pr)[NB][4], uint32_t vcodes, uint32_t vmeta,
-                                           const LaneOffsets<D> &at) {
+                                           const float (&pr)[2][NB][4], uint32_t vcodes, uint32_t vmeta,
+                                           const uint32_t (&chunk)[D / 32], int g) {
     using C = Cfg<D, NB>;
-    uint32_t m0[C::kGroups], m1[C::kGroups];  // rows g and g + 8 of the scores' layout
-    lds_words(vmeta + at.m, m0);
-    lds_words(vmeta + at.m + 8 * C::kMetaBytes, m1);
+    uint32_t m0[2][C::kGroups], m1[2][C::kGroups];  // rows g and g + 8 of each tile
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile) {
+        lds_words(vmeta + (16 * tile + g) * C::kMetaBytes, m0[tile]);
+        lds_words(vmeta + (16 * tile + g + 8) * C::kMetaBytes, m1[tile]);
+    }
 #pragma unroll
     for (int gr = 0; gr < C::kGroups; ++gr) {
-        // codes of channels 32 gr + 4 g .. + 3 of rows t, t + 4, t + 8, t + 12
         uint32_t w[4];
+        load_matrices<true>(vcodes + chunk[gr], w);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            w[k] = lds16(vcodes + at.v[k & 1 ? gr ^ LaneOffsets<D>::kFlip : gr] + 4 * k * C::kRowBytes);
-        const uint32_t wa = __byte_perm(w[0], w[1], 0x5410), wb = __byte_perm(w[2], w[3], 0x5410);
-        const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
-        const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
-        const float s0 = __uint_as_float(m0[gr] << 16), n0 = __uint_as_float(m0[gr] & 0xffff0000u);
-        const float s1 = __uint_as_float(m1[gr] << 16), n1 = __uint_as_float(m1[gr] & 0xffff0000u);
+        for (int tile = 0; tile < 2; ++tile) {
+            const uint32_t wa = w[2 * tile], wb = w[2 * tile + 1];
+            const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
+            const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
+            const uint32_t x0 = m0[tile][gr], x1 = m1[tile][gr];
+            const float s0 = __uint_as_float(x0 << 16), n0 = __uint_as_float(x0 & 0xffff0000u);
+            const float s1 = __uint_as_float(x1 << 16), n1 = __uint_as_float(x1 & 0xffff0000u);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const float *q = pr[nb];
-            auto times = [](float a, float b) { return SAFE && a == 0.f ? 0.f : a * b; };
-            const uint32_t b[2] = {transpose8(pack_f16(times(q[0], s0), times(q[1], s0))),
-                                   transpose8(pack_f16(times(q[2], s1), times(q[3], s1)))};
-            mma(o[2 * gr][nb], a0, b);
-            mma(o[2 * gr + 1][nb], a1, b);
-            om[gr][nb][0] += times(q[0], n0) + times(q[2], n1);
-            om[gr][nb][1] += times(q[1], n0) + times(q[3], n1);
+            for (int nb = 0; nb < NB; ++nb) {
+                const float *q = pr[tile][nb];
+                auto times = [](float a, float b) { return SAFE && a == 0.f ? 0.f : a * b; };
+                const uint32_t b[2] = {transpose8(pack_f16(times(q[0], s0), times(q[1], s0))),
+                                       transpose8(pack_f16(times(q[2], s1), times(q[3], s1)))};
+                mma(o[2 * gr][nb], a0, b);
+                mma(o[2 * gr + 1][nb], a1, b);
+                if (SAFE) {
+                    om[gr][nb][0] += times(q[0], n0) + times(q[2], n1);
+                    om[gr][nb][1] += times(q[1], n0) + times(q[3], n1);
+                } else {
+                    om[gr][nb][0] = fmaf(q[2], n1, fmaf(q[0], n0, om[gr][nb][0]));
+                    om[gr][nb][1] = fmaf(q[3], n1, fmaf(q[1], n0, om[gr][nb][1]));
+                }
+            }
         }
     }
 }
@@ -352,33 +365,37 @@ template <int D, int NB>
 __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_kernel(const __grid_constant__ DecodeParams p) {
     using C = Cfg<D, NB>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long pre[kMaxSeqs + 1];
+    __shared__ int shared[2 * kMaxSeqs + 1];
     grid_dep_launch();  // the joining kernel may be set up meanwhile; it waits for this one's end
-    const Order order(p, pre, blockIdx.x == 0);
-    const long long W = order.total * order.HC;
-    const Ranges ranges(W, gridDim.x);
-    if (static_cast<int>(blockIdx.x) >= ranges.used) return;
-    const long long begin = ranges.begin(blockIdx.x), end = ranges.begin(blockIdx.x + 1);
+    const Deal deal(p, gridDim.x, shared, blockIdx.x == 0);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t pipe = smem_addr(smem) + warp * C::kStages * 2 * C::kHalfStage;
-    const LaneOffsets<D> at(g, t);
+    // where chunk gr of row `lane` lies: the address a lane gives to load_matrices
+    uint32_t chunk[C::kGroups];
+#pragma unroll
+    for (int gr = 0; gr < C::kGroups; ++gr) chunk[gr] = lane * C::kRowBytes + chunk_at<D>(lane, gr) * 16;
     // chunk `lane` of a step's codes: row lane / (chunks a row), in that row's order
     const uint32_t copy_to = (lane / (C::kRowBytes / 16)) * C::kRowBytes +
                              chunk_at<D>(lane / (C::kRowBytes / 16), lane % (C::kRowBytes / 16)) * 16;
     float *jo = reinterpret_cast<float *>(smem);                      // [warp][row][kOutStride]
     float *jm = jo + kWarps * C::kRows * C::kOutStride, *jl = jm + kWarps * C::kRows;  // [warp][row]
 
-    for (long long pos = begin; pos < end;) {
-        const int b = order.find(pos);
-        const Span sp = span_of(p, order.length(p, b));
-        const long long rel = pos - order.begin(b);
-        const int hc = static_cast<int>(Ranges::quotient(rel, sp.steps)), j0 = static_cast<int>(rel - static_cast<long long>(hc) * sp.steps);
-        const int j1 = static_cast<int>(min(static_cast<long long>(sp.steps), j0 + (end - pos)));
+    const int n_pieces = deal.total * deal.HC;
+    for (int piece = blockIdx.x; piece < n_pieces; piece += gridDim.x) {
+        const int b = deal.find(piece), cuts = deal.pieces_of(b);
+        const Span sp = span_of(p, deal.length(p, b));
+        const int rel = piece - deal.begin(b), hc = rel / cuts, place = rel - hc * cuts;
+        const int each = sp.steps / cuts, more = sp.steps - each * cuts;  // the first `more` pieces take one more
+        const int j0 = each * place + min(place, more), j1 = j0 + each + (place < more ? 1 : 0);
         const int h = hc / p.chunks, row0 = (hc - h * p.chunks) * C::kRows;
         const int n_rows = min(C::kRows, p.rows - row0);
         const size_t plane = (static_cast<size_t>(b) * p.Hkv + h) * p.cap;
         const size_t qrow = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.L + row0;
+
+        const int p0 = sp.n - p.L;  // position of the sequence's first new row
+        // the last position that has left the last row's window (-1: none)
+        const int past = p.window > 0 ? max(-1, sp.n - 1 - min(p.window, sp.n)) : -1;
 
         // copies of step j into stage st: codes in 16-byte chunks, steps and minima row by
         // row.  A lane's chunks lie 512 bytes apart on both sides (their rows' chunk
@@ -419,7 +436,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
         // the query rows as B fragments: lane (g, t) holds row g's channels 32 gr + 8 t ..
         // + 7, paired as the codes are (i, i + 4), those of odd i scaled by 2^-4 against
         // the codes' 2^4; bs: (0, sum of the group's q) of group t, split in two bf16;
-        // unit: what scores are multiplied by, for rows 2 t and 2 t + 1
+        // unit: what makes log2 scores of the products, for rows 2 t and 2 t + 1
         uint32_t bq[NB][C::kGroups][2][2], bs[NB][2];
         float unit[NB][2];
 #pragma unroll
@@ -446,7 +463,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // rho = 2^(14 - e), 2^e the power of two at or below the row's largest
             const int e = max(-86, static_cast<int>(__float_as_uint(top) >> 23) - 127);
-            const float rho = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+            const float size = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+            // a negative scale's sign goes with q, a scale of 0 makes it 0, so that the
+            // unit is positive
+            const float rho = p.scale > 0.f ? size : p.scale < 0.f ? -size : 0.f;
 #pragma unroll
             for (int gr = 0; gr < C::kGroups; ++gr) {
                 const uint32_t w[4] = {v[gr].x, v[gr].y, v[gr].z, v[gr].w};
@@ -466,12 +486,18 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
             const float head = __bfloat162float(__float2bfloat16_rn(mine));
             bs[nb][0] = pack_bf16(0.f, mine);
             bs[nb][1] = pack_bf16(0.f, mine - head);
-            const float un = 0x1p24f / rho;
+            const float un = 0x1p24f / size * (p.softcap > 0.f || p.scale == 0.f ? 1.f : fabsf(p.scale_log2));
             unit[nb][0] = __shfl_sync(0xffffffffu, un, 8 * t);
             unit[nb][1] = __shfl_sync(0xffffffffu, un, 8 * t + 4);
-            if (p.softcap == 0.f) unit[nb][0] *= p.scale_log2, unit[nb][1] *= p.scale_log2;
         }
 
+        float mul[NB][2];  // what is still to be multiplied into the scores
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mul[nb][e] = p.softcap > 0.f ? 1.f : unit[nb][e];
+        uint32_t highest = 0u;  // the largest step of V so far, as a bf16 pattern, and 2^es above it
+        float es = -40.f;
         float o[D / 16][NB][4], om[C::kGroups][NB][2], m[NB][2], l[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -499,31 +525,40 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
             here = here + kStageBytes == kPipe ? 0 : here + kStageBytes;
             const int key0 = (j < sp.fs ? j : j + sp.gap) * kStep;
 
-            // scores: [tile][nb][(row g, rows 2t, 2t + 1), (row g + 8, ..)]
+            // scores: [tile][nb][(position g, rows 2t, 2t + 1), (position g + 8, ..)]
             float sc[2][NB][4];
+            uint32_t k0[2][C::kGroups], k1[2][C::kGroups];
 #pragma unroll
             for (int tile = 0; tile < 2; ++tile) {
-                constexpr int kTileMeta = 16 * C::kMetaBytes, kTileCodes = 16 * C::kRowBytes;
-                const uint32_t ma = kmeta + at.m + tile * kTileMeta;
-                {
-                    // minima: the (s, m) word of group t as it lies there, twice
-                    const bool in = t < C::kGroups;
-                    const uint32_t x0 = in ? lds32(ma + t * 4) : 0u;
-                    const uint32_t x1 = in ? lds32(ma + t * 4 + 8 * C::kMetaBytes) : 0u;
-                    const uint32_t a[4] = {x0, x1, x0, x1};
+                lds_words(kmeta + (16 * tile + g) * C::kMetaBytes, k0[tile]);
+                lds_words(kmeta + (16 * tile + g + 8) * C::kMetaBytes, k1[tile]);
+            }
+            {
+                // minima: the (s, m) word of group t of each position as it lies there, twice
+                uint32_t x[4];
+                if constexpr (D == 128) {
+                    load_matrices<false>(kmeta + lane * C::kMetaBytes, x);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = t < C::kGroups ? lds32(kmeta + (8 * i + g) * C::kMetaBytes + t * 4) : 0u;
+                }
+#pragma unroll
+                for (int tile = 0; tile < 2; ++tile) {
+                    const uint32_t a[4] = {x[2 * tile], x[2 * tile + 1], x[2 * tile], x[2 * tile + 1]};
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) mma0_bf16(sc[tile][nb], a, bs[nb]);
                 }
-                uint32_t k0[C::kGroups], k1[C::kGroups];
-                lds_words(ma, k0);
-                lds_words(ma + 8 * C::kMetaBytes, k1);
+            }
 #pragma unroll
-                for (int gr = 0; gr < C::kGroups; ++gr) {
-                    const uint32_t w0 = lds32(kcodes + at.k[gr] + tile * kTileCodes);
-                    const uint32_t w1 = lds32(kcodes + at.k[gr] + tile * kTileCodes + 8 * C::kRowBytes);
+            for (int gr = 0; gr < C::kGroups; ++gr) {
+                uint32_t w[4];  // word t of the group of positions g, g + 8, g + 16, g + 24
+                load_matrices<false>(kcodes + chunk[gr], w);
+#pragma unroll
+                for (int tile = 0; tile < 2; ++tile) {
+                    const uint32_t w0 = w[2 * tile], w1 = w[2 * tile + 1];
                     const uint32_t a0[4] = {code_pair<0>(w0), code_pair<0>(w1), code_pair<1>(w0), code_pair<1>(w1)};
                     const uint32_t a1[4] = {code_pair<2>(w0), code_pair<2>(w1), code_pair<3>(w0), code_pair<3>(w1)};
-                    const float s0 = __uint_as_float(k0[gr] << 16), s1 = __uint_as_float(k1[gr] << 16);
+                    const float s0 = __uint_as_float(k0[tile][gr] << 16), s1 = __uint_as_float(k1[tile][gr] << 16);
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
                         float acc[4];
@@ -536,27 +571,17 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                     }
                 }
             }
-            if (p.softcap > 0.f) {
-                const float u = p.scale / p.softcap, cap2 = p.softcap * kLog2e;
+            if (p.softcap > 0.f) {  // log2 scores at once; unit is the products' own
+                const float u = fabsf(p.scale) / p.softcap, cap2 = p.softcap * kLog2e;
 #pragma unroll
                 for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) sc[tile][nb][e] = cap2 * tanhf(sc[tile][nb][e] * unit[nb][e & 1] * u);
-            } else {
-#pragma unroll
-                for (int tile = 0; tile < 2; ++tile)
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[tile][nb][e] *= unit[nb][e & 1];
             }
             // only steps at the causal edge, the tail or the window's edge hold hidden pairs
-            const int p0 = sp.n - p.L;  // position of a sequence's first new row
-            const bool edge = key0 + kStep - 1 > p0 ||
-                              (p.window > 0 && static_cast<long long>(key0) <= static_cast<long long>(sp.n) - 1 - p.window &&
-                               key0 + kStep > p.first);
+            const bool edge = key0 + kStep - 1 > p0 || (key0 <= past && key0 + kStep > p.first);
             if (edge) {
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
@@ -568,21 +593,26 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                         for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
-                                const int k = key0 + tile * 16 + row_of(g + 8 * half);
+                                const int k = key0 + tile * 16 + g + 8 * half;
                                 if (k > hi_k || (k < lo_k && k >= p.first)) sc[tile][nb][2 * half + e] = -CUDART_INF_F;
                             }
                     }
             }
 
-            // a power of two above the steps of V's rows, a row a lane
-            float es;
+            // a power of two above the steps of V's rows so far, a row a lane
             {
                 uint32_t w[C::kGroups], high = 0u;
                 lds_words(vmeta + lane * C::kMetaBytes, w);
 #pragma unroll
-                for (int gr = 0; gr < C::kGroups; ++gr) high = max(high, (w[gr] & 0x7fffu) < 0x7f80u ? w[gr] & 0x7fffu : 0u);
-                high = __reduce_max_sync(0xffffffffu, high);  // bf16 patterns: ordered like their values
-                es = static_cast<float>(min(80, max(-40, static_cast<int>(high >> 7) - 126)));  // step < 2^es
+                for (int gr = 0; gr < C::kGroups; ++gr) high = max(high, w[gr] & 0x7fffu);
+                if (__any_sync(0xffffffffu, high > highest)) {
+                    high = 0u;  // without steps that are not finite: they bound nothing
+#pragma unroll
+                    for (int gr = 0; gr < C::kGroups; ++gr)
+                        high = max(high, (w[gr] & 0x7fffu) < 0x7f80u ? w[gr] & 0x7fffu : 0u);
+                    highest = max(highest, __reduce_max_sync(0xffffffffu, high) | 0x7fu);  // bf16 patterns are ordered
+                    es = static_cast<float>(min(80, max(-40, static_cast<int>(highest >> 7) - 126)));  // step < 2^es
+                }
             }
             // the reference r of a row: moved up when 2^(score - r) 2^es would pass 2^15
             bool grow = false;
@@ -591,7 +621,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    top[nb][e] = fmaxf(fmaxf(sc[0][nb][e], sc[0][nb][2 + e]), fmaxf(sc[1][nb][e], sc[1][nb][2 + e])) + es;
+                    top[nb][e] = fmax3(sc[0][nb][e], sc[0][nb][2 + e], fmaxf(sc[1][nb][e], sc[1][nb][2 + e]));
+                    top[nb][e] = fmaf(top[nb][e], mul[nb][e], es);
                     grow |= top[nb][e] - m[nb][e] > 15.f;  // (false where both are -inf)
                 }
             if (__any_sync(0xffffffffu, grow)) {
@@ -623,18 +654,13 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                     const float mm = m[nb][e] == -CUDART_INF_F ? 0.f : m[nb][e];
 #pragma unroll
                     for (int tile = 0; tile < 2; ++tile) {
-                        sc[tile][nb][e] = ex2(sc[tile][nb][e] - mm);
-                        sc[tile][nb][2 + e] = ex2(sc[tile][nb][2 + e] - mm);
+                        sc[tile][nb][e] = ex2(fmaf(sc[tile][nb][e], mul[nb][e], -mm));
+                        sc[tile][nb][2 + e] = ex2(fmaf(sc[tile][nb][2 + e], mul[nb][e], -mm));
                         l[nb][e] += sc[tile][nb][e] + sc[tile][nb][2 + e];
                     }
                 }
-            if (edge) {
-                add_values<D, NB, true>(o, om, sc[0], vcodes, vmeta, at);
-                add_values<D, NB, true>(o, om, sc[1], vcodes + 16 * C::kRowBytes, vmeta + 16 * C::kMetaBytes, at);
-            } else {
-                add_values<D, NB, false>(o, om, sc[0], vcodes, vmeta, at);
-                add_values<D, NB, false>(o, om, sc[1], vcodes + 16 * C::kRowBytes, vmeta + 16 * C::kMetaBytes, at);
-            }
+            if (edge) add_values<D, NB, true>(o, om, sc, vcodes, vmeta, chunk, g);
+            else add_values<D, NB, false>(o, om, sc, vcodes, vmeta, chunk, g);
             __syncwarp();  // every lane has read the stage that the next copies fill
         }
         cp_wait<0>();
@@ -672,8 +698,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                 }
             }
         __syncthreads();
-        const bool whole = j0 == 0 && j1 == sp.steps;
-        float *slot = p.part + static_cast<size_t>(2 * blockIdx.x + (pos > begin ? 1 : 0)) * C::kSlotFloats;
+        float *slot = p.part + static_cast<size_t>(piece) * C::kSlotFloats;  // (only cut segments have one)
         for (int i = threadIdx.x; i < n_rows * (D / 4); i += 32 * kWarps) {
             const int row = i / (D / 4), c4 = i % (D / 4);
             float mx = -CUDART_INF_F;
@@ -690,7 +715,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                 sum = fmaf(f, jl[w * C::kRows + row], sum);
                 a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
             }
-            if (whole) {
+            if (cuts == 1) {
                 if (p.sinks && mx > -CUDART_INF_F)
                     sum += ex2(fmaf(__ldg(p.sinks + h * p.G + (row0 + row) / p.L), kLog2e, -mx));
                 const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
@@ -704,8 +729,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                 }
             }
         }
-        __syncthreads();  // before the next segment's copies
-        pos += j1 - j0;
+        __syncthreads();  // before the next piece's copies
     }
 }
 
@@ -719,34 +743,29 @@ constexpr int kJoinRows = 4;  // warps of a block
 template <int D, int NB>
 __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const __grid_constant__ DecodeParams p, int grid) {
     using C = Cfg<D, NB>;
-    __shared__ long long pre[kMaxSeqs + 1];
+    __shared__ int shared[2 * kMaxSeqs + 1];
     constexpr int kRowBlocks = C::kRows / kJoinRows, kVec = D / 32;
-    const Order order(p, pre, false);  // the lengths are the caller's: no need to wait for them
-    const int HC = order.HC;
-    const int segment = blockIdx.x / kRowBlocks, b = segment / HC, hc = segment - b * HC;
+    const Deal deal(p, grid, shared, false);  // the lengths are the caller's: no need to wait for them
+    const int segment = blockIdx.x / kRowBlocks, b = segment / deal.HC, hc = segment - b * deal.HC;
     const int h = hc / p.chunks, row0 = (hc - h * p.chunks) * C::kRows;
     const int row = (blockIdx.x % kRowBlocks) * kJoinRows + (threadIdx.x >> 5);
     const size_t qrow = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.L + row0;
-    const int steps = span_of(p, order.length(p, b)).steps;
-    const Ranges ranges(order.total * HC, grid);
-    const long long x0 = order.begin(b) + static_cast<long long>(hc) * steps;
-    const int c0 = steps ? ranges.cta_of(x0) : 0, c1 = steps ? ranges.cta_of(x0 + steps - 1) : 0;
-    const bool first_is_second = steps && ranges.begin(c0) < x0;  // c0's slot: its second piece
+    const int cuts = deal.pieces_of(b);  // 0: a sequence without a position
+    const float *slot0 = p.part + static_cast<size_t>(deal.begin(b) + hc * cuts) * C::kSlotFloats + row * D;
     grid_dep_wait();
-    if (row0 + row >= p.rows || (steps && c0 == c1)) return;  // (one CTA: finished where it was computed)
+    if (row0 + row >= p.rows || cuts == 1) return;  // (one piece: finished where it was computed)
     float mx = -CUDART_INF_F, sum = 0.f, a[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) a[i] = 0.f;
     constexpr int kBatch = 16;
-    for (int k0 = c0; k0 <= c1 && steps; k0 += kBatch) {
+    for (int k0 = 0; k0 < cuts; k0 += kBatch) {
         float mk[kBatch], lk[kBatch], v[kBatch][kVec];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int c = min(k0 + u, c1);
-            const float *s = p.part + static_cast<size_t>(2 * c + (c == c0 && first_is_second ? 1 : 0)) * C::kSlotFloats;
-            mk[u] = k0 + u <= c1 ? __ldcg(s + C::kRows * D + row) : -CUDART_INF_F;
-            lk[u] = __ldcg(s + C::kRows * (D + 1) + row);
-            const float *src = s + row * D + (threadIdx.x & 31) * kVec;
+            const float *s = slot0 + static_cast<size_t>(min(k0 + u, cuts - 1)) * C::kSlotFloats;
+            mk[u] = k0 + u < cuts ? __ldcg(s + C::kRows * D + row - row * D) : -CUDART_INF_F;
+            lk[u] = __ldcg(s + C::kRows * (D + 1) + row - row * D);
+            const float *src = s + (threadIdx.x & 31) * kVec;
             if constexpr (kVec == 4) {
                 const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
                 v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
