@@ -253,15 +253,17 @@ int launch_decode(DecodeParams &p, int sms, cudaStream_t stream) {
     decode_kernel<D, NB><<<grid, 32 * kWarps, C::kSmemBytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda("kv4 decode launch", e);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.chunks * (C::kRows / kJoinRows)));
-    cfg.blockDim = dim3(32 * kJoinRows);
+    const int rows = p.chunks > 1 ? C::kRows : p.rows;
+    const int items = p.B * p.Hkv * p.chunks * rows;
+    cfg.gridDim = dim3(static_cast<unsigned>(items < 4 * sms ? items : 4 * sms));
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, join_kernel<D, NB>, p, grid)) != cudaSuccess)
+    if ((e = cudaLaunchKernelEx(&cfg, join_kernel<D, NB>, p, grid, rows)) != cudaSuccess)
         return report_cuda("kv4 join launch", e);
     return TFA_OK;
 }

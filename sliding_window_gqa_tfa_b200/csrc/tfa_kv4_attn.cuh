@@ -397,6 +397,17 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
         // the last position that has left the last row's window (-1: none)
         const int past = p.window > 0 ? max(-1, sp.n - 1 - min(p.window, sp.n)) : -1;
 
+        // the query rows, asked for ahead of the copies that all warps ask for at once
+        uint4 qv[NB][C::kGroups];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int gr = 0; gr < C::kGroups; ++gr) {
+                qv[nb][gr] = make_uint4(0u, 0u, 0u, 0u);
+                if (8 * nb + g < n_rows)
+                    qv[nb][gr] = __ldg(reinterpret_cast<const uint4 *>(p.q + (qrow + 8 * nb + g) * D + 32 * gr + 8 * t));
+            }
+
         // copies of step j into stage st: codes in 16-byte chunks, steps and minima row by
         // row.  A lane's chunks lie 512 bytes apart on both sides (their rows' chunk
         // orders agree), so a whole step takes one address a tensor.
@@ -441,13 +452,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
         float unit[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            uint4 v[C::kGroups];
+            const uint4 (&v)[C::kGroups] = qv[nb];
             float top = 0.f, sum[C::kGroups];
 #pragma unroll
             for (int gr = 0; gr < C::kGroups; ++gr) {
-                v[gr] = make_uint4(0u, 0u, 0u, 0u);
-                if (8 * nb + g < n_rows)
-                    v[gr] = __ldg(reinterpret_cast<const uint4 *>(p.q + (qrow + 8 * nb + g) * D + 32 * gr + 8 * t));
                 const uint32_t w[4] = {v[gr].x, v[gr].y, v[gr].z, v[gr].w};
                 sum[gr] = 0.f;
 #pragma unroll
@@ -733,39 +741,32 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
     }
 }
 
-// Joins the pieces of the segments that were cut, and writes zeros for a sequence
-// without a position.  A warp takes one row of a segment, a lane D / 32 channels of
-// it; up to 16 pieces' loads are in flight together, as there may be as many pieces
-// as CTAs.  (One block for a segment's rows, eight pieces at a time and the ranges
-// divided out anew for each took 23 us for 8 segments of 37 pieces.)
-constexpr int kJoinRows = 4;  // warps of a block
+// One row of a segment, from its `cuts` pieces (0: zeros): a block's warps take every
+// fourth piece, a lane D / 32 channels; eight pieces' loads of each warp are in flight
+// together, as there may be as many pieces as CTAs (74 a segment for 8 segments).
+constexpr int kJoinWarps = 4;
+struct JoinShared {
+    float o[kJoinWarps][128], m[kJoinWarps], l[kJoinWarps];
+};
 
 template <int D, int NB>
-__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const __grid_constant__ DecodeParams p, int grid) {
+__device__ __forceinline__ void join_row(const DecodeParams &p, JoinShared &sh, const float *slot0, int cuts, int row,
+                                         int head, __nv_bfloat16 *out) {
     using C = Cfg<D, NB>;
-    __shared__ int shared[2 * kMaxSeqs + 1];
-    constexpr int kRowBlocks = C::kRows / kJoinRows, kVec = D / 32;
-    const Deal deal(p, grid, shared, false);  // the lengths are the caller's: no need to wait for them
-    const int segment = blockIdx.x / kRowBlocks, b = segment / deal.HC, hc = segment - b * deal.HC;
-    const int h = hc / p.chunks, row0 = (hc - h * p.chunks) * C::kRows;
-    const int row = (blockIdx.x % kRowBlocks) * kJoinRows + (threadIdx.x >> 5);
-    const size_t qrow = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.L + row0;
-    const int cuts = deal.pieces_of(b);  // 0: a sequence without a position
-    const float *slot0 = p.part + static_cast<size_t>(deal.begin(b) + hc * cuts) * C::kSlotFloats + row * D;
-    grid_dep_wait();
-    if (row0 + row >= p.rows || cuts == 1) return;  // (one piece: finished where it was computed)
+    constexpr int kVec = D / 32, kBatch = 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float mx = -CUDART_INF_F, sum = 0.f, a[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) a[i] = 0.f;
-    constexpr int kBatch = 16;
-    for (int k0 = 0; k0 < cuts; k0 += kBatch) {
+    for (int k0 = warp; k0 < cuts; k0 += kJoinWarps * kBatch) {
         float mk[kBatch], lk[kBatch], v[kBatch][kVec];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const float *s = slot0 + static_cast<size_t>(min(k0 + u, cuts - 1)) * C::kSlotFloats;
-            mk[u] = k0 + u < cuts ? __ldcg(s + C::kRows * D + row - row * D) : -CUDART_INF_F;
-            lk[u] = __ldcg(s + C::kRows * (D + 1) + row - row * D);
-            const float *src = s + (threadIdx.x & 31) * kVec;
+            const int k = k0 + u * kJoinWarps;
+            const float *s = slot0 + static_cast<size_t>(min(k, cuts - 1)) * C::kSlotFloats;
+            mk[u] = k < cuts ? __ldcg(s + C::kRows * D + row) : -CUDART_INF_F;
+            lk[u] = __ldcg(s + C::kRows * (D + 1) + row);
+            const float *src = s + row * D + lane * kVec;
             if constexpr (kVec == 4) {
                 const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
                 v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
@@ -791,11 +792,51 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const __grid_const
         }
         mx = mn;
     }
-    if (p.sinks && mx > -CUDART_INF_F) sum += ex2(fmaf(__ldg(p.sinks + h * p.G + (row0 + row) / p.L), kLog2e, -mx));
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + (qrow + row) * D) + (threadIdx.x & 31) * (kVec / 2);
 #pragma unroll
-    for (int i = 0; i < kVec / 2; ++i) dst[i] = pack_bf16(a[2 * i] * inv, a[2 * i + 1] * inv);
+    for (int i = 0; i < kVec; ++i) sh.o[warp][lane * kVec + i] = a[i];
+    if (lane == 0) sh.m[warp] = mx, sh.l[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+        mx = -CUDART_INF_F;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, sh.m[w]);
+        float x = 0.f, y = 0.f;
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (sh.m[w] == -CUDART_INF_F) continue;
+            const float f = ex2(sh.m[w] - mx);
+            sum = fmaf(f, sh.l[w], sum);
+            x = fmaf(f, sh.o[w][2 * threadIdx.x], x);
+            y = fmaf(f, sh.o[w][2 * threadIdx.x + 1], y);
+        }
+        if (p.sinks && mx > -CUDART_INF_F) sum += ex2(fmaf(__ldg(p.sinks + head), kLog2e, -mx));
+        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        reinterpret_cast<uint32_t *>(out)[threadIdx.x] = pack_bf16(x * inv, y * inv);
+    }
+    __syncthreads();
+}
+
+// Joins the pieces of the segments that were cut, row by row, and writes zeros for a
+// sequence without a position.  Few blocks, each working out the deal once: they can
+// be there before the main kernel ends.
+template <int D, int NB>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ DecodeParams p, int grid, int rows) {
+    using C = Cfg<D, NB>;
+    __shared__ int shared[2 * kMaxSeqs + 1];
+    __shared__ JoinShared sh;
+    const Deal deal(p, grid, shared, false);  // the lengths are the caller's: no need to wait for them
+    grid_dep_wait();
+    for (int item = blockIdx.x; item < p.B * deal.HC * rows; item += gridDim.x) {
+        const int segment = item / rows, row = item - segment * rows;
+        const int b = segment / deal.HC, hc = segment - b * deal.HC;
+        const int h = hc / p.chunks, first = (hc - h * p.chunks) * C::kRows + row;  // the row among the KV head's
+        const int cuts = deal.pieces_of(b);  // 0: a sequence without a position
+        if (first >= p.rows || cuts == 1) continue;  // (one piece: finished where it was computed)
+        const size_t at = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.L + first;
+        join_row<D, NB>(p, sh, p.part + static_cast<size_t>(deal.begin(b) + hc * cuts) * C::kSlotFloats, cuts, row,
+                        h * p.G + first / p.L, p.o + at * D);
+    }
 }
 
 }  // namespace kv4
