@@ -37,11 +37,14 @@ struct SplitScratch {
 };
 
 // Workspace of the backward pass, per (device, stream), grown on demand: the
-// recomputed forward output and per-row log-sum-exp, and delta = rowsum(dO o O).
+// recomputed forward output and per-row log-sum-exp, and delta = rowsum(dO o O);
+// with first tokens, the partial sums of the cut key tiles.
 struct BwdScratch {
     void *o = nullptr;
     float *lse = nullptr, *delta = nullptr;
     size_t rows = 0, o_bytes = 0;
+    float *part = nullptr;
+    size_t part_bytes = 0;
 };
 
 constexpr int kVariantsPerD = 30;  // forward kernel variants per head dim (variant_index)
@@ -246,8 +249,9 @@ int split_scratch(DeviceState &st, cudaStream_t stream, SplitScratch **out) {
     return TFA_OK;
 }
 
-// The backward workspace for `stream`, at least `rows` rows of D columns.
-int bwd_scratch(DeviceState &st, cudaStream_t stream, size_t rows, int D, BwdScratch **out) {
+// The backward workspace for `stream`, at least `rows` rows of D columns and
+// `part_bytes` bytes of partial sums.
+int bwd_scratch(DeviceState &st, cudaStream_t stream, size_t rows, int D, BwdScratch **out, size_t part_bytes = 0) {
     BwdScratch &bs = st.bwd[stream];
     const size_t o_bytes = rows * static_cast<size_t>(D) * 2;
     if (bs.rows < rows || bs.o_bytes < o_bytes) {
@@ -255,7 +259,9 @@ int bwd_scratch(DeviceState &st, cudaStream_t stream, size_t rows, int D, BwdScr
         cudaFree(bs.o);
         cudaFree(bs.lse);
         cudaFree(bs.delta);
-        bs = BwdScratch{};
+        bs.o = nullptr;
+        bs.lse = bs.delta = nullptr;
+        bs.rows = bs.o_bytes = 0;
         cudaError_t e = cudaMalloc(&bs.o, o_bytes);
         if (e == cudaSuccess) e = cudaMalloc(&bs.lse, rows * sizeof(float));
         if (e == cudaSuccess) e = cudaMalloc(&bs.delta, rows * sizeof(float));
@@ -263,14 +269,48 @@ int bwd_scratch(DeviceState &st, cudaStream_t stream, size_t rows, int D, BwdScr
             cudaFree(bs.o);
             cudaFree(bs.lse);
             cudaFree(bs.delta);
-            bs = BwdScratch{};
+            bs.o = nullptr;
+            bs.lse = bs.delta = nullptr;
             return cuda_fail("cudaMalloc(backward workspace)", e);
         }
         bs.rows = rows;
         bs.o_bytes = o_bytes;
     }
+    if (bs.part_bytes < part_bytes) {
+        if (int rc = refuse_under_capture(stream, "a larger backward workspace")) return rc;
+        cudaFree(bs.part);
+        bs.part = nullptr;
+        bs.part_bytes = 0;
+        const cudaError_t e = cudaMalloc(&bs.part, part_bytes);
+        if (e != cudaSuccess) return cuda_fail("cudaMalloc(backward partial sums)", e);
+        bs.part_bytes = part_bytes;
+    }
     *out = &bs;
     return TFA_OK;
+}
+
+// How the first tokens' key tiles are cut in the backward pass: into parts of about
+// as many query tiles as a key tile inside the window has.  Whole, one such tile
+// kept one CTA busy twice as long as the others (4096 rows, window 1024, 8 KV heads:
+// dK/dV 267 us, cut FIRST_CUT_US).  At most 32 parts, which bounds the workspace, and
+// no cut beyond 4 tiles: there are then enough long items to even out.
+struct FirstCut {
+    int tiles = 0, parts = 1;
+    size_t bytes(int B, int Hkv, int D) const {
+        return tiles ? static_cast<size_t>(tiles) * B * Hkv * parts * 2 * 128 * D * sizeof(float) : 0;
+    }
+};
+FirstCut first_cut(int L, int S, int window, int first) {
+    FirstCut c;
+    const int tiles = (first + tfa::kBlockK - 1) / tfa::kBlockK;
+    if (first <= 0 || tiles > 4) return c;
+    const tfa::KeyRange all = tfa::ktile_query_range(L, S, 1, 0, 0);
+    const int n = all.hi - all.lo + 1, inside = (window < L ? window : L) / tfa::kBlockQ + 1;
+    const int parts = (n + inside - 1) / inside;
+    if (parts < 2) return c;
+    c.tiles = tiles;
+    c.parts = parts < 32 ? parts : 32;
+    return c;
 }
 
 int validate(const void *q, const void *k, const void *v, const void *o, int B, int Hq, int Hkv,
@@ -718,7 +758,12 @@ int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void 
     dq_kern<<<static_cast<int>(nq_items < st.sm_count ? nq_items : st.sm_count), bw::kThreads, smem, stream>>>(
         mq, mdo, mk, mv, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail("dQ kernel launch", e);
-    const long long nk_items = static_cast<long long>(B) * Hkv * ((S + tfa::kBlockK - 1) / tfa::kBlockK);
+    const FirstCut cut = first_cut(L, S, p.window, first);
+    p.cut_tiles = cut.tiles;
+    p.parts = cut.parts;
+    p.part = bs.part;
+    const long long nk_items = static_cast<long long>(B) * Hkv *
+                               ((S + tfa::kBlockK - 1) / tfa::kBlockK + cut.tiles * (cut.parts - 1));
     p.n_items = static_cast<int>(nk_items);
     const Kern dkv_kern = first ? first_kern(true) : key_mask ? Kern(bw::dkv_kernel<D, true>) : Kern(bw::dkv_kernel<D, false>);
     // Programmatic stream serialisation: the dK/dV CTAs start on the SMs the
@@ -736,6 +781,12 @@ int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void 
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, dkv_kern, mq, mdo, mk, mv, p)) != cudaSuccess)
         return cuda_fail("dK/dV kernel launch", e);
+    if (cut.tiles) {
+        const dim3 grid(static_cast<unsigned>(B) * Hkv, (cut.tiles * 128 * (D / 4) + 255) / 256, 2);
+        reinterpret_cast<void (*)(const bw::BwdParams)>(const_cast<void *>(tfa::first_sum_parts_kernel(D)))
+            <<<grid, 256, 0, stream>>>(p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail("partial sums kernel launch", e);
+    }
     return TFA_OK;
 }
 }  // namespace
@@ -848,9 +899,10 @@ extern "C" int tfa_prefill_first_backward(const void *q, const void *k, const vo
     DeviceState *st = nullptr;
     BwdScratch *bs = nullptr;
     std::lock_guard<std::mutex> lk(g_mutex);
-    if ((rc = device_state(s, &st)) || (rc = bwd_scratch(*st, s, static_cast<size_t>(B) * Hq * L, D, &bs)))
-        return rc;
     const int f = first < S ? first : S;
+    if ((rc = device_state(s, &st)) || (rc = bwd_scratch(*st, s, static_cast<size_t>(B) * Hq * L, D, &bs,
+                                                         first_cut(L, S, window, f).bytes(B, Hkv, D))))
+        return rc;
     return (D == 128) ? backward_impl<128>(*st, nullptr, *bs, q, k, v, dout, dq, dk, dv, B, Hq, Hkv, L, S, scale, 1,
                                            window, key_mask, s, o, lse, f)
                       : backward_impl<64>(*st, nullptr, *bs, q, k, v, dout, dq, dk, dv, B, Hq, Hkv, L, S, scale, 1,

@@ -73,6 +73,12 @@ struct BwdParams {
     unsigned *status;
     int B, Hq, Hkv, L, S, G, causal, window;
     int first;  // first tokens that stay visible (kernels instantiated with FIRST)
+    // dKV kernel with FIRST: every later row sees the first tokens' key tiles, so
+    // each of the first `cut_tiles` key tiles is cut into `parts` items over its query
+    // tiles, which leave their sums (fp32, [tile][b][g][part][dK, dV][128][D]) in `part`
+    // for sum_parts_kernel; cut_tiles == 0: nothing is cut
+    int cut_tiles, parts;
+    float *part;
     float scale, scale_log2;
     int n_items;
 };
@@ -170,12 +176,23 @@ __device__ __forceinline__ QItem q_item(const BwdParams &p, int item) {
 }
 struct KItem {
     int b, g, kt, qlo, qhi, nq, steps;  // per head of the group: query tiles [qlo, qhi]
+    int part;  // with FIRST: the part of a cut key tile, else -1
 };
 template <bool FIRST>
 __device__ __forceinline__ KItem k_item(const BwdParams &p, int item) {
     const int bg = p.B * p.Hkv;
-    const int kt = item / bg, rem = item - kt * bg;
+    int kt = item / bg;
+    const int rem = item - kt * bg;
     KItem it;
+    it.part = -1;
+    if (FIRST && p.cut_tiles > 0) {  // the parts of the cut tiles come first
+        if (kt < p.cut_tiles * p.parts) {
+            it.part = kt % p.parts;
+            kt /= p.parts;
+        } else {
+            kt -= p.cut_tiles * (p.parts - 1);
+        }
+    }
     it.kt = kt;
     it.b = rem / p.Hkv;
     it.g = rem - it.b * p.Hkv;
@@ -185,8 +202,41 @@ __device__ __forceinline__ KItem k_item(const BwdParams &p, int item) {
     it.qlo = qr.lo;
     it.qhi = qr.hi;
     it.nq = qr.hi >= qr.lo ? qr.hi - qr.lo + 1 : 0;
+    if (FIRST && it.part >= 0) {
+        const int a = static_cast<int>(static_cast<long long>(it.nq) * it.part / p.parts);
+        const int e = static_cast<int>(static_cast<long long>(it.nq) * (it.part + 1) / p.parts);
+        it.qlo += a;
+        it.nq = e - a;
+        it.qhi = it.qlo + it.nq - 1;
+    }
     it.steps = it.nq * p.G;
     return it;
+}
+
+// Where part `part` of cut key tile kt keeps its dK (which = 1) or dV (0).
+template <int D>
+__device__ __forceinline__ float *part_at(const BwdParams &p, int kt, int b, int g, int part, int which) {
+    return p.part + (((static_cast<size_t>(kt) * p.B + b) * p.Hkv + g) * p.parts + part) * (2 * 128 * D) + which * 128 * D;
+}
+
+// dK and dV of the cut key tiles: their parts added up in order, four channels a
+// thread; grid: B Hkv, the cut tiles' rows in blocks, dV and dK.
+template <int D>
+__global__ void __launch_bounds__(256) sum_parts_kernel(const BwdParams p) {
+    const int i = blockIdx.y * 256 + threadIdx.x;  // over cut_tiles x 128 rows x D / 4
+    const int row = i / (D / 4), c4 = i % (D / 4), kt = row / kBlockK, key = row;
+    if (kt >= p.cut_tiles || key >= p.S) return;
+    const int b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv, which = blockIdx.z;
+    const float4 *src = reinterpret_cast<const float4 *>(part_at<D>(p, kt, b, g, 0, which) + (row % kBlockK) * D) + c4;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int j = 0; j < p.parts; ++j) {
+        const float4 x = __ldcg(src + static_cast<size_t>(j) * (2 * 128 * D / 4));
+        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    }
+    const float f = which ? p.scale : 1.f;
+    __nv_bfloat16 *dst = (which ? p.dk : p.dv) + ((static_cast<size_t>(b) * p.Hkv + g) * p.S + key) * D + 4 * c4;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(a.x * f, a.y * f), pack_bf16(a.z * f, a.w * f));
 }
 
 // Common set-up of both kernels: barriers, tensor memory, the abort flag.
@@ -719,7 +769,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (FIRST && key < p.first) q_hi = p.L - 1;
             if (!kept) q_hi = q_lo - 1;
             const size_t oidx = (static_cast<size_t>(it.b * p.Hkv + it.g) * p.S + key) * D;
-            if (it.steps == 0) {  // no row sees this key tile: zero gradients
+            if (it.steps == 0) {  // no row sees this key tile (part): zero gradients
+                if (FIRST && it.part >= 0) {
+                    for (int which = 0; which < 2; ++which) {
+                        float4 *d4 = reinterpret_cast<float4 *>(part_at<D>(p, it.kt, it.b, it.g, it.part, which) + r * D);
+                        for (int v4 = hf * (D / 8); v4 < (hf + 1) * (D / 8); ++v4) __stcg(d4 + v4, make_float4(0.f, 0.f, 0.f, 0.f));
+                    }
+                    continue;
+                }
                 if (kvalid) {
                     uint4 *dk4 = reinterpret_cast<uint4 *>(p.dk + oidx);
                     uint4 *dv4 = reinterpret_cast<uint4 *>(p.dv + oidx);
@@ -828,6 +885,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int cc = hf * (D / 64); cc < (hf + 1) * (D / 64); ++cc) {
                     uint32_t o[32];
                     tmem_ld32((which ? tD : tC) + 32 * cc, o);
+                    if (FIRST && it.part >= 0) {
+                        float4 *d4 = reinterpret_cast<float4 *>(part_at<D>(p, it.kt, it.b, it.g, it.part, which) + r * D + cc * 32);
+#pragma unroll
+                        for (int v4 = 0; v4 < 8; ++v4)
+                            __stcg(d4 + v4, make_float4(__uint_as_float(o[4 * v4]), __uint_as_float(o[4 * v4 + 1]),
+                                                        __uint_as_float(o[4 * v4 + 2]), __uint_as_float(o[4 * v4 + 3])));
+                        continue;
+                    }
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)

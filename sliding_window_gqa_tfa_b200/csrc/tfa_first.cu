@@ -32,4 +32,9 @@ const void *first_backward_kernel(int D, bool key_mask, bool keys) {
 #undef TFA_PICK
 }
 
+const void *first_sum_parts_kernel(int D) {
+    return D == 128 ? reinterpret_cast<const void *>(bwd::sum_parts_kernel<128>)
+                    : reinterpret_cast<const void *>(bwd::sum_parts_kernel<64>);
+}
+
 }  // namespace tfa

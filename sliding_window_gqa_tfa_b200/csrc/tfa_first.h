@@ -8,4 +8,7 @@ const void *first_forward_kernel(int D, bool key_mask, int mode, bool packed);
 // bwd::dq_kernel, or (keys) bwd::dkv_kernel, with first tokens.
 const void *first_backward_kernel(int D, bool key_mask, bool keys);
 
+// bwd::sum_parts_kernel.
+const void *first_sum_parts_kernel(int D);
+
 }  // namespace tfa

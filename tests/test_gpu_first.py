@@ -95,6 +95,10 @@ CASES = [
     ("first128_window128", 1, 4, 1, 256, 1024, 128, 128, 128),
     ("cut_ranges", 1, 1, 1, 260, 20000, 128, 9000, 70),
     ("many_items", 3, 16, 4, 513, 900, 64, 200, 9),
+    ("cut_key_tiles", 2, 4, 2, 1500, 1500, 128, 100, 4),
+    ("two_cut_tiles_prefix", 1, 3, 1, 1200, 4000, 64, 128, 200),
+    ("uncut_tiles", 1, 2, 1, 900, 900, 128, 100, 600),
+    ("most_parts", 1, 1, 1, 9000, 9000, 64, 1, 1),
 ]
 IDS = [c[0] for c in CASES]
 
