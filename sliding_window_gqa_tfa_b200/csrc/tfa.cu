@@ -292,7 +292,7 @@ int bwd_scratch(DeviceState &st, cudaStream_t stream, size_t rows, int D, BwdScr
 // How the first tokens' key tiles are cut in the backward pass: into parts of about
 // as many query tiles as a key tile inside the window has.  Whole, one such tile
 // kept one CTA busy twice as long as the others (4096 rows, window 1024, 8 KV heads:
-// dK/dV 267 us, cut FIRST_CUT_US).  At most 32 parts, which bounds the workspace, and
+// dK/dV 267 us, cut 181 us).  At most 32 parts, which bounds the workspace, and
 // no cut beyond 4 tiles: there are then enough long items to even out.
 struct FirstCut {
     int tiles = 0, parts = 1;
@@ -472,8 +472,13 @@ int launch(DeviceState &st, const void *q, const void *k, const void *v, void *o
     sh.first = ad.first;
     sh.n_qp = tfa::shape_n_qp(L);
     auto steps_of = [&](const tfa::Shape &x) { return first ? tfa::total_steps<true>(x) : tfa::total_steps(x); };
+    // First layout, packed: the finalizer of a cut tile merges its pack_heads L rows
+    // alone, about a step for every five (measured: 128 rows over a 1024-token window
+    // 43 us cut, 21 us whole; over 16384 tokens 80 us cut, 172 us whole).
+    const int cut_cost = tfa::kPieceCostSteps + (first && packed ? pack_heads * L / 5 : 0);
     auto makespan = [&](const tfa::Shape &x) {
-        return first ? tfa::makespan_estimate<true>(x, p.W) : tfa::makespan_estimate(x, p.W);
+        const int cost = x.split ? cut_cost : tfa::kPieceCostSteps;
+        return first ? tfa::makespan_estimate<true>(x, p.W, cost) : tfa::makespan_estimate(x, p.W);
     };
     p.W = varlen ? 0 : steps_of(sh);  // varlen: per-sequence lengths live on the device
     // Head pairs for causal calls whose items are short (at most 16 key tiles

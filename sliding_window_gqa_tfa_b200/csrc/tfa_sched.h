@@ -287,14 +287,14 @@ TFA_HD int last_contributor(long long W, int grid, int c, const Segment &seg,
 constexpr int kPieceCostSteps = 6;
 
 template <bool FIRST = false>
-inline long long makespan_estimate(Shape s, long long W) {
+inline long long makespan_estimate(Shape s, long long W, int piece_cost = kPieceCostSteps) {
     long long worst = 0;
     for (int c = 0; c < s.grid; ++c) {
         SegIterT<FIRST> it;
         it.init(s, W, c);
         Segment seg;
         long long cost = 0;
-        while (it.next(s, seg)) cost += (seg.je - seg.jb + 1) + kPieceCostSteps;
+        while (it.next(s, seg)) cost += (seg.je - seg.jb + 1) + piece_cost;
         if (cost > worst) worst = cost;
     }
     return worst;
