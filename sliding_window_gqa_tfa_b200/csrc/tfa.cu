@@ -292,7 +292,7 @@ int bwd_scratch(DeviceState &st, cudaStream_t stream, size_t rows, int D, BwdScr
 // How the first tokens' key tiles are cut in the backward pass: into parts of about
 // as many query tiles as a key tile inside the window has.  Whole, one such tile
 // kept one CTA busy twice as long as the others (4096 rows, window 1024, 8 KV heads:
-// dK/dV 267 us, cut 181 us).  At most 32 parts, which bounds the workspace, and
+// forward and gradients 508 us, cut 422 us).  At most 32 parts, which bounds the workspace, and
 // no cut beyond 4 tiles: there are then enough long items to even out.
 struct FirstCut {
     int tiles = 0, parts = 1;

@@ -538,12 +538,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int ch = 2 * hf + c2;
                     uint32_t sv[32];
                     tmem_ld32(tS + 32 * ch, sv);
+                    const int k32 = kt * kBlockK + 32 * ch;  // with FIRST: one bit a key, as in the forward
+                    const uint32_t keep = FIRST ? (~bits_below(lo_abs - k32) | bits_below(p.first - k32)) &
+                                                      bits_below(hi_abs + 1 - k32) : 0u;
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         float pe = ex2(fmaf(__uint_as_float(sv[e]), c, -lse_r));
                         if (needs) {
-                            const int k = kt * kBlockK + 32 * ch + e;
-                            const bool al = (k >= lo_abs || (FIRST && k < p.first)) && k <= hi_abs && (!KM || __ldg(km_row + k) > 0.5f);
+                            const int k = k32 + e;
+                            const bool al = (FIRST ? ((keep >> e) & 1u) != 0u : k >= lo_abs && k <= hi_abs) &&
+                                            (!KM || __ldg(km_row + k) > 0.5f);
                             pe = al ? pe : 0.f;
                         }
                         pr[32 * c2 + e] = pe;
@@ -829,9 +833,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // P^T = 2^(S^T c - lse), kept in fp32 for dS^T
                 float pt[64];
+                uint32_t keep[2];  // with FIRST: one bit a query row
+#pragma unroll
+                for (int c2 = 0; c2 < 2; ++c2)
+                    keep[c2] = FIRST ? ~bits_below(q_lo - q0 - 32 * c2) & bits_below(q_hi + 1 - q0 - 32 * c2) : 0u;
 #pragma unroll
                 for (int e = 0; e < 64; ++e) {
-                    const bool allowed = (q0 + e >= q_lo) & (q0 + e <= q_hi);
+                    const bool allowed = FIRST ? ((keep[e >> 5] >> (e & 31)) & 1u) != 0u
+                                               : (q0 + e >= q_lo) & (q0 + e <= q_hi);
                     const float ev = ex2(fmaf(__uint_as_float(sv[e]), c, stage[64 * hf + e]));
                     pt[e] = allowed ? ev : 0.f;
                 }

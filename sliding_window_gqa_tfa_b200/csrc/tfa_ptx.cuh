@@ -318,6 +318,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The n lowest bits, n clamped to [0, 32].
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    uint32_t m;
+    asm("shl.b32 %0, %1, %2;" : "=r"(m) : "r"(0xffffffffu), "r"(n > 0 ? n : 0));  // (0 from 32 on)
+    return ~m;
+}
 // Three-input maximum (one instruction on sm_100).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;
