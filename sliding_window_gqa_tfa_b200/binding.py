@@ -238,11 +238,15 @@ def tfa_plan_pieces(B, Hq, L, S, causal, window, grid, split, cta, max_pieces=40
 
 
 # ---------------------------------------------------------- torch wrapper
-def _stream_handle(stream):
-    import torch
+# the current stream's handle without the Stream object around it (3 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+
+def _stream_handle(stream):
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
 
 
 def _check(t, name, dtype, ndim):
@@ -270,6 +274,11 @@ def prefill(q, k, v, *, scale=None, causal=True, window=0, key_mask=None, out=No
     fp32 [B,S] (1 keep / 0 drop).  Raises TfaError on a nonzero status."""
     import torch
 
+    if first:
+        if debug_flags:
+            raise ValueError("debug flags apply to tfa_prefill_debug only")
+        return _prefill_first(q, k, v, scale, causal, window, first, key_mask, softcap, sinks, out, None, False,
+                              stream)[0]
     _check(q, "q", torch.bfloat16, 4)
     _check(k, "k", torch.bfloat16, 4)
     _check(v, "v", torch.bfloat16, 4)
@@ -296,21 +305,13 @@ def prefill(q, k, v, *, scale=None, causal=True, window=0, key_mask=None, out=No
             float(scale), int(bool(causal)), int(window),
             ctypes.c_void_p(key_mask.data_ptr()) if key_mask is not None else None,
             _stream_handle(stream))
-    if softcap or sinks is not None or first:
+    if softcap or sinks is not None:
         if debug_flags:
             raise ValueError("debug flags apply to tfa_prefill_debug only")
         if sinks is not None:
             _check(sinks, "sinks", torch.float32, 1)
             if sinks.shape[0] != Hq:
                 raise ValueError("sinks must hold one logit per query head")
-        if first:
-            if not causal:
-                raise ValueError("first tokens need causal attention with a window")
-            rc = lib().tfa_prefill_first(*args[:4], None, *args[4:11], int(window), int(first), args[13], float(softcap),
-                                         _ptr_or_none(sinks), args[14])
-            if rc != TFA_OK:
-                raise TfaError(rc, "tfa_prefill_first")
-            return out
         rc = tfa_attention_ex(*args[:14], float(softcap),
                               ctypes.c_void_p(sinks.data_ptr()) if sinks is not None else None,
                               args[14])
@@ -343,6 +344,8 @@ def prefill_lse(q, k, v, *, scale=None, causal=True, window=0, key_mask=None, ou
     tokens that stay visible outside a causal window."""
     import torch
 
+    if first:
+        return _prefill_first(q, k, v, scale, causal, window, first, key_mask, 0.0, None, out, lse, True, stream)
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _check(t, n, torch.bfloat16, 4)
     B, Hq, L, D = q.shape
@@ -356,29 +359,12 @@ def prefill_lse(q, k, v, *, scale=None, causal=True, window=0, key_mask=None, ou
     lse = torch.empty((B, Hq, L), dtype=torch.float32, device=q.device) if lse is None else lse
     _check(out, "out", torch.bfloat16, 4)
     _check(lse, "lse", torch.float32, 3)
-    if first:
-        if not causal:
-            raise ValueError("first tokens need causal attention with a window")
-        _check_first_shapes(key_mask, out, lse, B, Hq, L, S, D)
-        rc = lib().tfa_prefill_first(*(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v, out, lse)),
-                                     B, Hq, Hkv, L, S, D, float(scale), int(window), int(first),
-                                     _ptr_or_none(key_mask), 0.0, None, _stream_handle(stream))
-        if rc != TFA_OK:
-            raise TfaError(rc, "tfa_prefill_first")
-        return out, lse
     rc = lib().tfa_prefill_lse(*(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v, out, lse)),
                                B, Hq, Hkv, L, S, D, float(scale), int(bool(causal)), int(window),
                                _ptr_or_none(key_mask), _stream_handle(stream))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_prefill_lse")
     return out, lse
-
-
-def _check_first_shapes(key_mask, out, lse, B, Hq, L, S, D):
-    if key_mask is not None and tuple(key_mask.shape) != (B, S):
-        raise ValueError("key_mask must be [B, S]")
-    if tuple(out.shape) != (B, Hq, L, D) or tuple(lse.shape) != (B, Hq, L):
-        raise ValueError("out and lse must be [B,Hq,L,D] and [B,Hq,L]")
 
 
 def backward(q, k, v, dout, *, scale=None, causal=True, window=0, key_mask=None, out=None,
@@ -389,6 +375,10 @@ def backward(q, k, v, dout, *, scale=None, causal=True, window=0, key_mask=None,
     prefill_lse, whose result is then needed in `saved`."""
     import torch
 
+    if first:
+        if saved is None:
+            raise ValueError("the gradient with first tokens takes prefill_lse's result in `saved`")
+        return _backward_first(q, k, v, dout, scale, causal, window, first, key_mask, out, saved, stream)
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (dout, "dout")):
         _check(t, n, torch.bfloat16, 4)
     B, Hq, L, D = q.shape
@@ -411,16 +401,6 @@ def backward(q, k, v, dout, *, scale=None, causal=True, window=0, key_mask=None,
         _check(lse, "lse", torch.float32, 3)
         if tuple(o.shape) != tuple(q.shape) or tuple(lse.shape) != (B, Hq, L):
             raise ValueError("saved (o, lse) have the wrong shape")
-        if first:
-            if not causal:
-                raise ValueError("first tokens need causal attention with a window")
-            _check_first_shapes(key_mask, o, lse, B, Hq, L, S, D)
-            rc = lib().tfa_prefill_first_backward(
-                *(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v, o, lse, dout, dq, dk, dv)), B, Hq, Hkv, L, S, D,
-                float(scale), int(window), int(first), _ptr_or_none(key_mask), _stream_handle(stream))
-            if rc != TFA_OK:
-                raise TfaError(rc, "tfa_prefill_first_backward")
-            return dq, dk, dv
         rc = lib().tfa_prefill_backward_saved(
             *(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v, o, lse, dout, dq, dk, dv)),
             B, Hq, Hkv, L, S, D, float(scale), int(bool(causal)), int(window), _ptr_or_none(key_mask),
@@ -428,8 +408,6 @@ def backward(q, k, v, dout, *, scale=None, causal=True, window=0, key_mask=None,
         if rc != TFA_OK:
             raise TfaError(rc, "tfa_prefill_backward_saved")
         return dq, dk, dv
-    if first:
-        raise ValueError("the gradient with first tokens takes prefill_lse's result in `saved`")
     rc = tfa_prefill_backward(*(ctypes.c_void_p(t.data_ptr()) for t in (q, k, v, dout, dq, dk, dv)),
                               B, Hq, Hkv, L, S, D, float(scale), int(bool(causal)), int(window),
                               _ptr_or_none(key_mask), _stream_handle(stream))
@@ -554,11 +532,6 @@ def _scope(index, stream):
     return _NO_SCOPE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
-# the current stream's handle without the Stream object around it (1.5 us less a call)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                      lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
 def _check_on(t, name, dtype, ndim, index=None, rows=False):
     """Checks a CUDA tensor's type, dimensions and device (`index`, or any); rows: any
     strides, as long as the last dimension is contiguous (else all of it must be)."""
@@ -577,6 +550,83 @@ def _check_on(t, name, dtype, ndim, index=None, rows=False):
     if index is not None and t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     raise ValueError(f"{name} must have a contiguous last dimension" if rows else f"{name} must be contiguous")
+
+
+def _first_inputs(q, k, v, causal, key_mask):
+    _check_on(q, "q", _BF16, 4)
+    dev = q.get_device()
+    _check_on(k, "k", _BF16, 4, dev)
+    _check_on(v, "v", _BF16, 4, dev)
+    B, Hq, L, D = q.shape
+    kv = k.shape
+    if v.shape != kv or kv[0] != B or kv[3] != D:
+        raise ValueError("q, k and v disagree")
+    if key_mask is not None:
+        _check_on(key_mask, "key_mask", _F32, 2, dev)
+        if key_mask.shape != (B, kv[2]):
+            raise ValueError("key_mask must be [B, S]")
+    if not causal:
+        raise ValueError("first tokens need causal attention with a window")
+    return dev, (B, Hq, kv[1], L, kv[2], D)
+
+
+def _prefill_first(q, k, v, scale, causal, window, first, key_mask, softcap, sinks, out, lse, want_lse, stream):
+    """(out, lse): prefill and prefill_lse with first tokens that stay visible."""
+    dev, dims = _first_inputs(q, k, v, causal, key_mask)
+    if sinks is not None:
+        _check_on(sinks, "sinks", _F32, 1, dev)
+        if sinks.shape[0] != dims[1]:
+            raise ValueError("sinks must hold one logit per query head")
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _check_on(out, "out", _BF16, 4, dev)
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+        if lse is not None:
+            _check_on(lse, "lse", _F32, 3, dev)
+            if lse.shape != q.shape[:3]:
+                raise ValueError("lse must be [B,Hq,L]")
+        elif want_lse:
+            lse = torch.empty(q.shape[:3], dtype=_F32, device=q.device)
+        rc = (_lib or lib()).tfa_prefill_first(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+            *dims, dims[5] ** -0.5 if scale is None else scale, window, first,
+            key_mask.data_ptr() if key_mask is not None else None, softcap,
+            sinks.data_ptr() if sinks is not None else None, _raw_stream(dev))
+    if rc != TFA_OK:
+        raise TfaError(rc, "tfa_prefill_first")
+    return out, lse
+
+
+def _backward_first(q, k, v, dout, scale, causal, window, first, key_mask, out, saved, stream):
+    """(dq, dk, dv): backward with first tokens that stay visible, from saved (o, lse)."""
+    dev, dims = _first_inputs(q, k, v, causal, key_mask)
+    o, lse = saved
+    for t, n in ((dout, "dout"), (o, "o")):
+        _check_on(t, n, _BF16, 4, dev)
+        if t.shape != q.shape:
+            raise ValueError(f"{n} must have q's shape")
+    _check_on(lse, "lse", _F32, 3, dev)
+    if lse.shape != q.shape[:3]:
+        raise ValueError("lse must be [B,Hq,L]")
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        else:
+            for t, ref, n in zip(out, (q, k, v), ("dq", "dk", "dv")):
+                _check_on(t, n, _BF16, 4, dev)
+                if t.shape != ref.shape:
+                    raise ValueError(f"{n} has the wrong shape")
+        dq, dk, dv = out
+        rc = (_lib or lib()).tfa_prefill_first_backward(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), dv.data_ptr(), *dims, dims[5] ** -0.5 if scale is None else scale, window, first,
+            key_mask.data_ptr() if key_mask is not None else None, _raw_stream(dev))
+    if rc != TFA_OK:
+        raise TfaError(rc, "tfa_prefill_first_backward")
+    return dq, dk, dv
 
 
 def rope_inv_freq(rot, base=10000.0, *, scaling=None, factor=1.0, original=8192, device=None):
@@ -739,16 +789,23 @@ def kv4_cache(B, Hkv, capacity, D, device=None):
 
 def _kv4_check(k_codes, k_meta, v_codes, v_meta):
     """Checks a cache's tensors; (B, Hkv, capacity, D, device index)."""
+    try:  # the usual case in one expression
+        shape, mshape, dev = k_codes.shape, k_meta.shape, k_codes.get_device()
+        B, Hkv, cap, half = shape
+        if (k_codes.dtype is _U8 and v_codes.dtype is _U8 and k_meta.dtype is _BF16 and v_meta.dtype is _BF16
+                and dev >= 0 and v_codes.get_device() == dev and k_meta.get_device() == dev
+                and v_meta.get_device() == dev and v_codes.shape == shape and v_meta.shape == mshape
+                and mshape == (B, Hkv, cap, half >> 4, 2) and k_codes.is_contiguous() and v_codes.is_contiguous()
+                and k_meta.is_contiguous() and v_meta.is_contiguous()):
+            return B, Hkv, cap, 2 * half, dev
+    except (AttributeError, ValueError):
+        pass
     _check_on(k_codes, "k_codes", _U8, 4)
     dev = k_codes.get_device()
-    B, Hkv, cap, half = k_codes.shape
-    meta = (B, Hkv, cap, half // (KV4_GROUP // 2), 2)
     _check_on(v_codes, "v_codes", _U8, 4, dev)
     _check_on(k_meta, "k_meta", _BF16, 5, dev)
     _check_on(v_meta, "v_meta", _BF16, 5, dev)
-    if v_codes.shape != k_codes.shape or k_meta.shape != meta or v_meta.shape != meta:
-        raise ValueError("a 4-bit cache is codes [B,Hkv,capacity,D/2] and meta [B,Hkv,capacity,D/32,2], twice")
-    return B, Hkv, cap, 2 * half, dev
+    raise ValueError("a 4-bit cache is codes [B,Hkv,capacity,D/2] and meta [B,Hkv,capacity,D/32,2], twice")
 
 
 def _kv4_start(start, B, dev):
@@ -843,8 +900,9 @@ def kv4_decode(q, k_codes, k_meta, v_codes, v_meta, lens, *, scale=None, window=
     with _scope(dev, stream):
         if out is None:
             out = torch.empty_like(q)
-        workspace = _kv4_workspace(workspace, (_lib or lib()).tfa_kv4_decode_workspace(Hq, Hkv, L, D), dev, k_codes)
-        rc = (_lib or lib()).tfa_kv4_decode(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
+        L_ = _lib or lib()
+        workspace = _kv4_workspace(workspace, L_.tfa_kv4_decode_workspace(Hq, Hkv, L, D), dev, k_codes)
+        rc = L_.tfa_kv4_decode(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
                                   v_meta.data_ptr(), lens.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, cap, D,
                                   D ** -0.5 if scale is None else scale, window, first, softcap,
                                   sinks.data_ptr() if sinks is not None else None, workspace.data_ptr(),
