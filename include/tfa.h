@@ -384,16 +384,17 @@ int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_meta, const
 size_t tfa_kv4_decode_workspace(int Hq, int Hkv, int L, int D);
 
 /* tfa_kv4_prefill -- the same attention for chunks of any L >= 1 rows, every
- * sequence with S cached positions (L <= S <= capacity, else TFA_ERR_CACHE).  The
- * positions that some row sees are brought back to bf16 in the workspace, of
- * tfa_kv4_prefill_workspace(B, Hkv, L, S, D, window, first) bytes (16-byte aligned,
- * not shared by calls that overlap), and the dense kernel runs on them; scratch
- * and graph capture as for tfa_prefill. */
+ * sequence with S cached positions (L <= S <= capacity, else TFA_ERR_CACHE).  A chunk
+ * of few rows takes tfa_kv4_decode's kernel; for the others the positions that some
+ * row sees are brought back to bf16 in the workspace and the dense kernel runs on
+ * them (scratch and graph capture as for tfa_prefill).  workspace: device memory of
+ * tfa_kv4_prefill_workspace(B, Hq, Hkv, L, S, D, window, first) bytes, 16-byte
+ * aligned, not shared by calls that overlap. */
 int tfa_kv4_prefill(const void *q, const void *k_codes, const void *k_meta, const void *v_codes, const void *v_meta,
                     void *o, int B, int Hq, int Hkv, int L, int S, int capacity, int D,
                     float scale, int window, int first, float softcap, const float *sinks,
                     void *workspace, tfa_stream_t stream);
-size_t tfa_kv4_prefill_workspace(int B, int Hkv, int L, int S, int D, int window, int first);
+size_t tfa_kv4_prefill_workspace(int B, int Hq, int Hkv, int L, int S, int D, int window, int first);
 
 /* Debug flags for tfa_prefill_debug. */
 #define TFA_DEBUG_NO_TILE_SKIP  1u /* visit every key tile, even fully masked ones   */

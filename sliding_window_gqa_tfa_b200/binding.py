@@ -130,7 +130,7 @@ def lib():
             L.tfa_kv4_decode.restype = i32
             L.tfa_kv4_prefill.argtypes = [P] * 6 + [i32] * 7 + [f32, i32, i32, f32, P, P, P]
             L.tfa_kv4_prefill.restype = i32
-            L.tfa_kv4_prefill_workspace.argtypes = [i32] * 7
+            L.tfa_kv4_prefill_workspace.argtypes = [i32] * 8
             L.tfa_kv4_prefill_workspace.restype = ctypes.c_size_t
             L.tfa_kv4_decode_workspace.argtypes = [i32] * 4
             L.tfa_kv4_decode_workspace.restype = ctypes.c_size_t
@@ -924,7 +924,7 @@ def kv4_prefill(q, k_codes, k_meta, v_codes, v_meta, *, S, scale=None, window=0,
     with _scope(dev, stream):
         if out is None:
             out = torch.empty_like(q)
-        need = (_lib or lib()).tfa_kv4_prefill_workspace(B, Hkv, L, S, D, window, first)
+        need = (_lib or lib()).tfa_kv4_prefill_workspace(B, Hq, Hkv, L, S, D, window, first)
         workspace = _kv4_workspace(workspace, max(need, 16), dev, k_codes)
         rc = (_lib or lib()).tfa_kv4_prefill(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
                                    v_meta.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, S, cap, D,

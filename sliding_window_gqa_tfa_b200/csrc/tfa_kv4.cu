@@ -334,27 +334,15 @@ extern "C" int tfa_kv4_read(const void *k_codes, const void *k_meta, const void 
     return launch_read(p, blocks, D, s);
 }
 
-extern "C" size_t tfa_kv4_decode_workspace(int Hq, int Hkv, int L, int D) {
-    if (Hkv < 1 || Hq < 1 || L < 1 || D < 1) return 0;
-    // a slot of 8 rows (NB = 1; 16 and half as many CTAs for NB = 2) for each piece of a cut segment
-    return static_cast<size_t>(kMaxRounds) * kMaxCtas * 8 * (D + 2) * sizeof(float);
-}
+namespace {
 
-extern "C" int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_meta, const void *v_codes,
-                              const void *v_meta, const int *lens, void *o, int B, int Hq, int Hkv, int L,
-                              int capacity, int D, float scale, int window, int first, float softcap,
-                              const float *sinks, void *workspace, tfa_stream_t stream) {
-    if (!q || !o || !lens || !workspace) return TFA_ERR_NULL;
-    if (int rc = check_cache(k_codes, k_meta, v_codes, v_meta, B, Hkv, capacity, D)) return rc;
-    if (Hq < 1 || Hq % Hkv != 0) return TFA_ERR_HEADS;
-    if (B > kMaxSeqs || L < 1 || L > TFA_MAX_DECODE_ROWS || static_cast<long long>(B) * Hq * L > (1ll << 26))
-        return TFA_ERR_SHAPE;
-    if (first < 0 || (first > 0 && window <= 0)) return TFA_ERR_WINDOW;
-    if (!std::isfinite(scale)) return TFA_ERR_SCALE;
-    if (!std::isfinite(softcap) || softcap < 0.f || (softcap > 0.f && scale == 0.f)) return TFA_ERR_SOFTCAP;
-    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lens, 4) || !aligned(sinks, 4) || !aligned(workspace, 16))
-        return TFA_ERR_ALIGN;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+// a slot of 8 rows (NB = 1; 16 and half as many CTAs for NB = 2) for each piece of a cut segment
+size_t decode_workspace(int D) { return static_cast<size_t>(kMaxRounds) * kMaxCtas * 8 * (D + 2) * sizeof(float); }
+
+// The kernel for few rows, arguments checked: lens on the device, or `all` positions each.
+int decode(const void *q, const void *k_codes, const void *k_meta, const void *v_codes, const void *v_meta,
+           const int *lens, int all, void *o, int B, int Hq, int Hkv, int L, int capacity, int D, float scale,
+           int window, int first, float softcap, const float *sinks, void *workspace, cudaStream_t s) {
     DecodeParams p = {};
     int sms = 0;
     if (int rc = tfa::device_info(s, &p.status, &sms)) return rc;
@@ -365,6 +353,7 @@ extern "C" int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_
     p.km = static_cast<const uint32_t *>(k_meta);
     p.vm = static_cast<const uint32_t *>(v_meta);
     p.lens = lens;
+    p.all = all;
     p.sinks = sinks;
     p.part = static_cast<float *>(workspace);
     p.B = B;
@@ -383,15 +372,53 @@ extern "C" int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_
     return D == 128 ? launch_decode<128, 2>(p, sms, s) : launch_decode<64, 2>(p, sms, s);
 }
 
-extern "C" size_t tfa_kv4_prefill_workspace(int B, int Hkv, int L, int S, int D, int window, int first) {
-    if (B < 1 || Hkv < 1 || L < 1 || S < L || D < 1 || first < 0) return 0;
-    return static_cast<size_t>(B) * Hkv * seen(L, S, window, first).rows() * D * 4;
+// Whether a chunk goes to the kernel for few rows, which multiplies the codes as they
+// are but walks them once for every 16 rows of a KV head, or is unpacked for the dense
+// kernel.  Measured (D = 128, 4 or 7 query heads a KV head): up to 64 rows the first is
+// always ahead (16 x 8 KV heads, 5000 positions: 138 against 160 us; one sequence of
+// 5000: 18 against 51 us); beyond, while its own time, some 3.4e-6 us a row and
+// position, stays below the dense kernel's 40 to 60 us for merging short tiles
+// (128 rows, one sequence of 5000: 28 against 76 us; 16 sequences: 270 against 160 us).
+bool few_rows(int B, int Hq, int Hkv, int L, const Seen &sn) {
+    const long long rows = static_cast<long long>(Hq / Hkv) * L;
+    if (B > kMaxSeqs || static_cast<long long>(B) * Hq * L > (1ll << 26)) return false;
+    return rows <= 64 || (L < 128 && static_cast<double>(B) * Hkv * sn.rows() * rows <= 12e6);
 }
 
-// A chunk's products are the tensor core's to bound, so K and V are brought back
-// to bf16 once, next to which they would be read by every query tile, and the
-// dense kernel runs on them.  Only positions that some row sees are brought back;
-// leaving the others out shifts rows and window alike.
+}  // namespace
+
+extern "C" size_t tfa_kv4_decode_workspace(int Hq, int Hkv, int L, int D) {
+    return Hkv < 1 || Hq < 1 || L < 1 || D < 1 ? 0 : decode_workspace(D);
+}
+
+extern "C" int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_meta, const void *v_codes,
+                              const void *v_meta, const int *lens, void *o, int B, int Hq, int Hkv, int L,
+                              int capacity, int D, float scale, int window, int first, float softcap,
+                              const float *sinks, void *workspace, tfa_stream_t stream) {
+    if (!q || !o || !lens || !workspace) return TFA_ERR_NULL;
+    if (int rc = check_cache(k_codes, k_meta, v_codes, v_meta, B, Hkv, capacity, D)) return rc;
+    if (Hq < 1 || Hq % Hkv != 0) return TFA_ERR_HEADS;
+    if (B > kMaxSeqs || L < 1 || L > TFA_MAX_DECODE_ROWS || static_cast<long long>(B) * Hq * L > (1ll << 26))
+        return TFA_ERR_SHAPE;
+    if (first < 0 || (first > 0 && window <= 0)) return TFA_ERR_WINDOW;
+    if (!std::isfinite(scale)) return TFA_ERR_SCALE;
+    if (!std::isfinite(softcap) || softcap < 0.f || (softcap > 0.f && scale == 0.f)) return TFA_ERR_SOFTCAP;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lens, 4) || !aligned(sinks, 4) || !aligned(workspace, 16))
+        return TFA_ERR_ALIGN;
+    return decode(q, k_codes, k_meta, v_codes, v_meta, lens, 0, o, B, Hq, Hkv, L, capacity, D, scale, window, first,
+                  softcap, sinks, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t tfa_kv4_prefill_workspace(int B, int Hq, int Hkv, int L, int S, int D, int window, int first) {
+    if (B < 1 || Hkv < 1 || Hq < 1 || L < 1 || S < L || D < 1 || first < 0) return 0;
+    const Seen sn = seen(L, S, window, first);
+    return few_rows(B, Hq, Hkv, L, sn) ? decode_workspace(D) : static_cast<size_t>(B) * Hkv * sn.rows() * D * 4;
+}
+
+// A long chunk's products are the tensor core's to bound, so K and V are brought back
+// to bf16 once (a rounding of each value, as a bf16 cache has), next to which they would
+// be read by every query tile, and the dense kernel runs on them.  Only positions that
+// some row sees are brought back; leaving the others out shifts rows and window alike.
 extern "C" int tfa_kv4_prefill(const void *q, const void *k_codes, const void *k_meta, const void *v_codes,
                                const void *v_meta, void *o, int B, int Hq, int Hkv, int L, int S, int capacity, int D,
                                float scale, int window, int first, float softcap, const float *sinks, void *workspace,
@@ -406,6 +433,9 @@ extern "C" int tfa_kv4_prefill(const void *q, const void *k_codes, const void *k
     if (!std::isfinite(softcap) || softcap < 0.f || (softcap > 0.f && scale == 0.f)) return TFA_ERR_SOFTCAP;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(sinks, 4) || !aligned(workspace, 16)) return TFA_ERR_ALIGN;
     const Seen sn = seen(L, S, window, first);
+    if (few_rows(B, Hq, Hkv, L, sn))
+        return decode(q, k_codes, k_meta, v_codes, v_meta, nullptr, S, o, B, Hq, Hkv, L, capacity, D, scale, window, first,
+                      softcap, sinks, workspace, reinterpret_cast<cudaStream_t>(stream));
     const int rows = static_cast<int>(sn.rows());
     const long long all = static_cast<long long>(B) * Hkv * rows;
     const unsigned blocks = row_blocks(all, D);

@@ -1,4 +1,4 @@
-// tfa_kv4_attn.cuh -- decoding attention over the 4-bit cache.
+// tfa_kv4_attn.cuh -- attention of few rows over the 4-bit cache.
 //
 // For a query row q of a KV group and cached position j, with s and m the step
 // and minimum of a group of 32 channels and c its codes:
@@ -61,7 +61,8 @@ struct DecodeParams {
     __nv_bfloat16 *o;        // [B, Hq, L, D]
     const uint8_t *kc, *vc;  // [B, Hkv, cap, D / 2]
     const uint32_t *km, *vm;  // [B, Hkv, cap, D / 32]
-    const int *lens;          // [B]
+    const int *lens;          // [B], or nullptr: `all` positions each
+    int all;
     const float *sinks;       // [Hq] or nullptr
     float *part;              // workspace: [kMaxRounds CTAs][rows (D + 2)], a slot a piece
     unsigned *status;
@@ -122,14 +123,14 @@ struct Deal {
         float all = 0.f;
         int count = 0;
         if (B <= 32) {
-            if (lane < B) n = __ldg(p.lens + lane);
+            if (lane < B) n = p.lens ? __ldg(p.lens + lane) : p.all;
             if (report && threadIdx.x < 32 && (n < 0 || n > p.cap)) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
             mine = span_of(p, n).steps;
             count = __popc(__ballot_sync(0xffffffffu, mine > 0));
             all = static_cast<float>(mine);
         } else {
             for (int b = threadIdx.x; b < B; b += blockDim.x) {
-                const int len = __ldg(p.lens + b);
+                const int len = p.lens ? __ldg(p.lens + b) : p.all;
                 if (report && (len < 0 || len > p.cap)) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
                 steps_of[b] = span_of(p, len).steps;
             }
@@ -205,7 +206,7 @@ struct Deal {
         return B <= 32 ? __shfl_sync(0xffffffffu, k, b) : first[b + 1] - first[b];
     }
     __device__ __forceinline__ int length(const DecodeParams &p, int b) const {
-        return B <= 32 ? __shfl_sync(0xffffffffu, n, b) : __ldg(p.lens + b);
+        return B <= 32 ? __shfl_sync(0xffffffffu, n, b) : p.lens ? __ldg(p.lens + b) : p.all;
     }
 };
 

@@ -367,6 +367,8 @@ PREFILL = [
     (1, 4, 1, 300, 700, 128, 700, 128, 600),
     (3, 4, 4, 5, 2000, 128, 2048, 1024, 64),
     (1, 2, 1, 40, 500, 64, 500, 2 ** 31 - 1, 9),
+    (40, 2, 2, 3, 70, 64, 77, 0, 0),
+    (40, 8, 2, 130, 200, 64, 210, 50, 4),
 ]
 
 
@@ -401,7 +403,7 @@ def test_prefill(c):
 def test_prefill_is_the_dense_attention_of_the_values_read_back():
     gen = _gen(21)
     cache = cache_of(_randn(gen, 2, 2, 600, 128).bfloat16(), _randn(gen, 2, 2, 600, 128).bfloat16(), 640)
-    q = _randn(gen, 2, 8, 50, 128).bfloat16()
+    q = _randn(gen, 2, 8, 130, 128).bfloat16()
     k, v = tb.kv4_read(*cache, rows=600)
     sinks = _randn(gen, 8)
     a = dict(softcap=20.0, sinks=sinks)
@@ -437,10 +439,27 @@ def test_a_chunk_then_decoding():
 def test_prefill_workspace_is_used_within_its_size():
     gen = _gen(23)
     cache = cache_of(_randn(gen, 1, 2, 400, 64).bfloat16(), _randn(gen, 1, 2, 400, 64).bfloat16(), 400)
-    q = _randn(gen, 1, 4, 20, 64).bfloat16()
-    need = tb.lib().tfa_kv4_prefill_workspace(1, 2, 20, 400, 64, 30, 4)
-    ws = torch.full((need + 64,), 77, dtype=torch.uint8, device="cuda")
-    got = tb.kv4_prefill(q, *cache, S=400, window=30, first=4, workspace=ws)
-    assert torch.equal(got, tb.kv4_prefill(q, *cache, S=400, window=30, first=4)) and (ws[need:] == 77).all()
+    for L in (20, 200):  # few rows, and many
+        q = _randn(gen, 1, 4, L, 64).bfloat16()
+        need = tb.lib().tfa_kv4_prefill_workspace(1, 4, 2, L, 400, 64, 30, 4)
+        ws = torch.full((need + 64,), 77, dtype=torch.uint8, device="cuda")
+        got = tb.kv4_prefill(q, *cache, S=400, window=30, first=4, workspace=ws)
+        assert torch.equal(got, tb.kv4_prefill(q, *cache, S=400, window=30, first=4)) and (ws[need:] == 77).all()
     with pytest.raises(ValueError):
         tb.kv4_prefill(q, *cache, S=400, workspace=ws)
+
+
+def test_few_rows_and_many_agree():
+    """Chunks on both sides of the border between the two kernels: the same rows."""
+    gen = _gen(24)
+    cache = cache_of(_randn(gen, 1, 2, 900, 128).bfloat16(), _randn(gen, 1, 2, 900, 128).bfloat16(), 900)
+    q = _randn(gen, 1, 8, 200, 128).bfloat16()
+    whole = tb.kv4_prefill(q, *cache, S=900, window=300, first=3)
+    n = torch.tensor([900], dtype=torch.int32, device="cuda")
+    for L in (1, 8, 33, 127):
+        part = tb.kv4_prefill(q[:, :, -L:].contiguous(), *cache, S=900, window=300, first=3)
+        ref, bound = reference(q[:, :, -L:], cache, [900], 128 ** -0.5, 300, 3)
+        assert ((part.double() - ref).abs() <= bound).all()
+        assert ((part.double() - whole[:, :, -L:].double()).abs() <= 2 ** -5 * (1 + ref.abs())).all()
+        if L <= 8:
+            assert torch.equal(part, tb.kv4_decode(q[:, :, -L:].contiguous(), *cache, n, window=300, first=3))

@@ -210,18 +210,23 @@ def _chunk(**over):
     (dict(softcap=float("nan")), tb.TFA_ERR_SOFTCAP),
     (dict(q=MIS), tb.TFA_ERR_ALIGN),
     (dict(ws=MIS), tb.TFA_ERR_ALIGN),
-    (dict(B=1 << 10, Hkv=1 << 10, Hq=1 << 10, L=1, S=1 << 20, cap=1 << 20), tb.TFA_ERR_SHAPE),
+    (dict(B=1 << 10, Hkv=1 << 10, Hq=1 << 10, L=200, S=1 << 20, cap=1 << 20), tb.TFA_ERR_SHAPE),
 ])
 def test_kv4_prefill_refusals(over, code):
     assert _chunk(**over) == code
 
 
 def test_kv4_workspaces():
-    size = tb.lib().tfa_kv4_prefill_workspace
-    assert size(2, 4, 10, 100, 128, 0, 0) == 2 * 4 * 100 * 128 * 4
-    assert size(2, 4, 10, 100, 64, 20, 5) == 2 * 4 * (5 + 29) * 64 * 4
-    assert size(1, 1, 10, 100, 64, 20, 71) == 100 * 64 * 4  # the first tokens meet the window
-    assert size(1, 1, 10, 9, 64, 20, 0) == 0
-    assert size(1, 1, 10, 100, 64, 2 ** 31 - 1, 2 ** 31 - 1) == 100 * 64 * 4
+    size, few = tb.lib().tfa_kv4_prefill_workspace, tb.lib().tfa_kv4_decode_workspace(8, 2, 1, 128)
+    assert size(2, 16, 4, 200, 1000, 128, 0, 0) == 2 * 4 * 1000 * 128 * 4
+    assert size(2, 16, 4, 200, 1000, 64, 20, 5) == 2 * 4 * (5 + 219) * 64 * 4
+    assert size(1, 4, 1, 200, 1000, 64, 20, 781) == 1000 * 64 * 4  # the first tokens meet the window
+    assert size(1, 4, 1, 200, 1000, 64, 2 ** 31 - 1, 2 ** 31 - 1) == 1000 * 64 * 4
+    assert size(1, 1, 1, 10, 9, 64, 20, 0) == 0
+    # few rows: the kernel of tfa_kv4_decode and its pieces
+    assert size(64, 32, 8, 16, 5000, 128, 0, 0) == few
+    assert size(1, 32, 8, 32, 5000, 128, 0, 0) == few
+    assert size(16, 32, 8, 32, 5000, 128, 0, 0) == 16 * 8 * 5000 * 128 * 4
+    assert size(2000, 8, 8, 1, 10, 128, 0, 0) == 2000 * 8 * 10 * 128 * 4  # more sequences than it takes
     assert tb.lib().tfa_kv4_decode_workspace(8, 2, 1, 128) == 4 * 640 * 8 * 130 * 4
     assert tb.lib().tfa_kv4_decode_workspace(8, 0, 1, 128) == 0
