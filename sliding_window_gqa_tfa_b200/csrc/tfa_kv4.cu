@@ -236,21 +236,21 @@ Cache cache_of(void *kc, void *km, void *vc, void *vm) {
 // ------------------------------------------------------------------- decoding
 constexpr int kMaxCtas = 640;  // of NB = 1, half of it of NB = 2: bounds the workspace whatever the device
 
-template <int D, int NB>
+template <int D, int NB, int REP>
 int launch_decode(DecodeParams &p, int sms, cudaStream_t stream) {
-    using C = Cfg<D, NB>;
+    using C = Cfg<D, NB, REP>;
     p.chunks = (p.rows + C::kRows - 1) / C::kRows;
     static std::atomic<bool> prepared[kMaxDevices];  // the attribute holds for one device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return report_cuda("cudaGetDevice", e);
     if (!prepared[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(decode_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        e = cudaFuncSetAttribute(decode_kernel<D, NB, REP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
         if (e != cudaSuccess) return report_cuda("cudaFuncSetAttribute(kv4 decode smem)", e);
         prepared[dev].store(true, std::memory_order_release);
     }
     const int grid = sms * C::kCtasPerSm < kMaxCtas / NB ? sms * C::kCtasPerSm : kMaxCtas / NB;
-    decode_kernel<D, NB><<<grid, 32 * kWarps, C::kSmemBytes, stream>>>(p);
+    decode_kernel<D, NB, REP><<<grid, 32 * kWarps, C::kSmemBytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda("kv4 decode launch", e);
     cudaLaunchConfig_t cfg = {};
     const int rows = p.chunks > 1 ? C::kRows : p.rows;
@@ -368,8 +368,14 @@ int decode(const void *q, const void *k_codes, const void *k_meta, const void *v
     p.scale = scale;
     p.scale_log2 = scale * kLog2e;
     p.softcap = softcap;
-    if (p.rows <= 8) return D == 128 ? launch_decode<128, 1>(p, sms, s) : launch_decode<64, 1>(p, sms, s);
-    return D == 128 ? launch_decode<128, 2>(p, sms, s) : launch_decode<64, 2>(p, sms, s);
+    if (D == 128)
+        return p.rows <= 2   ? launch_decode<128, 1, 4>(p, sms, s)
+               : p.rows <= 4 ? launch_decode<128, 1, 2>(p, sms, s)
+               : p.rows <= 8 ? launch_decode<128, 1, 1>(p, sms, s)
+                             : launch_decode<128, 2, 1>(p, sms, s);
+    return p.rows <= 4   ? launch_decode<64, 1, 2>(p, sms, s)
+           : p.rows <= 8 ? launch_decode<64, 1, 1>(p, sms, s)
+                         : launch_decode<64, 2, 1>(p, sms, s);
 }
 
 // Whether a chunk goes to the kernel for few rows, which multiplies the codes as they

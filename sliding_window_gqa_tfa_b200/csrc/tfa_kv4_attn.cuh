@@ -291,8 +291,16 @@ __device__ __forceinline__ void load_matrices(uint32_t a, uint32_t (&w)[4]) {
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
 }
 
-template <int D, int NB>
+// NB: blocks of 8 columns (query rows).  REP (NB = 1): with at most 8 / REP rows the
+// columns hold REP copies of them, copy c for the groups g = c (mod REP): p times a
+// step is then taken once for all of a product's columns, not once for each group
+// (at REP = 4 a fifth of the instructions: 16 sequences of 2 rows 31 -> 27.7 us).
+template <int D, int NB, int REP = 1>
 struct Cfg {
+    static_assert(NB == 1 || REP == 1, "copies fill one block of columns");
+    static constexpr int kCols = 8 / REP;             // columns of a copy
+    static constexpr int kParts = (D / 32) / REP;     // groups of a copy
+
     static constexpr int kGroups = D / 32;
     static constexpr int kRowBytes = D / 2, kMetaBytes = D / 8;
     static constexpr int kRows = 8 * NB;
@@ -317,60 +325,83 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
 // O += P V for a step's two 16-row tiles.  A group's 16 bytes are eight 16-bit words
 // of four channels each: the transposing load hands lane (g, t) word g of rows 2 t and
 // 2 t + 1, channels 32 gr + 4 g .. + 3 of two positions, as the product's A side takes
-// them.  SAFE: a position that a row does not see adds nothing even where its step or
+// them.  copy: of the lane's columns 2 t and 2 t + 1; part f of it is group f REP + copy.
+// SAFE: a position that a row does not see adds nothing even where its step or
 // minimum is not finite.
-template <int D, int NB, bool SAFE>
-__device__ __forceinline__ void add_values(float (&o)[D / 16][NB][4], float (&om)[D / 32][NB][2],
+template <int D, int NB, int REP, bool SAFE>
+__device__ __forceinline__ void add_values(float (&o)[D / 16][NB][4], float (&om)[D / 32 / REP][NB][2],
                                            const float (&pr)[2][NB][4], uint32_t vcodes, uint32_t vmeta,
-                                           const uint32_t (&chunk)[D / 32], int g) {
-    using C = Cfg<D, NB>;
-    uint32_t m0[2][C::kGroups], m1[2][C::kGroups];  // rows g and g + 8 of each tile
+                                           const uint32_t (&chunk)[D / 32], int g, int copy) {
+    using C = Cfg<D, NB, REP>;
+    uint32_t m0[2][C::kParts], m1[2][C::kParts];  // rows g and g + 8 of each tile
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
-        lds_words(vmeta + (16 * tile + g) * C::kMetaBytes, m0[tile]);
-        lds_words(vmeta + (16 * tile + g + 8) * C::kMetaBytes, m1[tile]);
+        const uint32_t row = vmeta + (16 * tile + g) * C::kMetaBytes;
+        if constexpr (REP == 1) {
+            lds_words(row, m0[tile]);
+            lds_words(row + 8 * C::kMetaBytes, m1[tile]);
+        } else {
+#pragma unroll
+            for (int f = 0; f < C::kParts; ++f) {
+                m0[tile][f] = lds32(row + (f * REP + copy) * 4);
+                m1[tile][f] = lds32(row + 8 * C::kMetaBytes + (f * REP + copy) * 4);
+            }
+        }
     }
 #pragma unroll
-    for (int gr = 0; gr < C::kGroups; ++gr) {
-        uint32_t w[4];
-        load_matrices<true>(vcodes + chunk[gr], w);
+    for (int f = 0; f < C::kParts; ++f) {
+        uint32_t b[2][NB][2];
 #pragma unroll
         for (int tile = 0; tile < 2; ++tile) {
-            const uint32_t wa = w[2 * tile], wb = w[2 * tile + 1];
-            const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
-            const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
-            const uint32_t x0 = m0[tile][gr], x1 = m1[tile][gr];
+            const uint32_t x0 = m0[tile][f], x1 = m1[tile][f];
             const float s0 = __uint_as_float(x0 << 16), n0 = __uint_as_float(x0 & 0xffff0000u);
             const float s1 = __uint_as_float(x1 << 16), n1 = __uint_as_float(x1 & 0xffff0000u);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const float *q = pr[tile][nb];
                 auto times = [](float a, float b) { return SAFE && a == 0.f ? 0.f : a * b; };
-                const uint32_t b[2] = {transpose8(pack_f16(times(q[0], s0), times(q[1], s0))),
-                                       transpose8(pack_f16(times(q[2], s1), times(q[3], s1)))};
-                mma(o[2 * gr][nb], a0, b);
-                mma(o[2 * gr + 1][nb], a1, b);
+                b[tile][nb][0] = transpose8(pack_f16(times(q[0], s0), times(q[1], s0)));
+                b[tile][nb][1] = transpose8(pack_f16(times(q[2], s1), times(q[3], s1)));
                 if (SAFE) {
-                    om[gr][nb][0] += times(q[0], n0) + times(q[2], n1);
-                    om[gr][nb][1] += times(q[1], n0) + times(q[3], n1);
+                    om[f][nb][0] += times(q[0], n0) + times(q[2], n1);
+                    om[f][nb][1] += times(q[1], n0) + times(q[3], n1);
                 } else {
-                    om[gr][nb][0] = fmaf(q[2], n1, fmaf(q[0], n0, om[gr][nb][0]));
-                    om[gr][nb][1] = fmaf(q[3], n1, fmaf(q[1], n0, om[gr][nb][1]));
+                    om[f][nb][0] = fmaf(q[2], n1, fmaf(q[0], n0, om[f][nb][0]));
+                    om[f][nb][1] = fmaf(q[3], n1, fmaf(q[1], n0, om[f][nb][1]));
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < REP; ++c) {
+            const int gr = f * REP + c;
+            uint32_t w[4];
+            load_matrices<true>(vcodes + chunk[gr], w);
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                const uint32_t wa = w[2 * tile], wb = w[2 * tile + 1];
+                const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
+                const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    mma(o[2 * gr][nb], a0, b[tile][nb]);
+                    mma(o[2 * gr + 1][nb], a1, b[tile][nb]);
                 }
             }
         }
     }
 }
 
-template <int D, int NB>
-__global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_kernel(const __grid_constant__ DecodeParams p) {
-    using C = Cfg<D, NB>;
+template <int D, int NB, int REP>
+__global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB, REP>::kCtasPerSm)
+    decode_kernel(const __grid_constant__ DecodeParams p) {
+    using C = Cfg<D, NB, REP>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int shared[2 * kMaxSeqs + 1];
     grid_dep_launch();  // the joining kernel may be set up meanwhile; it waits for this one's end
     const Deal deal(p, gridDim.x, shared, blockIdx.x == 0);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int copy = 2 * t / C::kCols;  // of the lane's columns 2 t and 2 t + 1
     const uint32_t pipe = smem_addr(smem) + warp * C::kStages * 2 * C::kHalfStage;
     // where chunk gr of row `lane` lies: the address a lane gives to load_matrices
     uint32_t chunk[C::kGroups];
@@ -405,8 +436,9 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
 #pragma unroll
             for (int gr = 0; gr < C::kGroups; ++gr) {
                 qv[nb][gr] = make_uint4(0u, 0u, 0u, 0u);
-                if (8 * nb + g < n_rows)
-                    qv[nb][gr] = __ldg(reinterpret_cast<const uint4 *>(p.q + (qrow + 8 * nb + g) * D + 32 * gr + 8 * t));
+                const int row = 8 * nb + g % C::kCols;
+                if (row < n_rows)
+                    qv[nb][gr] = __ldg(reinterpret_cast<const uint4 *>(p.q + (qrow + row) * D + 32 * gr + 8 * t));
             }
 
         // copies of step j into stage st: codes in 16-byte chunks, steps and minima row by
@@ -507,7 +539,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
             for (int e = 0; e < 2; ++e) mul[nb][e] = p.softcap > 0.f ? 1.f : unit[nb][e];
         uint32_t highest = 0u;  // the largest step of V so far, as a bf16 pattern, and 2^es above it
         float es = -40.f;
-        float o[D / 16][NB][4], om[C::kGroups][NB][2], m[NB][2], l[NB][2];
+        float o[D / 16][NB][4], om[C::kParts][NB][2], m[NB][2], l[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -515,7 +547,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][nb][e] = 0.f;
 #pragma unroll
-            for (int gr = 0; gr < C::kGroups; ++gr) om[gr][nb][0] = om[gr][nb][1] = 0.f;
+            for (int f = 0; f < C::kParts; ++f) om[f][nb][0] = om[f][nb][1] = 0.f;
             m[nb][0] = m[nb][1] = -CUDART_INF_F;
             l[nb][0] = l[nb][1] = 0.f;
         }
@@ -596,7 +628,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int hi_k = p0 + (row0 + 8 * nb + 2 * t + e) % p.L;
+                        const int hi_k = p0 + (row0 + 8 * nb + (2 * t + e) % C::kCols) % p.L;
                         const long long lo_k = p.window > 0 ? static_cast<long long>(hi_k) - p.window + 1 : 0;
 #pragma unroll
                         for (int tile = 0; tile < 2; ++tile)
@@ -653,7 +685,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                             o[i][nb][2 + e] *= f;
                         }
 #pragma unroll
-                        for (int gr = 0; gr < C::kGroups; ++gr) om[gr][nb][e] *= f;
+                        for (int i = 0; i < C::kParts; ++i) om[i][nb][e] *= f;
                     }
             }
 #pragma unroll
@@ -668,8 +700,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                         l[nb][e] += sc[tile][nb][e] + sc[tile][nb][2 + e];
                     }
                 }
-            if (edge) add_values<D, NB, true>(o, om, sc, vcodes, vmeta, chunk, g);
-            else add_values<D, NB, false>(o, om, sc, vcodes, vmeta, chunk, g);
+            if (edge) add_values<D, NB, REP, true>(o, om, sc, vcodes, vmeta, chunk, g, copy);
+            else add_values<D, NB, REP, false>(o, om, sc, vcodes, vmeta, chunk, g, copy);
             __syncwarp();  // every lane has read the stage that the next copies fill
         }
         cp_wait<0>();
@@ -683,29 +715,41 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB>::kCtasPerSm) decode_ke
                 for (int x = 4; x < 32; x <<= 1) {
                     l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], x);
 #pragma unroll
-                    for (int gr = 0; gr < C::kGroups; ++gr)
-                        om[gr][nb][e] += __shfl_xor_sync(0xffffffffu, om[gr][nb][e], x);
+                    for (int f = 0; f < C::kParts; ++f) om[f][nb][e] += __shfl_xor_sync(0xffffffffu, om[f][nb][e], x);
                 }
             }
         __syncthreads();  // every warp's copies have landed and been read
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int f = 0; f < C::kParts; ++f) {
+            // the lane's columns hold its copy's group of part f
+            float x[NB][8];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = 8 * nb + 2 * t + e;
-                float *dst = jo + (warp * C::kRows + row) * C::kOutStride;
+            for (int c = 0; c < REP; ++c)
+                if (REP == 1 || copy == c) {
 #pragma unroll
-                for (int gr = 0; gr < C::kGroups; ++gr)
-                    *reinterpret_cast<float4 *>(dst + 32 * gr + 4 * g) =  // out of the codes' units
-                        make_float4(fmaf(o[2 * gr][nb][e], 0x1p24f, om[gr][nb][e]),
-                                    fmaf(o[2 * gr][nb][2 + e], 0x1p20f, om[gr][nb][e]),
-                                    fmaf(o[2 * gr + 1][nb][e], 0x1p24f, om[gr][nb][e]),
-                                    fmaf(o[2 * gr + 1][nb][2 + e], 0x1p20f, om[gr][nb][e]));
-                if (g == 0) {
-                    jm[warp * C::kRows + row] = m[nb][e];
-                    jl[warp * C::kRows + row] = l[nb][e];
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[nb][e] = o[2 * (f * REP + c)][nb][e];
+                            x[nb][4 + e] = o[2 * (f * REP + c) + 1][nb][e];
+                        }
                 }
-            }
+            const int gr = f * REP + (REP == 1 ? 0 : copy);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = 8 * nb + (2 * t + e) % C::kCols;
+                    *reinterpret_cast<float4 *>(jo + (warp * C::kRows + row) * C::kOutStride + 32 * gr + 4 * g) =
+                        make_float4(fmaf(x[nb][e], 0x1p24f, om[f][nb][e]), fmaf(x[nb][2 + e], 0x1p20f, om[f][nb][e]),
+                                    fmaf(x[nb][4 + e], 0x1p24f, om[f][nb][e]),
+                                    fmaf(x[nb][6 + e], 0x1p20f, om[f][nb][e]));  // out of the codes' units
+                    if (f == 0 && g == 0 && copy == 0) {
+                        jm[warp * C::kRows + row] = m[nb][e];
+                        jl[warp * C::kRows + row] = l[nb][e];
+                    }
+                }
+        }
         __syncthreads();
         float *slot = p.part + static_cast<size_t>(piece) * C::kSlotFloats;  // (only cut segments have one)
         for (int i = threadIdx.x; i < n_rows * (D / 4); i += 32 * kWarps) {

@@ -204,6 +204,14 @@ CASES = [
     ("first_past_window", 2, 4, 2, 2, 128, 400, [400, 150], 33, 300),
     ("window_past_all", 1, 4, 2, 2, 128, 100, [100], 2 ** 31 - 1, 7),
     ("first33", 1, 7, 1, 8, 64, 900, [900], 128, 33),
+    # one to four rows of a KV head: copies in the products' columns
+    ("rows1", 2, 3, 3, 1, 128, 700, [700, 40], 0, 0),
+    ("rows2_window", 3, 4, 2, 1, 128, 900, [900, 33, 5], 70, 3),
+    ("rows2_l2", 1, 2, 2, 2, 128, 300, [300], 0, 0),
+    ("rows3", 2, 6, 2, 1, 128, 500, [500, 100], 0, 0),
+    ("rows4_l4", 2, 2, 2, 4, 128, 400, [400, 3], 50, 7),
+    ("rows1_d64", 1, 2, 2, 1, 64, 400, [399], 0, 0),
+    ("rows3_l3_d64", 2, 2, 2, 3, 64, 400, [399, 2], 20, 1),
 ]
 
 
