@@ -529,7 +529,10 @@ def _scope(index, stream):
         if stream.device.index != index:
             raise ValueError("stream belongs to another device than the tensors")
         return torch.cuda.stream(stream)
-    return _NO_SCOPE if index == torch.cuda.current_device() else torch.cuda.device(index)
+    return _NO_SCOPE if index == _current_device() else torch.cuda.device(index)
+
+
+_current_device = torch.cuda.current_device
 
 
 def _check_on(t, name, dtype, ndim, index=None, rows=False):
@@ -656,32 +659,35 @@ def rope_inv_freq(rot, base=10000.0, *, scaling=None, factor=1.0, original=8192,
 
 
 def _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight):
-    """Checks shared by the pass and its gradient; the C call's middle arguments."""
+    """Checks shared by the pass and its gradient; (device index, the C call's middle
+    arguments, its sizes)."""
+    _check_on(q, "q", _BF16, 4, rows=True)
     dev = q.get_device()
     _check_on(k, "k", _BF16, 4, dev, rows=True)
     B, L, Hq, D = q.shape
-    if k.shape[0] != B or k.shape[1] != L or k.shape[3] != D:
+    Bk, Lk, Hkv, Dk = k.shape
+    if Bk != B or Lk != L or Dk != D:
         raise ValueError("q and k disagree on batch, tokens or head dimension")
     _check_on(inv_freq, "inv_freq", _F64, 1, dev)
-    if (q_weight is None) != (k_weight is None):
+    wq = wk = None
+    if q_weight is not None and k_weight is not None:
+        _check_on(q_weight, "q_weight", _BF16, 1, dev)
+        _check_on(k_weight, "k_weight", _BF16, 1, dev)
+        if q_weight.shape[0] != D or k_weight.shape[0] != D:
+            raise ValueError("q_weight and k_weight must hold one weight per channel")
+        wq, wk = q_weight.data_ptr(), k_weight.data_ptr()
+    elif q_weight is not k_weight:
         raise ValueError("q_weight and k_weight must be given together")
-    if q_weight is not None:
-        for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            _check_on(t, n, _BF16, 1, dev)
-            if t.shape[0] != D:
-                raise ValueError(f"{n} must hold one weight per channel")
     per_row, first, ptr = 0, 0, None
     if isinstance(positions, int):
         first = positions
     else:
-        _check_on(positions, "positions", _I32, positions.dim() if isinstance(positions, torch.Tensor) else 1, dev)
-        per_row = int(positions.dim() == 2)
-        if tuple(positions.shape) != ((B, L) if per_row else (B,)):
+        per_row = 1 if isinstance(positions, torch.Tensor) and positions.dim() == 2 else 0
+        _check_on(positions, "positions", _I32, 1 + per_row, dev)
+        if positions.shape != ((B, L) if per_row else (B,)):
             raise ValueError("positions must be an int, [B] or [B, L]")
         ptr = positions.data_ptr()
-    return (q_weight.data_ptr() if q_weight is not None else None,
-            k_weight.data_ptr() if k_weight is not None else None, inv_freq.data_ptr(), ptr, per_row,
-            first), (B, L, Hq, k.shape[2], D, 2 * inv_freq.shape[0])
+    return dev, (wq, wk, inv_freq.data_ptr(), ptr, per_row, first), (B, L, Hq, Hkv, D, 2 * inv_freq.shape[0])
 
 
 _PACK6, _PACK12, _PACK18 = (struct.Struct(f"{n}q").pack for n in (6, 12, 18))
@@ -715,10 +721,8 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     an int.  inv_freq: fp64 [rot/2] on the device (rope_inv_freq), rot a multiple of
     16 up to D, the other channels pass through.  q_out and k_out may be views, e.g.
     a key cache's rows, in [B,H,L,D] order.  Raises TfaError on a nonzero status."""
-    _check_on(q, "q", _BF16, 4, rows=True)
-    mid, dims = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight)
+    dev, mid, dims = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight)
     B, L, Hq, Hkv, D, rot = dims
-    dev = q.get_device()
     with _scope(dev, stream):
         if q_out is None:
             q_out = q.new_empty((B, Hq, L, D))
@@ -728,9 +732,11 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
             k_out = k.new_empty((B, Hkv, L, D))
         else:
             _check_rows(k_out, "k_out", (B, Hkv, L, D), dev)
+        (qb, ql, qh, _), (kb, kl, kh, _) = q.stride(), k.stride()
+        (ob, oh, ol, _), (pb, ph, pl, _) = q_out.stride(), k_out.stride()
         rc = (_lib or lib()).tfa_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-            _PACK12(*_tokens(q), *_tokens(k), *_heads(q_out), *_heads(k_out)), *mid, *dims, interleaved, eps, mscale,
+            _PACK12(qb, ql, qh, kb, kl, kh, ob, ol, oh, pb, pl, ph), *mid, *dims, interleaved, eps, mscale,
             _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_qk_norm_rope")
@@ -743,10 +749,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
     dq_out [B,Hq,L,D] and dk_out [B,Hkv,L,D] (bf16, any strides with contiguous
     channels).  dq [B,L,Hq,D] and dk [B,L,Hkv,D] are bf16 (views in `out` are fine);
     the weights' are fp32 [D], None without weights."""
-    _check_on(q, "q", _BF16, 4, rows=True)
-    mid, dims = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight)
+    dev, mid, dims = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight)
     B, L, Hq, Hkv, D, rot = dims
-    dev = q.get_device()
     _check_rows(dq_out, "dq_out", (B, Hq, L, D), dev)
     _check_rows(dk_out, "dk_out", (B, Hkv, L, D), dev)
     with _scope(dev, stream):
@@ -825,13 +829,15 @@ def kv4_append(k, v, k_codes, k_meta, v_codes, v_meta, *, start, stream=None):
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
     _check_on(k, "k", _BF16, 4, dev, rows=True)
     _check_on(v, "v", _BF16, 4, dev, rows=True)
-    if k.shape != v.shape or k.shape[0] != B or k.shape[1] != Hkv or k.shape[3] != D:
+    L = k.shape[2]
+    if k.shape != (B, Hkv, L, D) or v.shape != (B, Hkv, L, D):
         raise ValueError("k and v must be [B,Hkv,L,D] of the cache's B, Hkv and D")
     ptr, first = _kv4_start(start, B, dev)
-    strides = _PACK6(*k.stride()[:3], *v.stride()[:3])
+    (kb, kh, kl, _), (vb, vh, vl, _) = k.stride(), v.stride()
+    strides = _PACK6(kb, kh, kl, vb, vh, vl)
     with _scope(dev, stream):
         rc = (_lib or lib()).tfa_kv4_append(k.data_ptr(), v.data_ptr(), strides, k_codes.data_ptr(), k_meta.data_ptr(),
-                                  v_codes.data_ptr(), v_meta.data_ptr(), ptr, first, B, Hkv, k.shape[2], cap, D,
+                                  v_codes.data_ptr(), v_meta.data_ptr(), ptr, first, B, Hkv, L, cap, D,
                                   _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_kv4_append")
