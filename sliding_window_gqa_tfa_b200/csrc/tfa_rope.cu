@@ -25,6 +25,7 @@
 
 #include "../../include/tfa.h"
 #include "tfa_internal.h"
+#include "tfa_ptx.cuh"
 
 namespace tfa {
 namespace rope {
@@ -58,14 +59,38 @@ __device__ __forceinline__ int position(const Params &p, int b, int l) {
     return p.pos_per_row ? __ldg(p.pos + static_cast<long long>(b) * p.L + l) : __ldg(p.pos + b) + l;
 }
 
-// cos and sin (times mscale) of pair i's angle at a position.
-__device__ __forceinline__ float2 angle(const Params &p, int pos, int i) {
+// What the channels of a position are multiplied by: each by its own c, its partner by
+// its own s (minus the sine for a pair's first channel); channels past rot by 1 and 0.
+// A lane's 8 channels lie as two float4, the lanes' first ones side by side, so that a
+// row's lanes read different banks.
+template <int D>
+struct Table {
+    float c[D], s[D];
+    __device__ __forceinline__ static int at(int channel) {
+        return ((channel >> 2) & 1) * (D / 2) + (channel >> 3) * 4 + (channel & 3);
+    }
+};
+
+// Pair i's angle at a position, into its two channels.
+template <int D>
+__device__ __forceinline__ void angle(const Params &p, int pos, int i, Table<D> &tab) {
     constexpr double kInv2Pi = 0.15915494309189533577;
     double turns = static_cast<double>(pos) * p.inv_freq[i] * kInv2Pi;
     turns -= rint(turns);
     float s, c;
     sincospif(2.f * static_cast<float>(turns), &s, &c);
-    return make_float2(c * p.mscale, (p.conj ? -s : s) * p.mscale);
+    c *= p.mscale;
+    s *= p.conj ? -p.mscale : p.mscale;
+    const int a = p.inter ? 2 * i : i, b = p.inter ? 2 * i + 1 : i + (p.rot >> 1);
+    tab.c[Table<D>::at(a)] = tab.c[Table<D>::at(b)] = c;
+    tab.s[Table<D>::at(a)] = -s;
+    tab.s[Table<D>::at(b)] = s;
+}
+// The channels that pass through.
+template <int D>
+__device__ __forceinline__ void pass_through(const Params &p, Table<D> &tab) {
+    const int i = p.rot + threadIdx.x;
+    if (i < D) tab.c[Table<D>::at(i)] = 1.f, tab.s[Table<D>::at(i)] = 0.f;
 }
 
 __device__ __forceinline__ void unpack(const uint4 &v, float (&x)[8]) {
@@ -84,48 +109,45 @@ __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The lane's cos / sin factors: half layout, 8 pairs; interleaved, 4.
-template <bool INTER>
+// The lane's 8 channels' factors; interleaved, one cosine and sine a pair.
+template <int D, bool INTER>
 struct Factors {
     float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
-    __device__ __forceinline__ void load(const float2 *tab, int lane8, int rot) {
-        const int half = rot >> 4;  // lanes of a half (half layout)
-        if (lane8 * 8 >= rot) {
+    __device__ __forceinline__ void load(const Table<D> &tab, int lane8) {
 #pragma unroll
-            for (int e = 0; e < (INTER ? 4 : 8); ++e) c[e] = 1.f, s[e] = 0.f;
-            return;
-        }
-        const int i0 = INTER ? lane8 * 4 : (lane8 < half ? lane8 : lane8 - half) * 8;
-#pragma unroll
-        for (int e = 0; e < (INTER ? 4 : 8); ++e) {
-            const float2 t = tab[i0 + e];
-            c[e] = t.x;
-            // the first of a pair takes - sin, the second + sin
-            s[e] = INTER ? t.y : (lane8 < half ? -t.y : t.y);
+        for (int i = 0; i < 2; ++i) {
+            const float4 x = *reinterpret_cast<const float4 *>(tab.c + i * (D / 2) + lane8 * 4);
+            const float4 y = *reinterpret_cast<const float4 *>(tab.s + i * (D / 2) + lane8 * 4);
+            if constexpr (INTER) {
+                c[2 * i] = x.x, c[2 * i + 1] = x.z;
+                s[2 * i] = y.y, s[2 * i + 1] = y.w;
+            } else {
+                c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
+                s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = y.z, s[4 * i + 3] = y.w;
+            }
         }
     }
     // Rotates the lane's 8 channels; every lane of the warp calls it (the half
-    // layout's partners sit rot / 16 lanes away).
-    __device__ __forceinline__ void rotate(float (&y)[8], int lane8, int rot) const {
-        if constexpr (INTER) {
+    // layout's partners sit in another lane: partner).
+    __device__ __forceinline__ void rotate(float (&y)[8], int partner) const {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < (INTER ? 4 : 8); ++e) {
+            if constexpr (INTER) {
                 const float a = y[2 * e], b = y[2 * e + 1];
                 y[2 * e] = fmaf(a, c[e], -b * s[e]);
                 y[2 * e + 1] = fmaf(b, c[e], a * s[e]);
-            }
-        } else {
-            const int half = rot >> 4;
-            const int lane = threadIdx.x & 31;
-            const int partner = lane8 * 8 >= rot ? lane : (lane8 < half ? lane + half : lane - half);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            } else {
                 const float o = __shfl_sync(0xffffffffu, y[e], partner);
                 y[e] = fmaf(y[e], c[e], o * s[e]);
             }
         }
     }
 };
+// The half layout's partner lane: rot / 16 lanes away, in the same row.
+__device__ __forceinline__ int partner_lane(int lane8, int rot) {
+    const int half = rot >> 4, lane = threadIdx.x & 31;
+    return lane8 * 8 >= rot ? lane : (lane8 < half ? lane + half : lane - half);
+}
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -135,9 +157,9 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 template <int D, bool NORM, bool INTER>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 3) forward_kernel(const __grid_constant__ Params p) {
     constexpr int LPR = D / 8, kSlots = kThreads / LPR;
-    __shared__ float2 tab[D / 2];
+    __shared__ __align__(16) Table<D> tab;
     const int token = blockIdx.x, b = token / p.L, l = token - b * p.L;
     const int lane8 = threadIdx.x % LPR, slot = threadIdx.x / LPR;
     const int n_rows = p.Hq + p.Hkv;
@@ -160,15 +182,17 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
         }
     };
     load(row0);
-    if (threadIdx.x < static_cast<unsigned>(p.rot >> 1)) tab[threadIdx.x] = angle(p, position(p, b, l), threadIdx.x);
+    if (threadIdx.x < static_cast<unsigned>(p.rot >> 1)) angle(p, position(p, b, l), threadIdx.x, tab);
+    pass_through(p, tab);
     float wq[8], wk[8];
     if constexpr (NORM) {
         unpack(*reinterpret_cast<const uint4 *>(p.wq + lane8 * 8), wq);
         unpack(*reinterpret_cast<const uint4 *>(p.wk + lane8 * 8), wk);
     }
     __syncthreads();
-    Factors<INTER> f;
-    f.load(tab, lane8, p.rot);
+    Factors<D, INTER> f;
+    f.load(tab, lane8);
+    const int partner = partner_lane(lane8, p.rot);
     for (int base = row0; base < row1; base += kAhead * kSlots) {
         if (base > row0) load(base);
 #pragma unroll
@@ -185,113 +209,138 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] *= r * (row < p.Hq ? wq[e] : wk[e]);
             }
-            f.rotate(y, lane8, p.rot);
+            f.rotate(y, partner);
             if (row < row1)
                 *reinterpret_cast<uint4 *>(row < p.Hq ? qo + row * p.sqo.h : ko + (row - p.Hq) * p.sko.h) = pack(y);
         }
     }
 }
 
-// Gradient with norms: blocks walk groups of tokens, so that the weight's gradient
-// gathers in registers over all of a block's rows; one partial sum per block, added
+// Gradient with norms: a block walks its own run of tokens, so that the weight's
+// gradient gathers in registers over all of its rows; one partial sum per block, added
 // up in block order by the second kernel (the same order every time).
 // A block takes query rows only or key rows only, in proportion to their heads: the
 // strides and the tensors are then the same for all its threads, and a thread keeps
 // one weight and one sum (with both kinds in a block the loop spilled and took 39
-// instructions a channel).  With few heads a round holds several tokens' rows.
-// The loads of a round are issued while the round before is computed, and the next
-// tokens' angles while these ones' rows are.
-constexpr int kMaxTokens = 4;  // tokens of a group
+// instructions a channel).  The run's rows, token by token and head by head, are dealt
+// to the slots (the lanes of a row) in turn; a slot's pointers move from row to row by
+// constant strides.  The next row's loads are issued while a row is computed, and the
+// angles of the next four tokens while these four's rows are, by all threads, between
+// two barriers (a barrier and a fourth of the threads for each token: 50 us for 4 x
+// 2047 tokens of 24 heads, this way BWD_US us; the 151 MB would take 23).
+constexpr int kTokens = 4;  // of a table
 
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const __grid_constant__ Params p) {
     constexpr int LPR = D / 8, kSlots = kThreads / LPR;
-    __shared__ float2 tab[2][kMaxTokens][D / 2];
+    __shared__ __align__(16) Table<D> tab[2][kTokens];
     __shared__ float red[kSlots][D + 4];
     const bool isq = static_cast<int>(blockIdx.x) < p.q_blocks;  // the block's kind
     const int block = isq ? blockIdx.x : blockIdx.x - p.q_blocks;
     const int blocks = isq ? p.q_blocks : static_cast<int>(gridDim.x) - p.q_blocks;
     const int heads = isq ? p.Hq : p.Hkv;
-    const __nv_bfloat16 *xs = isq ? p.q : p.k, *gs = isq ? p.dq : p.dk;
-    __nv_bfloat16 *os = isq ? p.qo : p.ko;
     const Strides sx = isq ? p.sq : p.sk, sg = isq ? p.sdq : p.sdk, so = isq ? p.sqo : p.sko;
     const int n_tokens = p.B * p.L;
-    const int per = heads < kSlots ? min(kMaxTokens, kSlots / heads) : 1;  // tokens of a group
-    const int rounds = (heads + kSlots - 1) / kSlots;
-    const int n_groups = (n_tokens + per - 1) / per;
+    const int t0 = static_cast<int>(static_cast<long long>(n_tokens) * block / blocks);
+    const int t1 = static_cast<int>(static_cast<long long>(n_tokens) * (block + 1) / blocks);
     const int lane8 = threadIdx.x % LPR, slot = threadIdx.x / LPR;
-    const int sub = per > 1 ? slot / heads : 0, h0 = per > 1 ? slot - sub * heads : slot;  // (sub may be past the group)
+    const int partner = partner_lane(lane8, p.rot);
     float w[8], acc[8];
     unpack(*reinterpret_cast<const uint4 *>((isq ? p.wq : p.wk) + lane8 * 8), w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    // Every thread's token moves by the same number of tokens from group to group:
-    // db sequences and dl rows, and where that leaves the sequence one more sequence
-    // and L rows back.  Pointers move by the same, without a product or a division.
-    const int stride = blocks * per, db = stride / p.L, dl = stride - db * p.L;
-    struct Place {
-        int t, b, l;
-    };
-    auto place = [&](int t) { return Place{t, t / p.L, t - t / p.L * p.L}; };
-    auto move = [&](Place &c) {  // whether it left its sequence
-        c.t += stride;
-        c.b += db;
-        c.l += dl;
-        const bool wrap = c.l >= p.L;
-        if (wrap) c.b += 1, c.l -= p.L;
-        return wrap;
-    };
-    // the angles of a group's tokens, D / 2 threads a token
-    Place at = place(block * per + threadIdx.x / (D / 2));
-    const int pair = threadIdx.x % (D / 2);
-    const bool fills = static_cast<int>(threadIdx.x) / (D / 2) < per && pair < (p.rot >> 1);
-    auto angles = [&](int buf) {
-        if (fills && at.t < n_tokens) tab[buf][threadIdx.x / (D / 2)][pair] = angle(p, position(p, at.b, at.l), pair);
-        move(at);
-    };
-    const bool has = sub < per && h0 < heads;  // the slot has a row in a group's first round
-    Place c = place(block * per + sub);
-    const __nv_bfloat16 *xp = xs + c.b * sx.b + c.l * sx.l + h0 * sx.h + lane8 * 8;
-    const __nv_bfloat16 *gp = gs + c.b * sg.b + c.l * sg.l + h0 * sg.h + lane8 * 8;
-    __nv_bfloat16 *op = os + c.b * so.b + c.l * so.l + h0 * so.h + lane8 * 8;
-    const long long mx = db * sx.b + dl * sx.l, mg = db * sg.b + dl * sg.l, mo = db * so.b + dl * so.l;
-    const long long wx = sx.b - p.L * sx.l, wg = sg.b - p.L * sg.l, wo = so.b - p.L * so.l;
-    uint4 xv, gv;
-    auto load = [&](bool in, long long x_off, long long g_off) {
-        xv = gv = make_uint4(0u, 0u, 0u, 0u);
-        if (in) {
-            xv = *reinterpret_cast<const uint4 *>(xp + x_off);
-            gv = *reinterpret_cast<const uint4 *>(gp + g_off);
+
+    // a table's angles: D / 2 threads a token, kThreads / (D / 2) tokens at a time
+    auto angles = [&](int first, int buf) {
+#pragma unroll
+        for (int k = 0; k < kTokens; k += kThreads / (D / 2)) {
+            const int sub = k + threadIdx.x / (D / 2), i = threadIdx.x % (D / 2), t = first + sub;
+            if (sub < kTokens && t < t1 && i < (p.rot >> 1)) angle(p, position(p, t / p.L, t % p.L), i, tab[buf][sub]);
         }
     };
-    int which = 0;
-    bool live = has && c.t < n_tokens;
-    load(live, 0, 0);
-    angles(0);
+    for (int i = 0; i < 2 * kTokens; ++i) pass_through(p, tab[i / kTokens][i % kTokens]);
+
+    // the slot's row: head h of token `sub` of the group, at place l of its sequence; a row
+    // further is `dsub` tokens and `dh` heads further, and a token more where that passes
+    // the last head
+    const int dsub = kSlots / heads, dh = kSlots - dsub * heads;
+    const int sub0 = slot / heads, h0 = slot - sub0 * heads;
+    int l0 = (t0 + sub0) % p.L;  // of the group's first row
+    const long long seq = (t0 + sub0) / p.L;
+    const __nv_bfloat16 *x0 = (isq ? p.q : p.k) + seq * sx.b + l0 * sx.l + h0 * sx.h + lane8 * 8;
+    const __nv_bfloat16 *g0 = (isq ? p.dq : p.dk) + seq * sg.b + l0 * sg.l + h0 * sg.h + lane8 * 8;
+    __nv_bfloat16 *o0 = (isq ? p.qo : p.ko) + seq * so.b + l0 * so.l + h0 * so.h + lane8 * 8;
+    const __nv_bfloat16 *xp, *gp;
+    __nv_bfloat16 *op;
+    int group = t0, rows = 0, row = 0, sub = 0, h = 0, l = 0;
+    uint4 xv, gv;
+    auto load = [&](bool in) {
+        xv = gv = make_uint4(0u, 0u, 0u, 0u);
+        if (in) {
+            xv = *reinterpret_cast<const uint4 *>(xp);
+            gv = *reinterpret_cast<const uint4 *>(gp);
+        }
+    };
+    auto enter = [&]() {  // the first row of the group
+        rows = min(kTokens, t1 - group) * heads;
+        row = slot, sub = sub0, h = h0, l = l0, xp = x0, gp = g0, op = o0;
+        load(row < rows);
+    };
+    auto next_row = [&]() {
+        row += kSlots;
+        sub += dsub;
+        l += dsub;
+        h += dh;
+        xp += dsub * sx.l + dh * sx.h;
+        gp += dsub * sg.l + dh * sg.h;
+        op += dsub * so.l + dh * so.h;
+        if (h >= heads) {
+            h -= heads, sub += 1, l += 1;
+            xp += sx.l - heads * sx.h;
+            gp += sg.l - heads * sg.h;
+            op += so.l - heads * so.h;
+        }
+        while (l >= p.L) {
+            l -= p.L;
+            xp += sx.b - p.L * sx.l;
+            gp += sg.b - p.L * sg.l;
+            op += so.b - p.L * so.l;
+        }
+        load(row < rows);
+    };
+    auto next_group = [&]() {
+        group += kTokens;
+        l0 += kTokens;
+        x0 += kTokens * sx.l;
+        g0 += kTokens * sg.l;
+        o0 += kTokens * so.l;
+        while (l0 >= p.L) {
+            l0 -= p.L;
+            x0 += sx.b - p.L * sx.l;
+            g0 += sg.b - p.L * sg.l;
+            o0 += so.b - p.L * so.l;
+        }
+        if (group < t1) enter();
+    };
+
+    grid_dep_launch();
+    enter();
+    angles(t0, 0);
     __syncthreads();
-    for (int group = block; group < n_groups; group += blocks, which ^= 1) {
-        Factors<INTER> f;
-        f.load(tab[which][sub < per ? sub : 0], lane8, p.rot);
-        angles(which ^ 1);
-        __nv_bfloat16 *orow = op;
-        int h = h0;
-        for (int i = 0; i < rounds; ++i, h += kSlots, orow += kSlots * so.h) {
+    for (int which = 0, here = t0; here < t1; here += kTokens, which ^= 1) {
+        if (here + kTokens < t1) angles(here + kTokens, which ^ 1);
+        const int n_rows = min(kTokens, t1 - here) * heads;
+        for (int base = 0; base < n_rows; base += kSlots) {
             float x[8], g[8];
             unpack(xv, x);
             unpack(gv, g);
-            const bool in = live;
-            if (i + 1 < rounds) {
-                live = in && h + kSlots < heads;
-                load(live, (i + 1) * kSlots * sx.h, (i + 1) * kSlots * sg.h);
-            } else {
-                const bool wrap = move(c);
-                xp += mx + (wrap ? wx : 0);
-                gp += mg + (wrap ? wg : 0);
-                op += mo + (wrap ? wo : 0);
-                live = has && c.t < n_tokens;
-                load(live, 0, 0);
-            }
-            f.rotate(g, lane8, p.rot);
+            const bool in = base + slot < n_rows;
+            __nv_bfloat16 *const out = op;
+            Factors<D, INTER> f;
+            f.load(tab[which][in ? sub : 0], lane8);
+            if (base + kSlots < n_rows) next_row();
+            else next_group();
+            f.rotate(g, partner);
             float ss = 0.f, dot = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
@@ -307,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const __grid_cons
             const float m = -dot * r * r * (1.f / D);  // dx = r (w g - x r^2 mean(w g x))
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] = r * fmaf(x[e], m, g[e] * w[e]);
-            if (in) *reinterpret_cast<uint4 *>(orow) = pack(g);
+            if (in) *reinterpret_cast<uint4 *>(out) = pack(g);
         }
         __syncthreads();  // this table may be overwritten, the next one is there
     }
@@ -323,21 +372,22 @@ __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const __grid_cons
 }
 
 // The weights' gradients: dwq sums partial[block][D] over the first q_blocks blocks,
-// dwk over the others; 32 columns a block, 8 threads a column, always in the same order.
+// dwk over the others; 8 columns a block, 32 threads a column, always in the same order.
 __global__ void __launch_bounds__(256) weight_kernel(const float *partial, int q_blocks, int blocks, int D, float *dwq,
                                                      float *dwk) {
-    __shared__ float red[8][33];
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), s = threadIdx.x >> 5;
+    __shared__ float red[32][9];
+    const int col = blockIdx.x * 8 + (threadIdx.x & 7), s = threadIdx.x >> 3;
     const bool isq = col < D;
     const int c = isq ? col : col - D, end = isq ? q_blocks : blocks;
+    grid_dep_wait();
     float sum = 0.f;
-#pragma unroll 4
-    for (int i = (isq ? 0 : q_blocks) + s; i < end; i += 8) sum += partial[static_cast<size_t>(i) * D + c];
-    red[s][threadIdx.x & 31] = sum;
+#pragma unroll 8
+    for (int i = (isq ? 0 : q_blocks) + s; i < end; i += 32) sum += __ldcg(partial + static_cast<size_t>(i) * D + c);
+    red[s][threadIdx.x & 7] = sum;
     __syncthreads();
     if (s == 0) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) sum += red[i][threadIdx.x & 31];
+        for (int i = 1; i < 32; ++i) sum += red[i][threadIdx.x & 7];
         (isq ? dwq : dwk)[c] = sum;
     }
 }
@@ -395,8 +445,16 @@ int launch_backward(Params &p, int D, float *dwq, float *dwk, cudaStream_t strea
     kern<<<blocks, kThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return report_cuda("qk_norm_rope gradient launch", e);
-    weight_kernel<<<2 * D / 32, 256, 0, stream>>>(p.partial, p.q_blocks, blocks, D, dwq, dwk);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * D / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];  // set up while the first kernel runs, which it waits for
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, weight_kernel, static_cast<const float *>(p.partial), p.q_blocks, blocks, D, dwq, dwk);
     return e == cudaSuccess ? TFA_OK : report_cuda("norm weight gradient launch", e);
 }
 

@@ -60,6 +60,9 @@ CASES = [
     (1, 9, 33, 31, 64, 16, False, False, 0),
     (1, 601, 12, 4, 64, 32, True, True, 2_000_000_000),
     (2, 3, 4, 2, 128, 0, True, False, 0),
+    (40, 50, 1, 1, 64, 64, True, False, 3),  # many tokens and sequences in a round
+    (1000, 1, 3, 1, 128, 32, True, True, 77),
+    (7, 131, 20, 5, 128, 112, True, False, 9),
 ]
 IDS = ["-".join(map(str, c)) for c in CASES]
 
