@@ -13,10 +13,11 @@
 // Gradient, with g the rotated-back dy (the transposed rotation) and h = x r:
 //   dw += g h,   dx = r (w g - h mean(w g h)).
 //
-// Layout: a row is D / 8 lanes of 16 bytes, so a warp instruction moves whole
+// Layout: a row is D / 8 lanes of two times 8 bytes, so a warp instruction moves whole
 // 128-byte lines; tokens come in the projection's order ([B, L, H, D], any
 // strides) and leave in the attention's ([B, H, L, D], or a cache's rows), so
 // no separate transpose reads the data again.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -31,7 +32,7 @@ namespace tfa {
 namespace rope {
 
 constexpr int kThreads = 256;
-constexpr int kBwdBlocks = 444;  // gradient kernel: most blocks, so most partial sums of a weight
+constexpr int kBwdBlocks = 296;  // gradient kernel: most blocks, so most partial sums of a weight
 
 struct Strides {
     long long b, l, h;  // elements
@@ -59,95 +60,83 @@ __device__ __forceinline__ int position(const Params &p, int b, int l) {
     return p.pos_per_row ? __ldg(p.pos + static_cast<long long>(b) * p.L + l) : __ldg(p.pos + b) + l;
 }
 
-// What the channels of a position are multiplied by: each by its own c, its partner by
-// its own s (minus the sine for a pair's first channel); channels past rot by 1 and 0.
-// A lane's 8 channels lie as two float4, the lanes' first ones side by side, so that a
-// row's lanes read different banks.
+// The cosines and sines of a position's pairs, times mscale; a gradient's sines are negated.
 template <int D>
 struct Table {
-    float c[D], s[D];
-    __device__ __forceinline__ static int at(int channel) {
-        return ((channel >> 2) & 1) * (D / 2) + (channel >> 3) * 4 + (channel & 3);
-    }
+    float c[D / 2], s[D / 2];
 };
-
-// Pair i's angle at a position, into its two channels.
-template <int D>
-__device__ __forceinline__ void angle(const Params &p, int pos, int i, Table<D> &tab) {
+__device__ __forceinline__ double turns_per_token(const Params &p, int i) {
     constexpr double kInv2Pi = 0.15915494309189533577;
-    double turns = static_cast<double>(pos) * p.inv_freq[i] * kInv2Pi;
+    return p.inv_freq[i] * kInv2Pi;
+}
+template <int D>
+__device__ __forceinline__ void angle(const Params &p, int pos, double per_token, int i, Table<D> &tab) {
+    double turns = static_cast<double>(pos) * per_token;
     turns -= rint(turns);
     float s, c;
     sincospif(2.f * static_cast<float>(turns), &s, &c);
-    c *= p.mscale;
-    s *= p.conj ? -p.mscale : p.mscale;
-    const int a = p.inter ? 2 * i : i, b = p.inter ? 2 * i + 1 : i + (p.rot >> 1);
-    tab.c[Table<D>::at(a)] = tab.c[Table<D>::at(b)] = c;
-    tab.s[Table<D>::at(a)] = -s;
-    tab.s[Table<D>::at(b)] = s;
-}
-// The channels that pass through.
-template <int D>
-__device__ __forceinline__ void pass_through(const Params &p, Table<D> &tab) {
-    const int i = p.rot + threadIdx.x;
-    if (i < D) tab.c[Table<D>::at(i)] = 1.f, tab.s[Table<D>::at(i)] = 0.f;
+    tab.c[i] = c * p.mscale;
+    tab.s[i] = s * (p.conj ? -p.mscale : p.mscale);
 }
 
-__device__ __forceinline__ void unpack(const uint4 &v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// Lane `lane` of a row holds channels a .. a+3 and b .. b+3, chosen so that it holds
+// both channels of its pairs 4 lane .. 4 lane + 3: no lane needs another's values.
+struct Channels {
+    int a, b;
+    bool turns;  // a pair's channels; else they pass through
+    __device__ __forceinline__ Channels(const Params &p, int lane) {
+        turns = lane * 8 < p.rot;
+        a = turns && !p.inter ? lane * 4 : lane * 8;
+        b = turns && !p.inter ? a + (p.rot >> 1) : a + 4;
     }
+};
+
+// Eight channels as fp32 pairs: channels a, a+1 | a+2, a+3 | b, b+1 | b+2, b+3.
+struct Eight {
+    float2 v[4];
+};
+__device__ __forceinline__ float2 unpack(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ Eight unpack(uint2 a, uint2 b) {
+    return Eight{{unpack(a.x), unpack(a.y), unpack(b.x), unpack(b.y)}};
+}
+__device__ __forceinline__ uint32_t pack(float2 v) { return pack_bf16(v.x, v.y); }
+__device__ __forceinline__ Eight load_eight(const __nv_bfloat16 *row, const Channels &ch) {
+    return unpack(*reinterpret_cast<const uint2 *>(row + ch.a), *reinterpret_cast<const uint2 *>(row + ch.b));
+}
+__device__ __forceinline__ void store_eight(__nv_bfloat16 *row, const Channels &ch, const Eight &x) {
+    *reinterpret_cast<uint2 *>(row + ch.a) = make_uint2(pack(x.v[0]), pack(x.v[1]));
+    *reinterpret_cast<uint2 *>(row + ch.b) = make_uint2(pack(x.v[2]), pack(x.v[3]));
 }
 
-// The lane's 8 channels' factors; interleaved, one cosine and sine a pair.
+// The lane's four pairs' factors.
 template <int D, bool INTER>
 struct Factors {
-    float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
-    __device__ __forceinline__ void load(const Table<D> &tab, int lane8) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 x = *reinterpret_cast<const float4 *>(tab.c + i * (D / 2) + lane8 * 4);
-            const float4 y = *reinterpret_cast<const float4 *>(tab.s + i * (D / 2) + lane8 * 4);
-            if constexpr (INTER) {
-                c[2 * i] = x.x, c[2 * i + 1] = x.z;
-                s[2 * i] = y.y, s[2 * i + 1] = y.w;
-            } else {
-                c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
-                s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = y.z, s[4 * i + 3] = y.w;
-            }
-        }
+    float4 c, s;
+    __device__ __forceinline__ void load(const Table<D> &tab, int lane) {
+        c = *reinterpret_cast<const float4 *>(tab.c + lane * 4);
+        s = *reinterpret_cast<const float4 *>(tab.s + lane * 4);
     }
-    // Rotates the lane's 8 channels; every lane of the warp calls it (the half
-    // layout's partners sit in another lane: partner).
-    __device__ __forceinline__ void rotate(float (&y)[8], int partner) const {
+    __device__ __forceinline__ void rotate(Eight &x) const {
+        const float2 c2[2] = {{c.x, c.y}, {c.z, c.w}}, s2[2] = {{s.x, s.y}, {s.z, s.w}};
+        if constexpr (INTER) {
+            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-        for (int e = 0; e < (INTER ? 4 : 8); ++e) {
-            if constexpr (INTER) {
-                const float a = y[2 * e], b = y[2 * e + 1];
-                y[2 * e] = fmaf(a, c[e], -b * s[e]);
-                y[2 * e + 1] = fmaf(b, c[e], a * s[e]);
-            } else {
-                const float o = __shfl_sync(0xffffffffu, y[e], partner);
-                y[e] = fmaf(y[e], c[e], o * s[e]);
+            for (int e = 0; e < 4; ++e) {
+                const float2 y = x.v[e];
+                x.v[e] = make_float2(fmaf(y.x, cc[e], -y.y * ss[e]), fmaf(y.y, cc[e], y.x * ss[e]));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float2 a = x.v[e], b = x.v[2 + e];
+                x.v[e] = fma2(a, c2[e], mul2(b, make_float2(-s2[e].x, -s2[e].y)));
+                x.v[2 + e] = fma2(b, c2[e], mul2(a, s2[e]));
             }
         }
     }
 };
-// The half layout's partner lane: rot / 16 lanes away, in the same row.
-__device__ __forceinline__ int partner_lane(int lane8, int rot) {
-    const int half = rot >> 4, lane = threadIdx.x & 31;
-    return lane8 * 8 >= rot ? lane : (lane8 < half ? lane + half : lane - half);
-}
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -156,62 +145,79 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
+// Both sums at once: a half of the row's lanes goes on with each, until the last exchange.
+template <int LPR>
+__device__ __forceinline__ void row_sums(float &x, float &y) {
+    const bool upper = threadIdx.x & (LPR / 2);
+    float mine = upper ? y : x;
+    mine += __shfl_xor_sync(0xffffffffu, upper ? x : y, LPR / 2);
+#pragma unroll
+    for (int o = LPR / 4; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    const float other = __shfl_xor_sync(0xffffffffu, mine, LPR / 2);
+    x = upper ? other : mine;
+    y = upper ? mine : other;
+}
+
 template <int D, bool NORM, bool INTER>
-__global__ void __launch_bounds__(kThreads, 3) forward_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 5) forward_kernel(const __grid_constant__ Params p) {
     constexpr int LPR = D / 8, kSlots = kThreads / LPR;
     __shared__ __align__(16) Table<D> tab;
     const int token = blockIdx.x, b = token / p.L, l = token - b * p.L;
-    const int lane8 = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+    const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+    const Channels ch(p, lane);
     const int n_rows = p.Hq + p.Hkv;
     const int row0 = blockIdx.y * p.rows_per_block;
     const int row1 = min(row0 + p.rows_per_block, n_rows);
-    const __nv_bfloat16 *q = p.q + b * p.sq.b + l * p.sq.l + lane8 * 8;
-    const __nv_bfloat16 *k = p.k + b * p.sk.b + l * p.sk.l + lane8 * 8;
-    __nv_bfloat16 *qo = p.qo + b * p.sqo.b + l * p.sqo.l + lane8 * 8;
-    __nv_bfloat16 *ko = p.ko + b * p.sko.b + l * p.sko.l + lane8 * 8;
+    const __nv_bfloat16 *q = p.q + b * p.sq.b + l * p.sq.l;
+    const __nv_bfloat16 *k = p.k + b * p.sk.b + l * p.sk.l;
+    __nv_bfloat16 *qo = p.qo + b * p.sqo.b + l * p.sqo.l;
+    __nv_bfloat16 *ko = p.ko + b * p.sko.b + l * p.sko.l;
     // the first rows are on their way while the table is computed
-    constexpr int kAhead = 4;
-    uint4 x[kAhead];
+    constexpr int kAhead = 2;
+    uint2 xa[kAhead], xb[kAhead];
     auto load = [&](int base) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int row = base + slot + u * kSlots;
-            x[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < row1)
-                x[u] = *reinterpret_cast<const uint4 *>(row < p.Hq ? q + row * p.sq.h : k + (row - p.Hq) * p.sk.h);
+            xa[u] = xb[u] = make_uint2(0u, 0u);
+            if (row < row1) {
+                const __nv_bfloat16 *x = row < p.Hq ? q + row * p.sq.h : k + (row - p.Hq) * p.sk.h;
+                xa[u] = *reinterpret_cast<const uint2 *>(x + ch.a);
+                xb[u] = *reinterpret_cast<const uint2 *>(x + ch.b);
+            }
         }
     };
     load(row0);
-    if (threadIdx.x < static_cast<unsigned>(p.rot >> 1)) angle(p, position(p, b, l), threadIdx.x, tab);
-    pass_through(p, tab);
-    float wq[8], wk[8];
+    if (threadIdx.x < static_cast<unsigned>(p.rot >> 1)) 
+        angle(p, position(p, b, l), turns_per_token(p, threadIdx.x), threadIdx.x, tab);
+    uint2 wq[2], wk[2];  // as bf16: as fp32 they cost a block of the SM's five
     if constexpr (NORM) {
-        unpack(*reinterpret_cast<const uint4 *>(p.wq + lane8 * 8), wq);
-        unpack(*reinterpret_cast<const uint4 *>(p.wk + lane8 * 8), wk);
+        wq[0] = *reinterpret_cast<const uint2 *>(p.wq + ch.a), wq[1] = *reinterpret_cast<const uint2 *>(p.wq + ch.b);
+        wk[0] = *reinterpret_cast<const uint2 *>(p.wk + ch.a), wk[1] = *reinterpret_cast<const uint2 *>(p.wk + ch.b);
     }
     __syncthreads();
     Factors<D, INTER> f;
-    f.load(tab, lane8);
-    const int partner = partner_lane(lane8, p.rot);
+    if (ch.turns) f.load(tab, lane);
     for (int base = row0; base < row1; base += kAhead * kSlots) {
         if (base > row0) load(base);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int row = base + slot + u * kSlots;
             if (base + u * kSlots >= row1) break;  // block-uniform
-            float y[8];
-            unpack(x[u], y);
+            Eight y = unpack(xa[u], xb[u]);
             if constexpr (NORM) {
-                float ss = 0.f;
+                float2 ss = mul2(y.v[0], y.v[0]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-                const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+                for (int e = 1; e < 4; ++e) ss = fma2(y.v[e], y.v[e], ss);
+                const float r = rsqrtf(row_sum<LPR>(ss.x + ss.y) * (1.f / D) + p.eps);
+                const float2 r2 = make_float2(r, r);
+                const bool isq = row < p.Hq;
+                const Eight w = unpack(isq ? wq[0] : wk[0], isq ? wq[1] : wk[1]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] *= r * (row < p.Hq ? wq[e] : wk[e]);
+                for (int e = 0; e < 4; ++e) y.v[e] = mul2(y.v[e], mul2(r2, w.v[e]));
             }
-            f.rotate(y, partner);
-            if (row < row1)
-                *reinterpret_cast<uint4 *>(row < p.Hq ? qo + row * p.sqo.h : ko + (row - p.Hq) * p.sko.h) = pack(y);
+            if (ch.turns) f.rotate(y);
+            if (row < row1) store_eight(row < p.Hq ? qo + row * p.sqo.h : ko + (row - p.Hq) * p.sko.h, ch, y);
         }
     }
 }
@@ -219,149 +225,173 @@ __global__ void __launch_bounds__(kThreads, 3) forward_kernel(const __grid_const
 // Gradient with norms: a block walks its own run of tokens, so that the weight's
 // gradient gathers in registers over all of its rows; one partial sum per block, added
 // up in block order by the second kernel (the same order every time).
-// A block takes query rows only or key rows only, in proportion to their heads: the
-// strides and the tensors are then the same for all its threads, and a thread keeps
-// one weight and one sum (with both kinds in a block the loop spilled and took 39
-// instructions a channel).  The run's rows, token by token and head by head, are dealt
-// to the slots (the lanes of a row) in turn; a slot's pointers move from row to row by
-// constant strides.  The next row's loads are issued while a row is computed, and the
-// angles of the next four tokens while these four's rows are, by all threads, between
-// two barriers (a barrier and a fourth of the threads for each token: 50 us for 4 x
-// 2047 tokens of 24 heads, this way BWD_US us; the 151 MB would take 23).
-constexpr int kTokens = 4;  // of a table
+// A block takes query rows only or key rows only, in proportion to their rounds: the
+// weight is the block's, not the row's.  A slot (the lanes of a row) keeps one token of
+// a group and takes its heads kHeads apart, kRows of them in a round, so the angles
+// stay in its registers over the group's rounds and its pointers move by constant
+// strides; other head counts than multiples of 8 leave slots idle in the last round.
+// The next group's angles are computed while this one's rows are, one a thread, between
+// two barriers.  Rows are copied to shared memory kAhead rounds before they are needed.
+// Instructions bound it more than the memory: 4 x 2047 tokens of 24 heads took 44 us
+// with the rows dealt to the slots in order and a channel's partner in another lane (337
+// instructions a warp for two rows), 39 with pairs in a lane and fixed tokens (204), 37
+// with 2 blocks of 102 registers an SM instead of 3 of 80 (169), and takes 35 with two
+// rows a round (153); the 151 MB would take 23.
+constexpr int kHeads = 4;
+constexpr int kRows = 2;
+constexpr int kAhead = 2;
+constexpr int kRingBytes = (kAhead + 1) * kRows * 2 * kThreads * 16;
 
-template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, 3) backward_kernel(const __grid_constant__ Params p) {
-    constexpr int LPR = D / 8, kSlots = kThreads / LPR;
+// (Nothing is read at `src` where the row is not `in`: zeros are written.)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+// A block of query rows (ISQ) or of key rows: its `block` of the kind's `blocks`.  (The
+// kind is a template's so that strides and weights are the launch's constants: chosen
+// at run time they cost 40 integer instructions a round.)
+template <int D, bool INTER, bool ISQ>
+__device__ __forceinline__ void backward_block(const Params &p, int block, int blocks) {
+    constexpr int LPR = D / 8, kSlots = kThreads / LPR, kTokens = kSlots / kHeads;
+    static_assert(kTokens * (D / 2) == kThreads, "an angle a thread");
     __shared__ __align__(16) Table<D> tab[2][kTokens];
-    __shared__ float red[kSlots][D + 4];
-    const bool isq = static_cast<int>(blockIdx.x) < p.q_blocks;  // the block's kind
-    const int block = isq ? blockIdx.x : blockIdx.x - p.q_blocks;
-    const int blocks = isq ? p.q_blocks : static_cast<int>(gridDim.x) - p.q_blocks;
-    const int heads = isq ? p.Hq : p.Hkv;
-    const Strides sx = isq ? p.sq : p.sk, sg = isq ? p.sdq : p.sdk, so = isq ? p.sqo : p.sko;
+    extern __shared__ uint4 dynamic[];
+    __nv_bfloat16 *const ring = reinterpret_cast<__nv_bfloat16 *>(dynamic);  // [kAhead + 1][kRows][2][kSlots][D]
+    float (*red)[D + 4] = reinterpret_cast<float (*)[D + 4]>(dynamic);       // [kSlots], after the last row
+    static_assert(kSlots * (D + 4) * sizeof(float) <= kRingBytes, "the sums fit in the rows' place");
+    const int heads = ISQ ? p.Hq : p.Hkv;
+    const Strides &sx = ISQ ? p.sq : p.sk, &sg = ISQ ? p.sdq : p.sdk, &so = ISQ ? p.sqo : p.sko;
     const int n_tokens = p.B * p.L;
     const int t0 = static_cast<int>(static_cast<long long>(n_tokens) * block / blocks);
     const int t1 = static_cast<int>(static_cast<long long>(n_tokens) * (block + 1) / blocks);
-    const int lane8 = threadIdx.x % LPR, slot = threadIdx.x / LPR;
-    const int partner = partner_lane(lane8, p.rot);
-    float w[8], acc[8];
-    unpack(*reinterpret_cast<const uint4 *>((isq ? p.wq : p.wk) + lane8 * 8), w);
+    const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+    const int sub = slot / kHeads, h0 = slot % kHeads;
+    const Channels ch(p, lane);
+    const Eight w = load_eight(ISQ ? p.wq : p.wk, ch);
+    Eight acc = {};
+
+    // The places of token `group + of` of the groups one after the other: moves l and
+    // returns the sequences that the move leaves behind.
+    auto next_group = [&](int &l) {
+        l += kTokens;
+        int wraps = 0;
+        while (l >= p.L) l -= p.L, ++wraps;
+        return wraps;
+    };
+    auto move = [&](auto *&ptr, const Strides &s, int wraps) {
+        ptr += kTokens * s.l;
+        if (wraps) ptr += wraps * (s.b - p.L * s.l);
+    };
+
+    // this thread's pair and its token of the group, for the tables
+    const int pair = threadIdx.x % (D / 2), pair_of = threadIdx.x / (D / 2);
+    const double per_token = pair < (p.rot >> 1) ? turns_per_token(p, pair) : 0.;
+    int pair_l = (t0 + pair_of) % p.L, pair_b = (t0 + pair_of) / p.L;
+    auto angles = [&](int group, int buf) {
+        if (group + pair_of < t1 && pair < (p.rot >> 1))
+            angle(p, position(p, pair_b, pair_l), per_token, pair, tab[buf][pair_of]);
+        pair_b += next_group(pair_l);
+    };
+
+    // A walk over the slot's rows: head h0 + round kHeads of token group + sub, at place l
+    // of its sequence.  The loads' walk (in_) is kAhead rounds before the computation's.
+    const int first_l = (t0 + sub) % p.L;
+    const long long seq = (t0 + sub) / p.L;
+    const __nv_bfloat16 *x0 = (ISQ ? p.q : p.k) + seq * sx.b + first_l * sx.l + h0 * sx.h + lane * 8, *xp = x0;
+    const __nv_bfloat16 *g0 = (ISQ ? p.dq : p.dk) + seq * sg.b + first_l * sg.l + h0 * sg.h + lane * 8, *gp = g0;
+    __nv_bfloat16 *o0 = (ISQ ? p.qo : p.ko) + seq * so.b + first_l * so.l + h0 * so.h;
+    int in_group = t0, in_h = h0, in_l = first_l, out_l = first_l;
+    uint32_t fill = smem_addr(dynamic) + threadIdx.x * 16;
+    const uint32_t fill_end = fill + kRingBytes;
+    auto fetch = [&]() {  // a round's rows
+        if (in_group < t1) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-
-    // a table's angles: D / 2 threads a token, kThreads / (D / 2) tokens at a time
-    auto angles = [&](int first, int buf) {
-#pragma unroll
-        for (int k = 0; k < kTokens; k += kThreads / (D / 2)) {
-            const int sub = k + threadIdx.x / (D / 2), i = threadIdx.x % (D / 2), t = first + sub;
-            if (sub < kTokens && t < t1 && i < (p.rot >> 1)) angle(p, position(p, t / p.L, t % p.L), i, tab[buf][sub]);
+            for (int u = 0; u < kRows; ++u) {
+                const bool in = in_group + sub < t1 && in_h + u * kHeads < heads;
+                copy16(fill + u * 2 * kThreads * 16, xp, in);
+                copy16(fill + (u * 2 + 1) * kThreads * 16, gp, in);
+                xp += kHeads * sx.h;
+                gp += kHeads * sg.h;
+            }
+            in_h += kRows * kHeads;
+            if (in_h - h0 >= heads) {
+                in_h = h0;
+                in_group += kTokens;
+                const int wraps = next_group(in_l);
+                move(x0, sx, wraps);
+                move(g0, sg, wraps);
+                xp = x0;
+                gp = g0;
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        fill += kRows * 2 * kThreads * 16;
+        if (fill == fill_end) fill -= kRingBytes;
     };
-    for (int i = 0; i < 2 * kTokens; ++i) pass_through(p, tab[i / kTokens][i % kTokens]);
-
-    // the slot's row: head h of token `sub` of the group, at place l of its sequence; a row
-    // further is `dsub` tokens and `dh` heads further, and a token more where that passes
-    // the last head
-    const int dsub = kSlots / heads, dh = kSlots - dsub * heads;
-    const int sub0 = slot / heads, h0 = slot - sub0 * heads;
-    int l0 = (t0 + sub0) % p.L;  // of the group's first row
-    const long long seq = (t0 + sub0) / p.L;
-    const __nv_bfloat16 *x0 = (isq ? p.q : p.k) + seq * sx.b + l0 * sx.l + h0 * sx.h + lane8 * 8;
-    const __nv_bfloat16 *g0 = (isq ? p.dq : p.dk) + seq * sg.b + l0 * sg.l + h0 * sg.h + lane8 * 8;
-    __nv_bfloat16 *o0 = (isq ? p.qo : p.ko) + seq * so.b + l0 * so.l + h0 * so.h + lane8 * 8;
-    const __nv_bfloat16 *xp, *gp;
-    __nv_bfloat16 *op;
-    int group = t0, rows = 0, row = 0, sub = 0, h = 0, l = 0;
-    uint4 xv, gv;
-    auto load = [&](bool in) {
-        xv = gv = make_uint4(0u, 0u, 0u, 0u);
-        if (in) {
-            xv = *reinterpret_cast<const uint4 *>(xp);
-            gv = *reinterpret_cast<const uint4 *>(gp);
-        }
-    };
-    auto enter = [&]() {  // the first row of the group
-        rows = min(kTokens, t1 - group) * heads;
-        row = slot, sub = sub0, h = h0, l = l0, xp = x0, gp = g0, op = o0;
-        load(row < rows);
-    };
-    auto next_row = [&]() {
-        row += kSlots;
-        sub += dsub;
-        l += dsub;
-        h += dh;
-        xp += dsub * sx.l + dh * sx.h;
-        gp += dsub * sg.l + dh * sg.h;
-        op += dsub * so.l + dh * so.h;
-        if (h >= heads) {
-            h -= heads, sub += 1, l += 1;
-            xp += sx.l - heads * sx.h;
-            gp += sg.l - heads * sg.h;
-            op += so.l - heads * so.h;
-        }
-        while (l >= p.L) {
-            l -= p.L;
-            xp += sx.b - p.L * sx.l;
-            gp += sg.b - p.L * sg.l;
-            op += so.b - p.L * so.l;
-        }
-        load(row < rows);
-    };
-    auto next_group = [&]() {
-        group += kTokens;
-        l0 += kTokens;
-        x0 += kTokens * sx.l;
-        g0 += kTokens * sg.l;
-        o0 += kTokens * so.l;
-        while (l0 >= p.L) {
-            l0 -= p.L;
-            x0 += sx.b - p.L * sx.l;
-            g0 += sg.b - p.L * sg.l;
-            o0 += so.b - p.L * so.l;
-        }
-        if (group < t1) enter();
-    };
-
     grid_dep_launch();
-    enter();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch();
     angles(t0, 0);
     __syncthreads();
-    for (int which = 0, here = t0; here < t1; here += kTokens, which ^= 1) {
-        if (here + kTokens < t1) angles(here + kTokens, which ^ 1);
-        const int n_rows = min(kTokens, t1 - here) * heads;
-        for (int base = 0; base < n_rows; base += kSlots) {
-            float x[8], g[8];
-            unpack(xv, x);
-            unpack(gv, g);
-            const bool in = base + slot < n_rows;
-            __nv_bfloat16 *const out = op;
-            Factors<D, INTER> f;
-            f.load(tab[which][in ? sub : 0], lane8);
-            if (base + kSlots < n_rows) next_row();
-            else next_group();
-            f.rotate(g, partner);
-            float ss = 0.f, dot = 0.f;
+    int take = 0;
+    for (int group = t0, which = 0; group < t1; group += kTokens, which ^= 1) {
+        if (group + kTokens < t1) angles(group + kTokens, which ^ 1);
+        Factors<D, INTER> f;
+        const bool token = group + sub < t1;
+        if (ch.turns) f.load(tab[which][token ? sub : 0], lane);  // a slot without a token turns zeros
+        __nv_bfloat16 *op = o0;
+        for (int base = 0; base < heads; base += kRows * kHeads) {
+            // this round's rows are there, all lanes' parts of them, and the last round's are read
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            __syncwarp();
+            fetch();
+            const __nv_bfloat16 *row = ring + (take * kRows * 2 * kSlots + slot) * D;
+            take = take == kAhead ? 0 : take + 1;
+            Eight x[kRows], g[kRows], t[kRows];
+            float sum[kRows], mean[kRows];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-            const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-            const float rr = in ? r : 0.f;  // (a row past the last holds zeros, but eps may be 0)
+            for (int u = 0; u < kRows; ++u) {
+                x[u] = load_eight(row + u * 2 * kSlots * D, ch);
+                g[u] = load_eight(row + (u * 2 + 1) * kSlots * D, ch);
+                if (ch.turns) f.rotate(g[u]);
+                float2 ss = mul2(x[u].v[0], x[u].v[0]), dot = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float gx = g[e] * x[e];
-                dot = fmaf(gx, w[e], dot);
-                acc[e] = fmaf(gx, rr, acc[e]);
+                for (int e = 1; e < 4; ++e) ss = fma2(x[u].v[e], x[u].v[e], ss);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    t[u].v[e] = mul2(g[u].v[e], w.v[e]);
+                    dot = fma2(t[u].v[e], x[u].v[e], dot);
+                }
+                sum[u] = ss.x + ss.y;
+                mean[u] = dot.x + dot.y;
             }
-            dot = row_sum<LPR>(dot);
-            const float m = -dot * r * r * (1.f / D);  // dx = r (w g - x r^2 mean(w g x))
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = r * fmaf(x[e], m, g[e] * w[e]);
-            if (in) *reinterpret_cast<uint4 *>(out) = pack(g);
+            for (int u = 0; u < kRows; ++u) row_sums<LPR>(sum[u], mean[u]);
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const bool in = token && base + u * kHeads + h0 < heads;
+                const float r = rsqrtf(sum[u] * (1.f / D) + p.eps);
+                const float rr = in ? r : 0.f;  // (a row past the last holds zeros, but eps may be 0)
+                const float m = -mean[u] * r * r * (1.f / D);  // dx = r w g - h mean(w g h), h = x r
+                const float2 r2 = make_float2(r, r), rr2 = make_float2(rr, rr), m2 = make_float2(m, m);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 hn = mul2(x[u].v[e], rr2);
+                    acc.v[e] = fma2(g[u].v[e], hn, acc.v[e]);
+                    t[u].v[e] = fma2(hn, m2, mul2(t[u].v[e], r2));
+                }
+                if (in) store_eight(op, ch, t[u]);
+                op += kHeads * so.h;
+            }
         }
+        move(o0, so, next_group(out_l));
         __syncthreads();  // this table may be overwritten, the next one is there
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[slot][lane8 * 8 + e] = acc[e];
+    for (int e = 0; e < 2; ++e) {
+        red[slot][ch.a + 2 * e] = acc.v[e].x, red[slot][ch.a + 2 * e + 1] = acc.v[e].y;
+        red[slot][ch.b + 2 * e] = acc.v[2 + e].x, red[slot][ch.b + 2 * e + 1] = acc.v[2 + e].y;
+    }
     __syncthreads();
     if (threadIdx.x < D) {
         float s = 0.f;
@@ -369,6 +399,15 @@ __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const __grid_cons
         for (int i = 0; i < kSlots; ++i) s += red[i][threadIdx.x];
         p.partial[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = s;
     }
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 2) backward_kernel(const __grid_constant__ Params p) {
+    const int block = blockIdx.x;
+    if (block < p.q_blocks)
+        backward_block<D, INTER, true>(p, block, p.q_blocks);
+    else
+        backward_block<D, INTER, false>(p, block - p.q_blocks, static_cast<int>(gridDim.x) - p.q_blocks);
 }
 
 // The weights' gradients: dwq sums partial[block][D] over the first q_blocks blocks,
@@ -432,8 +471,10 @@ int launch_forward(Params &p, int D, cudaStream_t stream) {
 
 int launch_backward(Params &p, int D, float *dwq, float *dwk, cudaStream_t stream) {
     const int tokens = p.B * p.L;
-    // blocks in proportion to the heads, one of each kind at least, none without a token
-    p.q_blocks = static_cast<int>(static_cast<long long>(kBwdBlocks) * p.Hq / (p.Hq + p.Hkv));
+    // blocks in proportion to the rounds, one of each kind at least, none without a token
+    constexpr int kRound = kRows * kHeads;
+    const int rq = (p.Hq + kRound - 1) / kRound, rk = (p.Hkv + kRound - 1) / kRound;
+    p.q_blocks = static_cast<int>(static_cast<long long>(kBwdBlocks) * rq / (rq + rk));
     p.q_blocks = p.q_blocks < 1 ? 1 : p.q_blocks > kBwdBlocks - 1 ? kBwdBlocks - 1 : p.q_blocks;
     int k_blocks = kBwdBlocks - p.q_blocks;
     if (p.q_blocks > tokens) p.q_blocks = tokens;
@@ -442,8 +483,19 @@ int launch_backward(Params &p, int D, float *dwq, float *dwk, cudaStream_t strea
     using Kern = void (*)(Params);
     const Kern kern = D == 128 ? (p.inter ? backward_kernel<128, true> : backward_kernel<128, false>)
                                : (p.inter ? backward_kernel<64, true> : backward_kernel<64, false>);
-    kern<<<blocks, kThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    static std::atomic<bool> prepared[kMaxDevices][4];  // the attribute holds for one device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return report_cuda("cudaGetDevice", e);
+    if (dev < 0 || dev >= kMaxDevices) return report_cuda("device index", cudaErrorInvalidDevice);
+    std::atomic<bool> &ready = prepared[dev][(D == 128 ? 2 : 0) + (p.inter ? 1 : 0)];
+    if (!ready.load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+        if (e != cudaSuccess) return report_cuda("cudaFuncSetAttribute(norm gradient smem)", e);
+        ready.store(true, std::memory_order_release);
+    }
+    kern<<<blocks, kThreads, kRingBytes, stream>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return report_cuda("qk_norm_rope gradient launch", e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * D / 8);
