@@ -62,7 +62,7 @@ def test_rope_refusals(back, over, code):
 def test_rope_backward_needs_its_buffers_with_weights():
     assert _rope(True, ws=None) == tb.TFA_ERR_NULL
     assert _rope(True, dw=None) == tb.TFA_ERR_NULL
-    assert tb.lib().tfa_qk_norm_rope_workspace(128) == 444 * 128 * 4
+    assert tb.lib().tfa_qk_norm_rope_workspace(128) == 296 * 128 * 4
 
 
 def test_rope_inv_freq_refusals():
