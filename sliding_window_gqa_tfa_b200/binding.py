@@ -136,8 +136,32 @@ def lib():
             L.tfa_kv4_decode_workspace.restype = ctypes.c_size_t
             L.tfa_qk_norm_rope_workspace.argtypes = [i32]
             L.tfa_qk_norm_rope_workspace.restype = ctypes.c_size_t
+            _load_calls(L)
             _lib = L
     return _lib
+
+
+_calls = None  # csrc/calls.cpp's module, once the library is loaded
+
+
+def _load_calls(L):
+    global _calls
+    try:
+        from . import _calls as module
+    except ImportError as e:
+        raise RuntimeError("_calls.so is missing or built for another torch: build it with "
+                           "`python -m sliding_window_gqa_tfa_b200.build`") from e
+    module.use(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+        "tfa_qk_norm_rope", "tfa_qk_norm_rope_backward", "tfa_qk_norm_rope_workspace", "tfa_kv4_append",
+        "tfa_kv4_read", "tfa_kv4_decode", "tfa_kv4_decode_workspace", "tfa_prefill_first")))
+    _calls = module
+
+
+def _native(result, where):
+    """What a native call that was made returned: its status, if that is not TFA_OK."""
+    if isinstance(result, int):
+        raise TfaError(result, where)
+    return result
 
 
 def declared_symbols() -> list[str]:
@@ -575,6 +599,10 @@ def _first_inputs(q, k, v, causal, key_mask):
 
 def _prefill_first(q, k, v, scale, causal, window, first, key_mask, softcap, sinks, out, lse, want_lse, stream):
     """(out, lse): prefill and prefill_lse with first tokens that stay visible."""
+    if _calls is not None and stream is None and causal:
+        made = _calls.prefill_first(q, k, v, scale, window, first, key_mask, softcap, sinks, out, lse, want_lse)
+        if made is not None:
+            return _native(made, "tfa_prefill_first")
     dev, dims = _first_inputs(q, k, v, causal, key_mask)
     if sinks is not None:
         _check_on(sinks, "sinks", _F32, 1, dev)
@@ -721,6 +749,10 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     an int.  inv_freq: fp64 [rot/2] on the device (rope_inv_freq), rot a multiple of
     16 up to D, the other channels pass through.  q_out and k_out may be views, e.g.
     a key cache's rows, in [B,H,L,D] order.  Raises TfaError on a nonzero status."""
+    if _calls is not None and stream is None:
+        made = _calls.rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, mscale, q_out, k_out)
+        if made is not None:
+            return _native(made, "tfa_qk_norm_rope")
     dev, mid, dims = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight)
     B, L, Hq, Hkv, D, rot = dims
     with _scope(dev, stream):
@@ -749,6 +781,11 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
     dq_out [B,Hq,L,D] and dk_out [B,Hkv,L,D] (bf16, any strides with contiguous
     channels).  dq [B,L,Hq,D] and dk [B,L,Hkv,D] are bf16 (views in `out` are fine);
     the weights' are fp32 [D], None without weights."""
+    if _calls is not None and stream is None and out is None:
+        made = _calls.rope_backward(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, mscale, dq_out,
+                                    dk_out)
+        if made is not None:
+            return _native(made, "tfa_qk_norm_rope_backward")
     dev, mid, dims = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight)
     B, L, Hq, Hkv, D, rot = dims
     _check_rows(dq_out, "dq_out", (B, Hq, L, D), dev)
@@ -826,6 +863,12 @@ def kv4_append(k, v, k_codes, k_meta, v_codes, v_meta, *, start, stream=None):
     """Writes k, v (bf16 [B,Hkv,L,D], any strides with contiguous channels) into the
     4-bit cache: row i of sequence b at cache row start[b] + i.  start: int32 [B] on
     the device (negative: nothing for that sequence), or an int for all."""
+    if _calls is not None and stream is None:
+        made = _calls.append(k, v, k_codes, k_meta, v_codes, v_meta, start)
+        if made == TFA_OK:
+            return
+        if made is not None:
+            raise TfaError(made, "tfa_kv4_append")
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
     _check_on(k, "k", _BF16, 4, dev, rows=True)
     _check_on(v, "v", _BF16, 4, dev, rows=True)
@@ -846,6 +889,10 @@ def kv4_append(k, v, k_codes, k_meta, v_codes, v_meta, *, start, stream=None):
 def kv4_read(k_codes, k_meta, v_codes, v_meta, *, start=0, rows=None, out=None, stream=None):
     """(k, v) bf16 [B,Hkv,rows,D]: the values of cached rows start[b] .. start[b] + rows - 1
     (start: int32 [B] on the device, or an int; rows: by default all from start on)."""
+    if _calls is not None and stream is None and out is None:
+        made = _calls.read(k_codes, k_meta, v_codes, v_meta, start, rows)
+        if made is not None:
+            return _native(made, "tfa_kv4_read")
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
     ptr, first = _kv4_start(start, B, dev)
     if rows is None:
@@ -897,6 +944,11 @@ def kv4_decode(q, k_codes, k_meta, v_codes, v_meta, lens, *, scale=None, window=
     on the device, holds each sequence's cached positions, its L new rows last among
     them.  window > 0: the last `window` positions and the `first` first ones.
     workspace: uint8 of tfa_kv4_decode_workspace bytes, by default allocated here."""
+    if _calls is not None and stream is None:
+        made = _calls.decode(q, k_codes, k_meta, v_codes, v_meta, lens, scale, window, first, softcap, sinks, out,
+                             workspace)
+        if made is not None:
+            return _native(made, "tfa_kv4_decode")
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
     _kv4_query(q, B, D, dev, sinks, out)
     _check_on(lens, "lens", _I32, 1, dev)

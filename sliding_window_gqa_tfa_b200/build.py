@@ -1,4 +1,5 @@
-"""Build libtfa.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a.
+"""Build libtfa.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a, and
+_calls.so (the binding's native calls, against the installed torch) with g++.
 
     python -m sliding_window_gqa_tfa_b200.build [--verbose] [--changed]
 
@@ -7,18 +8,22 @@ source, or any header, is newer than the object).
 
 The library is written next to this file; it links the CUDA runtime
 statically and resolves the driver's cuTensorMapEncodeTiled at run time, so it
-needs no library path beyond the NVIDIA driver.
+needs no library path beyond the NVIDIA driver.  _calls.so takes the library's
+addresses from it and resolves torch's from the torch that is imported.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtfa.so")
+CALLS = os.path.join(HERE, "_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "calls.cpp")
 OBJ = os.path.join(HERE, "_build")  # object files (git-ignored)
 SOURCES = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith(".cu")]
 HEADERS = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
@@ -33,10 +38,23 @@ def nvcc() -> str:
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in SOURCES + HEADERS)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    return any(os.path.getmtime(f) > t for f in SOURCES + HEADERS + [CALLS_SOURCE])
+
+
+def calls_command(out: str) -> list[str]:
+    """g++'s command for _calls.so."""
+    import torch
+
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", base, "-isystem",
+            sysconfig.get_paths()["include"], "-isystem", cuda, "-o", out, CALLS_SOURCE,
+            "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -58,11 +76,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(src), header_time):
             cmd = base + ["-c", "-o", obj + f".tmp{os.getpid()}", src]
             running.append((cmd, obj, subprocess.Popen(cmd)))
+    calls_tmp = CALLS + f".tmp{os.getpid()}"
+    if force or not os.path.exists(CALLS) or os.path.getmtime(CALLS) < max(os.path.getmtime(CALLS_SOURCE), header_time):
+        cmd = calls_command(calls_tmp)
+        running.append((cmd, None, subprocess.Popen(cmd)))
     failed = [(cmd, p.returncode) for cmd, _, p in running if p.wait() != 0]
     if failed:
         raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
     for _, obj, _ in running:
-        os.replace(obj + f".tmp{os.getpid()}", obj)
+        if obj is None:
+            os.replace(calls_tmp, CALLS)
+        else:
+            os.replace(obj + f".tmp{os.getpid()}", obj)
     subprocess.run(base + ["-shared", "-o", tmp] + objs, check=True)
     os.replace(tmp, LIB)
     return LIB

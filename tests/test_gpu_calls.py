@@ -1,0 +1,144 @@
+"""The native calls (csrc/calls.cpp) against the wrappers' Python code, which makes the
+same C calls: the same bits, the same refusals, and None where a call is not theirs."""
+import pytest
+import torch
+
+from sliding_window_gqa_tfa_b200 import binding as tb
+
+D, B, HQ, HKV, L, CAP = 64, 3, 4, 2, 2, 70
+
+
+def _rows(seed, *shape):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=g).bfloat16()
+
+
+def _calls(device):
+    """name -> (a wrapper's call, given what overrides its tensors)."""
+    on = lambda t: t.to(device)
+    q, k = on(_rows(0, B, L, HQ, D)), on(_rows(1, B, L, HKV, D))
+    w = on(_rows(2, D))
+    freq, _ = tb.rope_inv_freq(D, device=device)
+    pos = on(torch.tensor([0, 5, 900], dtype=torch.int32))
+    dq, dk = on(_rows(3, B, HQ, L, D)), on(_rows(4, B, HKV, L, D))
+    ck, cv = on(_rows(5, B, HKV, CAP, D)), on(_rows(6, B, HKV, CAP, D))
+    lens = on(torch.tensor([CAP, 0, 33], dtype=torch.int32))
+    sinks = on(torch.randn(HQ, generator=torch.Generator().manual_seed(7)))
+
+    def cache():
+        c = tb.kv4_cache(B, HKV, CAP, D, device=device)
+        tb.kv4_append(ck, cv, *c, start=0)
+        return c
+
+    def append():
+        c = tb.kv4_cache(B, HKV, CAP, D, device=device)
+        tb.kv4_append(ck[:, :, :L], cv[:, :, :L], *c, start=pos.clamp(max=CAP - L))
+        return c
+
+    return {
+        "rope": lambda: tb.qk_norm_rope(q, k, pos, freq, q_weight=w, k_weight=w),
+        "rope_plain": lambda: tb.qk_norm_rope(q, k, 17, freq, interleaved=True, mscale=1.25),
+        "rope_per_row": lambda: tb.qk_norm_rope(q, k, pos[:, None].expand(B, L).contiguous(), freq),
+        "backward": lambda: tb.qk_norm_rope_backward(dq, dk, q, k, pos, freq, q_weight=w, k_weight=w),
+        "append": append,
+        "read": lambda: tb.kv4_read(*cache(), start=pos.clamp(max=40), rows=9),
+        "read_rest": lambda: tb.kv4_read(*cache(), start=60),
+        "decode": lambda: tb.kv4_decode(dq, *cache(), lens, window=20, first=3, sinks=sinks),
+        "decode_scaled": lambda: tb.kv4_decode(dq, *cache(), lens, scale=-0.25, softcap=9),
+        "first": lambda: tb.prefill(dq, ck, cv, window=16, first=4, sinks=sinks),
+        "first_lse": lambda: tb.prefill_lse(dq, ck, cv, window=16, first=4),
+    }
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", sorted(_calls("cpu")))
+def test_native_calls_give_the_python_codes_bits(name, monkeypatch):
+    call = _calls("cuda")[name]
+    tb.lib()
+    taken, native = [], tb._calls
+
+    class Recorded:
+        def __getattr__(self, attr):
+            def f(*a):
+                r = getattr(native, attr)(*a)
+                taken.append(r is not None)
+                return r
+            return f
+
+    monkeypatch.setattr(tb, "_calls", Recorded())
+    a = call()
+    # kv4_read without its rows is the Python code's
+    assert taken and (all(taken) or name == "read_rest")
+    monkeypatch.setattr(tb, "_calls", None)
+    b = call()
+    a, b = (x if isinstance(x, tuple) else (x,) for x in (a, b))
+    assert len(a) == len(b)
+    for x, y in zip(a, b):
+        assert x.dtype == y.dtype and x.shape == y.shape and x.stride() == y.stride()
+        bits = torch.int32 if x.dtype == torch.float32 else torch.int16 if x.dtype == torch.bfloat16 else x.dtype
+        assert torch.equal(x.view(bits), y.view(bits))
+
+
+def test_native_calls_leave_host_tensors_and_wrong_arguments_alone():
+    tb.lib()
+    q = _rows(0, 1, 1, 1, D)
+    assert tb._calls.rope(q, q, 0, q, None, None, 1e-6, False, 1.0, None, None) is None
+    assert tb._calls.rope(*[None] * 11) is None
+    assert tb._calls.rope_backward(*["x"] * 11) is None
+    assert tb._calls.append(*[q] * 7) is None
+    assert tb._calls.read(q, q, q, q, 0, 1) is None
+    assert tb._calls.decode(*[q] * 13) is None
+    assert tb._calls.prefill_first(*[q] * 12) is None
+    with pytest.raises(TypeError):
+        tb._calls.rope(q)
+
+
+@pytest.mark.gpu
+def test_native_calls_pass_statuses_and_refusals_on():
+    dev = "cuda"
+    tb.lib()
+    q, k = _rows(0, B, L, HQ, D).to(dev), _rows(1, B, L, HKV, D).to(dev)
+    freq, _ = tb.rope_inv_freq(24, device=dev)  # 24 channels: no multiple of 16
+    with pytest.raises(tb.TfaError) as e:
+        tb.qk_norm_rope(q, k, 0, freq)
+    assert e.value.code == tb.TFA_ERR_ROPE
+    freq, _ = tb.rope_inv_freq(D, device=dev)
+    with pytest.raises(tb.TfaError) as e:  # eps refused by the C call
+        tb.qk_norm_rope_backward(q.transpose(1, 2), k.transpose(1, 2), q, k, 0, freq,
+                                 q_weight=q[0, 0, 0], k_weight=k[0, 0, 0], eps=-1.0)
+    assert e.value.code == tb.TFA_ERR_ROPE
+    cache = tb.kv4_cache(B, HKV, CAP, D, device=dev)
+    rows = k.transpose(1, 2)
+    with pytest.raises(tb.TfaError):  # past the capacity
+        tb.kv4_append(rows, rows, *cache, start=CAP - 1)
+    with pytest.raises(tb.TfaError):
+        tb.kv4_decode(q.transpose(1, 2).contiguous(), *cache, torch.zeros(B, dtype=torch.int32, device=dev), first=1)
+    with pytest.raises(ValueError):  # the Python code's refusal
+        tb.kv4_decode(q.transpose(1, 2).contiguous(), *cache, torch.zeros(B + 1, dtype=torch.int32, device=dev))
+    with pytest.raises(tb.TfaError):
+        tb.prefill(q.transpose(1, 2).contiguous(), rows.contiguous(), rows.contiguous(), window=0, first=2)
+
+
+@pytest.mark.gpu
+def test_native_calls_on_a_stream_that_is_current():
+    """The current stream is the one a call runs on, and the one its outputs belong to."""
+    call = _calls("cuda")["decode"]
+    want = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = call()
+    side.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    q, c = _rows(8, B, HQ, L, D).cuda(), tb.kv4_cache(B, HKV, CAP, D, device="cuda")
+    lens = torch.full((B,), CAP, dtype=torch.int32, device="cuda")
+    tb.kv4_decode(q, *c, lens)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = tb.kv4_decode(q, *c, lens)
+    rows = _rows(9, B, HKV, CAP, D).cuda()
+    tb.kv4_append(rows, rows, *c, start=0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, tb.kv4_decode(q, *c, lens))
