@@ -153,7 +153,8 @@ def _load_calls(L):
                            "`python -m sliding_window_gqa_tfa_b200.build`") from e
     module.use(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
         "tfa_qk_norm_rope", "tfa_qk_norm_rope_backward", "tfa_qk_norm_rope_workspace", "tfa_kv4_append",
-        "tfa_kv4_read", "tfa_kv4_decode", "tfa_kv4_decode_workspace", "tfa_prefill_first")))
+        "tfa_kv4_read", "tfa_kv4_decode", "tfa_kv4_decode_workspace", "tfa_prefill_first",
+        "tfa_prefill_first_backward", "tfa_kv4_prefill", "tfa_kv4_prefill_workspace")))
     _calls = module
 
 
@@ -633,6 +634,10 @@ def _prefill_first(q, k, v, scale, causal, window, first, key_mask, softcap, sin
 
 def _backward_first(q, k, v, dout, scale, causal, window, first, key_mask, out, saved, stream):
     """(dq, dk, dv): backward with first tokens that stay visible, from saved (o, lse)."""
+    if _calls is not None and stream is None and out is None and causal:
+        made = _calls.backward_first(q, k, v, dout, *saved, scale, window, first, key_mask)
+        if made is not None:
+            return _native(made, "tfa_prefill_first_backward")
     dev, dims = _first_inputs(q, k, v, causal, key_mask)
     o, lse = saved
     for t, n in ((dout, "dout"), (o, "o")):
@@ -976,6 +981,10 @@ def kv4_prefill(q, k_codes, k_meta, v_codes, v_meta, *, S, scale=None, window=0,
     the 4-bit cache (the chunk's own rows last among them); window and first as for
     kv4_decode.  workspace: uint8 of tfa_kv4_prefill_workspace bytes, by default
     allocated here."""
+    if _calls is not None and stream is None:
+        made = _calls.prefill(q, k_codes, k_meta, v_codes, v_meta, S, scale, window, first, softcap, sinks, out, workspace)
+        if made is not None:
+            return _native(made, "tfa_kv4_prefill")
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
     _kv4_query(q, B, D, dev, sinks, out)
     Hq, L = q.shape[1], q.shape[2]

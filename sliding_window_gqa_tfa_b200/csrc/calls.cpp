@@ -13,7 +13,8 @@
 // The library's entry points come as addresses from the loaded library, so that there
 // is one copy of it.
 #include <climits>
-#include <utility>
+#include <cmath>
+#include <initializer_list>
 
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -34,6 +35,9 @@ struct Library {
     decltype(&tfa_kv4_decode) decode;
     decltype(&tfa_kv4_decode_workspace) decode_workspace;
     decltype(&tfa_prefill_first) first;
+    decltype(&tfa_prefill_first_backward) first_backward;
+    decltype(&tfa_kv4_prefill) prefill;
+    decltype(&tfa_kv4_prefill_workspace) prefill_workspace;
 } lib;
 
 // What is not a usual call; the functions turn it into None.
@@ -109,12 +113,19 @@ struct Strides {  // (batch, token, head) of [B, L, H, D] or [B, H, L, D] tensor
     void heads(const at::Tensor &t) { s[n] = t.stride(0), s[n + 1] = t.stride(2), s[n + 2] = t.stride(1), n += 3; }
 };
 
-PyObject *result(const at::Tensor &a, const at::Tensor &b) {
-    PyObject *x = THPVariable_Wrap(a), *y = THPVariable_Wrap(b);
-    PyObject *pair = x && y ? PyTuple_Pack(2, x, y) : nullptr;
-    Py_XDECREF(x);
-    Py_XDECREF(y);
-    return pair;
+PyObject *result(const at::Tensor &t) { return THPVariable_Wrap(t); }
+PyObject *result(std::initializer_list<at::Tensor> tensors) {  // a tuple; an undefined tensor is None
+    PyObject *all = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()));
+    Py_ssize_t i = 0;
+    for (const at::Tensor &t : tensors) {
+        PyObject *x = all ? THPVariable_Wrap(t) : nullptr;
+        if (!x) {
+            Py_XDECREF(all);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(all, i++, x);
+    }
+    return all;
 }
 
 template <typename F>
@@ -187,7 +198,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
                             r.wq, r.wk, static_cast<const double *>(r.freq.const_data_ptr()), r.pos, r.per_row, r.first,
                             r.B, r.L, r.Hq, r.Hkv, r.D, r.rot, inter, eps, mscale, stream);
         });
-        return rc == TFA_OK ? result(qo, ko) : PyLong_FromLong(rc);
+        return rc == TFA_OK ? result({qo, ko}) : PyLong_FromLong(rc);
     });
 }
 
@@ -216,12 +227,7 @@ PyObject *rope_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                      static_cast<const double *>(r.freq.const_data_ptr()), r.pos, r.per_row, r.first, r.B,
                                      r.L, r.Hq, r.Hkv, r.D, r.rot, inter, eps, mscale, space.mutable_data_ptr(), stream);
         });
-        if (rc != TFA_OK) return PyLong_FromLong(rc);
-        PyObject *rows_ = result(dq, dk), *weights = rows_ ? result(dwq, dwk) : nullptr;
-        PyObject *all = weights ? PySequence_Concat(rows_, weights) : nullptr;
-        Py_XDECREF(rows_);
-        Py_XDECREF(weights);
-        return all;
+        return rc == TFA_OK ? result({dq, dk, dwq, dwk}) : PyLong_FromLong(rc);
     });
 }
 
@@ -286,7 +292,7 @@ PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t n) {
                             k.mutable_data_ptr(), v.mutable_data_ptr(), start, first, c.B, c.Hkv, count, c.cap, c.D,
                             stream);
         });
-        return rc == TFA_OK ? result(k, v) : PyLong_FromLong(rc);
+        return rc == TFA_OK ? result({k, v}) : PyLong_FromLong(rc);
     });
 }
 
@@ -320,51 +326,110 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
                               o.mutable_data_ptr(), c.B, Hq, c.Hkv, L, c.cap, c.D, scale, window, first, softcap, sinks,
                               space.mutable_data_ptr(), stream);
         });
-        if (rc != TFA_OK) return PyLong_FromLong(rc);
-        return THPVariable_Wrap(o);
+        return rc == TFA_OK ? result(o) : PyLong_FromLong(rc);
     });
 }
+
+// q, the cache, S, scale, window, first, softcap, sinks, out, workspace
+PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 13, [&]() -> PyObject * {
+        const Cache c(a + 1);
+        const at::Tensor &q = whole(beside(c.kc, a[0], at::kBFloat16, 4));
+        need(q.size(0) == c.B && q.size(3) == c.D);
+        const int Hq = small(q.size(1)), L = small(q.size(2)), S = integer(a[5]);
+        const float scale = scale_or(a[6], c.D), softcap = number(a[9]);
+        const int window = integer(a[7]), first = integer(a[8]);
+        const float *sinks = sinks_of(a[10], q);
+        const at::Tensor o = given_or_empty(a[11], q, q.sizes());
+        const int64_t bytes = static_cast<int64_t>(lib.prefill_workspace(c.B, Hq, c.Hkv, L, S, c.D, window, first));
+        at::Tensor space;
+        if (a[12] == Py_None)
+            space = at::empty({bytes < 16 ? 16 : bytes}, c.kc.options());
+        else
+            need((space = whole(beside(q, a[12], at::kByte, 1))).size(0) >= bytes && space.size(0) >= 16);
+        const tfa_stream_t stream = stream_of(q);
+        const int rc = without_gil([&] {
+            return lib.prefill(q.const_data_ptr(), c.kc.const_data_ptr(), c.km.const_data_ptr(), c.vc.const_data_ptr(),
+                               c.vm.const_data_ptr(), o.mutable_data_ptr(), c.B, Hq, c.Hkv, L, S, c.cap, c.D, scale,
+                               window, first, softcap, sinks, space.mutable_data_ptr(), stream);
+        });
+        return rc == TFA_OK ? result(o) : PyLong_FromLong(rc);
+    });
+}
+
+// The dense tensors of attention with first tokens.
+struct First {
+    const at::Tensor &q, &k, &v;
+    int B, Hq, Hkv, L, S, D;
+    const float *mask = nullptr;
+    First(PyObject *q_, PyObject *k_, PyObject *v_, PyObject *mask_)
+        : q(whole(leading(q_, at::kBFloat16, 4))), k(whole(beside(q, k_, at::kBFloat16, 4))),
+          v(whole(beside(q, v_, at::kBFloat16, 4))) {
+        B = small(q.size(0)), Hq = small(q.size(1)), L = small(q.size(2)), D = small(q.size(3));
+        Hkv = small(k.size(1)), S = small(k.size(2));
+        need(k.size(0) == B && k.size(3) == D);
+        sized(v, k.sizes());
+        if (mask_ != Py_None)
+            mask = static_cast<const float *>(sized(whole(beside(q, mask_, at::kFloat, 2)), {B, S}).const_data_ptr());
+    }
+};
 
 // q, k, v, scale, window, first, key_mask, softcap, sinks, out, lse, want_lse
 PyObject *prefill_first(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 12, [&]() -> PyObject * {
-        const at::Tensor &q = whole(leading(a[0], at::kBFloat16, 4));
-        const at::Tensor &k = whole(beside(q, a[1], at::kBFloat16, 4)), &v = whole(beside(q, a[2], at::kBFloat16, 4));
-        const int B = small(q.size(0)), Hq = small(q.size(1)), L = small(q.size(2)), D = small(q.size(3));
-        const int Hkv = small(k.size(1)), S = small(k.size(2));
-        need(k.size(0) == B && k.size(3) == D);
-        sized(v, k.sizes());
-        const float scale = scale_or(a[3], D), softcap = number(a[7]);
+        const First d(a[0], a[1], a[2], a[6]);
+        const float scale = scale_or(a[3], d.D), softcap = number(a[7]);
         const int window = integer(a[4]), first = integer(a[5]);
-        const float *mask = nullptr, *sinks = sinks_of(a[8], q);
-        if (a[6] != Py_None)
-            mask = static_cast<const float *>(sized(whole(beside(q, a[6], at::kFloat, 2)), {B, S}).const_data_ptr());
+        const float *sinks = sinks_of(a[8], d.q);
         const int want = PyObject_IsTrue(a[11]);
         need(want >= 0);
-        const at::Tensor o = given_or_empty(a[9], q, q.sizes());
+        const at::Tensor o = given_or_empty(a[9], d.q, d.q.sizes());
         at::Tensor lse;
         if (a[10] != Py_None)
-            lse = sized(whole(beside(q, a[10], at::kFloat, 3)), {B, Hq, L});
+            lse = sized(whole(beside(d.q, a[10], at::kFloat, 3)), {d.B, d.Hq, d.L});
         else if (want)
-            lse = at::empty({B, Hq, L}, q.options().dtype(at::kFloat));
-        const tfa_stream_t stream = stream_of(q);
+            lse = at::empty({d.B, d.Hq, d.L}, d.q.options().dtype(at::kFloat));
+        const tfa_stream_t stream = stream_of(d.q);
         const int rc = without_gil([&] {
-            return lib.first(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), o.mutable_data_ptr(),
-                             lse.defined() ? static_cast<float *>(lse.mutable_data_ptr()) : nullptr, B, Hq, Hkv, L, S, D,
-                             scale, window, first, mask, softcap, sinks, stream);
+            return lib.first(d.q.const_data_ptr(), d.k.const_data_ptr(), d.v.const_data_ptr(), o.mutable_data_ptr(),
+                             lse.defined() ? static_cast<float *>(lse.mutable_data_ptr()) : nullptr, d.B, d.Hq, d.Hkv,
+                             d.L, d.S, d.D, scale, window, first, d.mask, softcap, sinks, stream);
         });
-        return rc == TFA_OK ? result(o, lse) : PyLong_FromLong(rc);  // (an undefined tensor is None)
+        return rc == TFA_OK ? result({o, lse}) : PyLong_FromLong(rc);
+    });
+}
+
+// q, k, v, dout, o, lse, scale, window, first, key_mask
+PyObject *backward_first(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> PyObject * {
+        const First d(a[0], a[1], a[2], a[9]);
+        const at::Tensor &dout = sized(whole(beside(d.q, a[3], at::kBFloat16, 4)), d.q.sizes());
+        const at::Tensor &o = sized(whole(beside(d.q, a[4], at::kBFloat16, 4)), d.q.sizes());
+        const at::Tensor &lse = sized(whole(beside(d.q, a[5], at::kFloat, 3)), {d.B, d.Hq, d.L});
+        const float scale = scale_or(a[6], d.D);
+        const int window = integer(a[7]), first = integer(a[8]);
+        const at::Tensor dq = at::empty(d.q.sizes(), d.q.options());
+        const at::Tensor dk = at::empty(d.k.sizes(), d.q.options()), dv = at::empty(d.k.sizes(), d.q.options());
+        const tfa_stream_t stream = stream_of(d.q);
+        const int rc = without_gil([&] {
+            return lib.first_backward(d.q.const_data_ptr(), d.k.const_data_ptr(), d.v.const_data_ptr(),
+                                      o.const_data_ptr(), static_cast<const float *>(lse.const_data_ptr()),
+                                      dout.const_data_ptr(), dq.mutable_data_ptr(), dk.mutable_data_ptr(),
+                                      dv.mutable_data_ptr(), d.B, d.Hq, d.Hkv, d.L, d.S, d.D, scale, window, first,
+                                      d.mask, stream);
+        });
+        return rc == TFA_OK ? result({dq, dk, dv}) : PyLong_FromLong(rc);
     });
 }
 
 // The library's addresses, in the order of Library.
 PyObject *use(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    void *at[8];
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "8 addresses wanted");
+    void *at[11];
+    if (n != 11) {
+        PyErr_SetString(PyExc_TypeError, "11 addresses wanted");
         return nullptr;
     }
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 11; ++i)
         if ((at[i] = PyLong_AsVoidPtr(a[i])) == nullptr && PyErr_Occurred()) return nullptr;
     lib.rope = reinterpret_cast<decltype(lib.rope)>(at[0]);
     lib.rope_backward = reinterpret_cast<decltype(lib.rope_backward)>(at[1]);
@@ -374,12 +439,15 @@ PyObject *use(PyObject *, PyObject *const *a, Py_ssize_t n) {
     lib.decode = reinterpret_cast<decltype(lib.decode)>(at[5]);
     lib.decode_workspace = reinterpret_cast<decltype(lib.decode_workspace)>(at[6]);
     lib.first = reinterpret_cast<decltype(lib.first)>(at[7]);
+    lib.first_backward = reinterpret_cast<decltype(lib.first_backward)>(at[8]);
+    lib.prefill = reinterpret_cast<decltype(lib.prefill)>(at[9]);
+    lib.prefill_workspace = reinterpret_cast<decltype(lib.prefill_workspace)>(at[10]);
     Py_RETURN_NONE;
 }
 
 #define CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {CALL(use),  CALL(rope),   CALL(rope_backward), CALL(append),
-                         CALL(read), CALL(decode), CALL(prefill_first), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {CALL(use),     CALL(rope),          CALL(rope_backward),  CALL(append), CALL(read), CALL(decode),
+                         CALL(prefill), CALL(prefill_first), CALL(backward_first), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

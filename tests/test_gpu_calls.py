@@ -23,6 +23,7 @@ def _calls(device):
     dq, dk = on(_rows(3, B, HQ, L, D)), on(_rows(4, B, HKV, L, D))
     ck, cv = on(_rows(5, B, HKV, CAP, D)), on(_rows(6, B, HKV, CAP, D))
     lens = on(torch.tensor([CAP, 0, 33], dtype=torch.int32))
+    long, long2 = on(_rows(8, B, HQ, 40, D)), on(_rows(9, B, HQ, 40, D))
     sinks = on(torch.randn(HQ, generator=torch.Generator().manual_seed(7)))
 
     def cache():
@@ -45,6 +46,10 @@ def _calls(device):
         "read_rest": lambda: tb.kv4_read(*cache(), start=60),
         "decode": lambda: tb.kv4_decode(dq, *cache(), lens, window=20, first=3, sinks=sinks),
         "decode_scaled": lambda: tb.kv4_decode(dq, *cache(), lens, scale=-0.25, softcap=9),
+        "prefill": lambda: tb.kv4_prefill(dq, *cache(), S=61, window=20, first=3, softcap=5.0),
+        "prefill_long": lambda: tb.kv4_prefill(long, *cache(), S=CAP),
+        "first_backward": lambda: tb.backward(long, ck, cv, long2, window=16, first=4,
+                                              saved=tb.prefill_lse(long, ck, cv, window=16, first=4)),
         "first": lambda: tb.prefill(dq, ck, cv, window=16, first=4, sinks=sinks),
         "first_lse": lambda: tb.prefill_lse(dq, ck, cv, window=16, first=4),
     }
@@ -88,7 +93,9 @@ def test_native_calls_leave_host_tensors_and_wrong_arguments_alone():
     assert tb._calls.append(*[q] * 7) is None
     assert tb._calls.read(q, q, q, q, 0, 1) is None
     assert tb._calls.decode(*[q] * 13) is None
+    assert tb._calls.prefill(*[q] * 13) is None
     assert tb._calls.prefill_first(*[q] * 12) is None
+    assert tb._calls.backward_first(*[q] * 10) is None
     with pytest.raises(TypeError):
         tb._calls.rope(q)
 
