@@ -58,30 +58,15 @@ struct AppendParams {
     unsigned *status;
 };
 
-// Both kernels: a lane takes 16 channels, half a group, so a row is D / 16 lanes;
-// blockIdx.y: K or V.  They should be bound by the bytes moved (2.625 a channel
-// each), which needs few instructions beside: 64-bit row indexes and their
-// divisions took longer than the rest of the kernel, IEEE divisions for the codes
-// as long again (4 x 2047 rows of 8 heads, append and read: 49.6 us, 35.3 us
-// without the 64-bit divisions).
-template <int D>
-__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
-    constexpr int LPR = D / 16;
-    const unsigned row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
-    const int lane = threadIdx.x % LPR;
-    const bool is_v = blockIdx.y != 0;
-    const bool in = row < p.n_rows;
-    const unsigned bh = in ? p.L.of(row) : 0u, i = in ? row - bh * p.L.d : 0u;
-    const unsigned b = p.Hkv.of(bh), h = bh - b * p.Hkv.d;
-    const long long *s = is_v ? p.sv : p.sk;
-    uint4 raw[2] = {};
-    if (in) {
-        const uint4 *src = reinterpret_cast<const uint4 *>((is_v ? p.v : p.k) + b * s[0] + h * s[1] + i * s[2] + lane * 16);
-        raw[0] = src[0];
-        raw[1] = src[1];
-    }
-    const long long first = p.start ? __ldg(p.start + b) : p.start0;
-    const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+// Both kernels: a lane takes 16 channels of K and of V, half a group, so a row is
+// D / 16 lanes.  They should be bound by the bytes moved (2.625 a channel each), which
+// needs few instructions beside (4 x 2047 rows of 8 heads, append and read: 49.6 us
+// with 64-bit row indexes and IEEE divisions for the codes, 22.2 us without, 18.5 us
+// with K and V found at once and packed arithmetic; the 88 MB would take 13.4).
+// The codes of a lane's 16 channels, a and b, and the word of the step and minimum of
+// the group that it shares with the lane beside it; every lane of the warp calls it.
+__device__ __forceinline__ unsigned long long encode(const uint4 &a, const uint4 &b, uint32_t &meta) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     // extremes two by two, NaN if any value is
     auto h2 = [](uint32_t x) { return *reinterpret_cast<__nv_bfloat162 *>(&x); };
     __nv_bfloat162 mn = h2(w[0]), mx = mn;
@@ -106,15 +91,19 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     };
     if (fine && step >= 0x1p-100f && step <= 0x1p100f) {
         const float inv = __frcp_rn(step);
+        const float2 inv2 = make_float2(inv, inv), step2 = make_float2(-step, -step), lo2 = make_float2(-lo, -lo);
         uint32_t half[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             half[j] = 0u;
 #pragma unroll
-            for (int e = 7; e >= 0; --e) {
-                const float d = value(8 * j + e), t = d * inv;
-                const float q = fmaf(fmaf(-t, step, d), inv, t) + 8388608.f;
-                half[j] = (half[j] << 4) + __float_as_uint(q);
+            for (int e = 3; e >= 0; --e) {
+                const uint32_t x = w[4 * j + e];
+                const float2 d = add2(make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), lo2);
+                const float2 t = mul2(d, inv2);
+                const float2 q = add2(fma2(fma2(t, step2, d), inv2, t), make_float2(8388608.f, 8388608.f));
+                half[j] = (half[j] << 4) + __float_as_uint(q.y);
+                half[j] = (half[j] << 4) + __float_as_uint(q.x);
             }
             half[j] -= 0xfb000000u;  // what the eight 0x4b000000 add up to: 0x4b000000 (1 + 16 + ...) mod 2^32
         }
@@ -124,6 +113,30 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
         for (int e = 0; e < 16; ++e)
             code |= static_cast<unsigned long long>(fminf(rintf(__fdiv_rn(value(e), step)), 15.f)) << (4 * e);
     }
+    meta = fine ? (__float_as_uint(step) >> 16) | (__float_as_uint(lo) & 0xffff0000u) : 0x7fc07fc0u;
+    return code;
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
+    constexpr int LPR = D / 16;
+    const unsigned row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const int lane = threadIdx.x % LPR;
+    const bool in = row < p.n_rows;
+    const unsigned bh = in ? p.L.of(row) : 0u, i = in ? row - bh * p.L.d : 0u;
+    const unsigned b = p.Hkv.of(bh), h = bh - b * p.Hkv.d;
+    uint4 k[2] = {}, v[2] = {};
+    if (in) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.k + b * p.sk[0] + h * p.sk[1] + i * p.sk[2] + lane * 16);
+        k[0] = src[0];
+        k[1] = src[1];
+        src = reinterpret_cast<const uint4 *>(p.v + b * p.sv[0] + h * p.sv[1] + i * p.sv[2] + lane * 16);
+        v[0] = src[0];
+        v[1] = src[1];
+    }
+    const long long first = p.start ? __ldg(p.start + b) : p.start0;
+    uint32_t km, vm;
+    const unsigned long long kc = encode(k[0], k[1], km), vc = encode(v[0], v[1], vm);
     if (!in || first < 0) return;  // a sequence without a place takes nothing
     const long long at = first + i;
     if (at >= p.cap) {
@@ -131,10 +144,12 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
         return;
     }
     const size_t dst = static_cast<size_t>(bh) * p.cap + at;
-    reinterpret_cast<unsigned long long *>(is_v ? p.c.vc : p.c.kc)[dst * LPR + lane] = code;
-    if ((lane & 1) == 0)
-        (is_v ? p.c.vm : p.c.km)[dst * (D / kGroup) + lane / 2] =
-            fine ? (__float_as_uint(step) >> 16) | (__float_as_uint(lo) & 0xffff0000u) : 0x7fc07fc0u;
+    reinterpret_cast<unsigned long long *>(p.c.kc)[dst * LPR + lane] = kc;
+    reinterpret_cast<unsigned long long *>(p.c.vc)[dst * LPR + lane] = vc;
+    if ((lane & 1) == 0) {
+        p.c.km[dst * (D / kGroup) + lane / 2] = km;
+        p.c.vm[dst * (D / kGroup) + lane / 2] = vm;
+    }
 }
 
 struct ReadParams {
@@ -162,31 +177,30 @@ __device__ __forceinline__ uint4 values8(uint32_t code, float s, float m) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// (A lane takes 8 channels here, so that a warp's store is one run of 512 bytes.)
 template <int D>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
-    constexpr int LPR = D / 16;
+    constexpr int LPR = D / 8;
     const unsigned row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
     const int lane = threadIdx.x % LPR;
     if (row >= p.n_rows) return;
-    const bool is_v = blockIdx.y != 0;
     const unsigned bh = p.rows.of(row), b = p.Hkv.of(bh);
     const int i = static_cast<int>(row - bh * p.rows.d);
     const long long first = p.start ? __ldg(p.start + b) : p.start0;
     const long long at = first + i + (i >= p.split ? p.skip : 0);
-    uint4 out[2] = {};
+    uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
     if (first >= 0 && at < p.cap) {
-        const size_t src = static_cast<size_t>(bh) * p.cap + at;
-        const uint2 code = __ldg(reinterpret_cast<const uint2 *>(is_v ? p.c.vc : p.c.kc) + src * LPR + lane);
-        const uint32_t meta = __ldg((is_v ? p.c.vm : p.c.km) + src * (D / kGroup) + lane / 2);
-        const float s = __uint_as_float(meta << 16), m = __uint_as_float(meta & 0xffff0000u);
-        out[0] = values8(code.x, s, m);
-        out[1] = values8(code.y, s, m);
+        const size_t src = static_cast<size_t>(bh) * p.cap + at, code = src * LPR + lane, word = src * (D / kGroup) + lane / 4;
+        const uint32_t kc = __ldg(reinterpret_cast<const uint32_t *>(p.c.kc) + code), km = __ldg(p.c.km + word);
+        const uint32_t vc = __ldg(reinterpret_cast<const uint32_t *>(p.c.vc) + code), vm = __ldg(p.c.vm + word);
+        k = values8(kc, __uint_as_float(km << 16), __uint_as_float(km & 0xffff0000u));
+        v = values8(vc, __uint_as_float(vm << 16), __uint_as_float(vm & 0xffff0000u));
     } else if (first >= 0 && lane == 0) {
         atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
     }
-    uint4 *dst = reinterpret_cast<uint4 *>((is_v ? p.v : p.k) + static_cast<size_t>(row) * D + lane * 16);
-    dst[0] = out[0];
-    dst[1] = out[1];
+    const size_t dst = static_cast<size_t>(row) * LPR + lane;
+    reinterpret_cast<uint4 *>(p.k)[dst] = k;
+    reinterpret_cast<uint4 *>(p.v)[dst] = v;
 }
 
 // --------------------------------------------------------------- host checks
@@ -208,7 +222,7 @@ unsigned row_blocks(long long rows, int D) {
 }
 
 int launch_read(const ReadParams &p, unsigned blocks, int D, cudaStream_t s) {
-    (D == 128 ? read_kernel<128> : read_kernel<64>)<<<dim3(blocks, 2), 256, 0, s>>>(p);
+    (D == 128 ? read_kernel<128> : read_kernel<64>)<<<2 * blocks, 256, 0, s>>>(p);  // twice an append's lanes a row
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? TFA_OK : report_cuda("kv4 read launch", e);
 }
@@ -256,14 +270,16 @@ int launch_decode(DecodeParams &p, int sms, cudaStream_t stream) {
     const int rows = p.chunks > 1 ? C::kRows : p.rows;
     const int items = p.B * p.Hkv * p.chunks * rows;
     cfg.gridDim = dim3(static_cast<unsigned>(items < 4 * sms ? items : 4 * sms));
-    cfg.blockDim = dim3(32 * kJoinWarps);
+    const int warps = grid >= 32 * p.B * p.Hkv * p.chunks ? 16 : 4;  // 32 pieces of a segment or more: join_row
+    cfg.blockDim = dim3(32 * warps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, join_kernel<D, NB>, p, grid, rows)) != cudaSuccess)
+    const auto join = warps == 16 ? join_kernel<D, NB, 16> : join_kernel<D, NB, 4>;
+    if ((e = cudaLaunchKernelEx(&cfg, join, p, grid, rows)) != cudaSuccess)
         return report_cuda("kv4 join launch", e);
     return TFA_OK;
 }
@@ -301,7 +317,7 @@ extern "C" int tfa_kv4_append(const void *k, const void *v, const long long *str
     p.Hkv = divisor(Hkv);
     p.L = divisor(L);
     p.cap = capacity;
-    (D == 128 ? append_kernel<128> : append_kernel<64>)<<<dim3(blocks, 2), 256, 0, s>>>(p);
+    (D == 128 ? append_kernel<128> : append_kernel<64>)<<<blocks, 256, 0, s>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? TFA_OK : tfa::report_cuda("kv4 append launch", e);
 }

@@ -786,16 +786,18 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB, REP>::kCtasPerSm)
     }
 }
 
-// One row of a segment, from its `cuts` pieces (0: zeros): a block's warps take every
-// fourth piece, a lane D / 32 channels; eight pieces' loads of each warp are in flight
-// together, as there may be as many pieces as CTAs (74 a segment for 8 segments).
-constexpr int kJoinWarps = 4;
+// One row of a segment, from its `cuts` pieces (0: zeros): a block's WARPS warps take
+// the pieces in turn, a lane D / 32 channels; eight pieces' loads of each warp are in
+// flight together.  Few rows may have as many pieces as there are CTAs (74 a segment
+// for 8 segments): 16 warps ask for them all at once (1 x 32768 positions of 8 heads 19.7 -> 18.8 us); many rows have few
+// pieces each, and blocks of 4 warps join more of them side by side.
+template <int WARPS>
 struct JoinShared {
-    float o[kJoinWarps][128], m[kJoinWarps], l[kJoinWarps];
+    float o[WARPS][128], m[WARPS], l[WARPS];
 };
 
-template <int D, int NB>
-__device__ __forceinline__ void join_row(const DecodeParams &p, JoinShared &sh, const float *slot0, int cuts, int row,
+template <int D, int NB, int WARPS>
+__device__ __forceinline__ void join_row(const DecodeParams &p, JoinShared<WARPS> &sh, const float *slot0, int cuts, int row,
                                          int head, __nv_bfloat16 *out) {
     using C = Cfg<D, NB>;
     constexpr int kVec = D / 32, kBatch = 8;
@@ -803,11 +805,11 @@ __device__ __forceinline__ void join_row(const DecodeParams &p, JoinShared &sh, 
     float mx = -CUDART_INF_F, sum = 0.f, a[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) a[i] = 0.f;
-    for (int k0 = warp; k0 < cuts; k0 += kJoinWarps * kBatch) {
+    for (int k0 = warp; k0 < cuts; k0 += WARPS * kBatch) {
         float mk[kBatch], lk[kBatch], v[kBatch][kVec];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int k = k0 + u * kJoinWarps;
+            const int k = k0 + u * WARPS;
             const float *s = slot0 + static_cast<size_t>(min(k, cuts - 1)) * C::kSlotFloats;
             mk[u] = k < cuts ? __ldcg(s + C::kRows * D + row) : -CUDART_INF_F;
             lk[u] = __ldcg(s + C::kRows * (D + 1) + row);
@@ -844,11 +846,11 @@ __device__ __forceinline__ void join_row(const DecodeParams &p, JoinShared &sh, 
     if (threadIdx.x < D / 2) {
         mx = -CUDART_INF_F;
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, sh.m[w]);
+        for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sh.m[w]);
         float x = 0.f, y = 0.f;
         sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             if (sh.m[w] == -CUDART_INF_F) continue;
             const float f = ex2(sh.m[w] - mx);
             sum = fmaf(f, sh.l[w], sum);
@@ -865,11 +867,11 @@ __device__ __forceinline__ void join_row(const DecodeParams &p, JoinShared &sh, 
 // Joins the pieces of the segments that were cut, row by row, and writes zeros for a
 // sequence without a position.  Few blocks, each working out the deal once: they can
 // be there before the main kernel ends.
-template <int D, int NB>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ DecodeParams p, int grid, int rows) {
+template <int D, int NB, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) join_kernel(const __grid_constant__ DecodeParams p, int grid, int rows) {
     using C = Cfg<D, NB>;
     __shared__ int shared[2 * kMaxSeqs + 1];
-    __shared__ JoinShared sh;
+    __shared__ JoinShared<WARPS> sh;
     const Deal deal(p, grid, shared, false);  // the lengths are the caller's: no need to wait for them
     grid_dep_wait();
     for (int item = blockIdx.x; item < p.B * deal.HC * rows; item += gridDim.x) {
@@ -879,7 +881,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
         const int cuts = deal.pieces_of(b);  // 0: a sequence without a position
         if (first >= p.rows || cuts == 1) continue;  // (one piece: finished where it was computed)
         const size_t at = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.L + first;
-        join_row<D, NB>(p, sh, p.part + static_cast<size_t>(deal.begin(b) + hc * cuts) * C::kSlotFloats, cuts, row,
+        join_row<D, NB, WARPS>(p, sh, p.part + static_cast<size_t>(deal.begin(b) + hc * cuts) * C::kSlotFloats, cuts, row,
                         h * p.G + first / p.L, p.o + at * D);
     }
 }
