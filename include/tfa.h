@@ -273,6 +273,7 @@ int tfa_prefill_backward_saved(const void *q, const void *k, const void *v, cons
  *                 b is at positions[b] + i), [B, L] with positions_per_row != 0;
  *                 NULL: row i of every sequence is at first_position + i
  *   rot           rotated channels, a multiple of 16 in [0, D]; 0: norms only
+ *   Hq, Hkv       1 to 65536; B L at most 2^30
  *   interleaved   0: pair i is channels (i, i + rot / 2); else (2i, 2i + 1)
  * Device pointers 16-byte aligned (inv_freq 8, positions 4).  Hq need not be a
  * multiple of Hkv here.  Asynchronous on `stream`, no workspace, capturable
@@ -374,9 +375,11 @@ int tfa_kv4_read(const void *k_codes, const void *k_meta, const void *v_codes, c
  *   workspace device memory of tfa_kv4_decode_workspace(Hq, Hkv, L, D) bytes,
  *             16-byte aligned; not shared by calls that overlap
  * The codes enter the products exactly; the softmax weights times a step are
- * rounded to bf16.  Asynchronous on `stream`; after one call on the device
- * (which creates its status word) it may be captured, and each replay reads the
- * lengths anew. */
+ * rounded to fp16, against a power of two above the steps seen: a term below
+ * 2^-30 of the largest may be lost, and steps of V are taken to lie in [2^-40,
+ * 2^80], channels of q in [-2^100, 2^100] (those 2^-28 below a row's largest lose
+ * bits).  Asynchronous on `stream`; after one call on the device (which creates
+ * its status word) it may be captured, and each replay reads the lengths anew. */
 int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_meta, const void *v_codes, const void *v_meta,
                    const int *lens, void *o, int B, int Hq, int Hkv, int L, int capacity, int D,
                    float scale, int window, int first, float softcap, const float *sinks,
@@ -384,8 +387,8 @@ int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_meta, const
 size_t tfa_kv4_decode_workspace(int Hq, int Hkv, int L, int D);
 
 /* tfa_kv4_prefill -- the same attention for chunks of any L >= 1 rows, every
- * sequence with S cached positions (L <= S <= capacity, else TFA_ERR_CACHE).  A chunk
- * of few rows takes tfa_kv4_decode's kernel; for the others the positions that some
+ * sequence with S cached positions (L <= S, else TFA_ERR_SHAPE; S <= capacity, else
+ * TFA_ERR_CACHE).  A chunk of few rows takes tfa_kv4_decode's kernel; for the others the positions that some
  * row sees are brought back to bf16 in the workspace and the dense kernel runs on
  * them (scratch and graph capture as for tfa_prefill).  workspace: device memory of
  * tfa_kv4_prefill_workspace(B, Hq, Hkv, L, S, D, window, first) bytes, 16-byte

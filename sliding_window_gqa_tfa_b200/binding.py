@@ -560,6 +560,13 @@ def _scope(index, stream):
 _current_device = torch.cuda.current_device
 
 
+def _int32(x, name):
+    """x, which a C call takes as an int; ctypes would drop the bits that do not fit."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit in 32 bits")
+    return x
+
+
 def _check_on(t, name, dtype, ndim, index=None, rows=False):
     """Checks a CUDA tensor's type, dimensions and device (`index`, or any); rows: any
     strides, as long as the last dimension is contiguous (else all of it must be)."""
@@ -580,7 +587,7 @@ def _check_on(t, name, dtype, ndim, index=None, rows=False):
     raise ValueError(f"{name} must have a contiguous last dimension" if rows else f"{name} must be contiguous")
 
 
-def _first_inputs(q, k, v, causal, key_mask):
+def _first_inputs(q, k, v, causal, window, first, key_mask):
     _check_on(q, "q", _BF16, 4)
     dev = q.get_device()
     _check_on(k, "k", _BF16, 4, dev)
@@ -595,6 +602,8 @@ def _first_inputs(q, k, v, causal, key_mask):
             raise ValueError("key_mask must be [B, S]")
     if not causal:
         raise ValueError("first tokens need causal attention with a window")
+    _int32(window, "window")
+    _int32(first, "first")
     return dev, (B, Hq, kv[1], L, kv[2], D)
 
 
@@ -604,7 +613,7 @@ def _prefill_first(q, k, v, scale, causal, window, first, key_mask, softcap, sin
         made = _calls.prefill_first(q, k, v, scale, window, first, key_mask, softcap, sinks, out, lse, want_lse)
         if made is not None:
             return _native(made, "tfa_prefill_first")
-    dev, dims = _first_inputs(q, k, v, causal, key_mask)
+    dev, dims = _first_inputs(q, k, v, causal, window, first, key_mask)
     if sinks is not None:
         _check_on(sinks, "sinks", _F32, 1, dev)
         if sinks.shape[0] != dims[1]:
@@ -638,7 +647,7 @@ def _backward_first(q, k, v, dout, scale, causal, window, first, key_mask, out, 
         made = _calls.backward_first(q, k, v, dout, *saved, scale, window, first, key_mask)
         if made is not None:
             return _native(made, "tfa_prefill_first_backward")
-    dev, dims = _first_inputs(q, k, v, causal, key_mask)
+    dev, dims = _first_inputs(q, k, v, causal, window, first, key_mask)
     o, lse = saved
     for t, n in ((dout, "dout"), (o, "o")):
         _check_on(t, n, _BF16, 4, dev)
@@ -713,7 +722,7 @@ def _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight):
         raise ValueError("q_weight and k_weight must be given together")
     per_row, first, ptr = 0, 0, None
     if isinstance(positions, int):
-        first = positions
+        first = _int32(positions, "positions")
     else:
         per_row = 1 if isinstance(positions, torch.Tensor) and positions.dim() == 2 else 0
         _check_on(positions, "positions", _I32, 1 + per_row, dev)
@@ -857,7 +866,7 @@ def _kv4_check(k_codes, k_meta, v_codes, v_meta):
 def _kv4_start(start, B, dev):
     """(device pointer or None, first row) of an int or int32 [B]."""
     if isinstance(start, int):
-        return None, start
+        return None, _int32(start, "start")
     _check_on(start, "start", _I32, 1, dev)
     if start.shape[0] != B:
         raise ValueError("start must hold one row per sequence")
@@ -904,6 +913,7 @@ def kv4_read(k_codes, k_meta, v_codes, v_meta, *, start=0, rows=None, out=None, 
         if ptr is not None:
             raise ValueError("rows must be given with a start for each sequence")
         rows = cap - first
+    _int32(rows, "rows")
     with _scope(dev, stream):
         if out is None:
             out = k_meta.new_empty((B, Hkv, rows, D)), k_meta.new_empty((B, Hkv, rows, D))
@@ -960,6 +970,7 @@ def kv4_decode(q, k_codes, k_meta, v_codes, v_meta, lens, *, scale=None, window=
     if lens.shape[0] != B:
         raise ValueError("lens must hold one length per sequence")
     Hq, L = q.shape[1], q.shape[2]
+    window, first = _int32(window, "window"), _int32(first, "first")
     with _scope(dev, stream):
         if out is None:
             out = torch.empty_like(q)
@@ -987,7 +998,9 @@ def kv4_prefill(q, k_codes, k_meta, v_codes, v_meta, *, S, scale=None, window=0,
             return _native(made, "tfa_kv4_prefill")
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
     _kv4_query(q, B, D, dev, sinks, out)
+    _int32(S, "S")
     Hq, L = q.shape[1], q.shape[2]
+    window, first = _int32(window, "window"), _int32(first, "first")
     with _scope(dev, stream):
         if out is None:
             out = torch.empty_like(q)

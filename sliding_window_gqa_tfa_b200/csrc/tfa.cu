@@ -871,6 +871,7 @@ extern "C" int tfa_prefill_first(const void *q, const void *k, const void *v, vo
     int rc = validate(q, k, v, o, B, Hq, Hkv, L, S, D, scale, 1, window, key_mask, true, decode);
     if (rc) return rc;
     if (window <= 0 || first < 0) return TFA_ERR_WINDOW;
+    window = window < S ? window : S;  // the same positions; sums of it stay in range
     if (!std::isfinite(softcap) || softcap < 0.f || (softcap > 0.f && scale == 0.f) || (lse && (softcap > 0.f || sinks)))
         return TFA_ERR_SOFTCAP;
     if ((reinterpret_cast<uintptr_t>(sinks) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return TFA_ERR_ALIGN;
@@ -897,6 +898,7 @@ extern "C" int tfa_prefill_first_backward(const void *q, const void *k, const vo
     if (rc) return rc;
     if (!o || !lse || !dq || !dk || !dv) return TFA_ERR_NULL;
     if (window <= 0 || first < 0) return TFA_ERR_WINDOW;
+    window = window < S ? window : S;  // the same positions; sums of it stay in range
     auto mis16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; };
     if (mis16(o) || mis16(dq) || mis16(dk) || mis16(dv) || (reinterpret_cast<uintptr_t>(lse) & 3u))
         return TFA_ERR_ALIGN;

@@ -644,6 +644,11 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB, REP>::kCtasPerSm)
             {
                 uint32_t w[C::kGroups], high = 0u;
                 lds_words(vmeta + lane * C::kMetaBytes, w);
+                // a row that none of the queries sees bounds nothing
+                if (edge && p.window > 0 && key0 + lane <= p0 - static_cast<long long>(p.window) && key0 + lane >= p.first) {
+#pragma unroll
+                    for (int gr = 0; gr < C::kGroups; ++gr) w[gr] = 0u;
+                }
 #pragma unroll
                 for (int gr = 0; gr < C::kGroups; ++gr) high = max(high, w[gr] & 0x7fffu);
                 if (__any_sync(0xffffffffu, high > highest)) {

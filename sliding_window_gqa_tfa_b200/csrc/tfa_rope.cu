@@ -433,8 +433,8 @@ __global__ void __launch_bounds__(256) weight_kernel(const float *partial, int q
 
 int check(const Params &p, int D) {
     if (p.Hq < 1 || p.Hkv < 1) return TFA_ERR_HEADS;
-    if (p.B < 1 || p.L < 1 || static_cast<long long>(p.B) * p.L > (1ll << 30) || p.Hq > (1 << 20) ||
-        p.Hkv > (1 << 20))
+    if (p.B < 1 || p.L < 1 || static_cast<long long>(p.B) * p.L > (1ll << 30) || p.Hq > (1 << 16) ||
+        p.Hkv > (1 << 16))
         return TFA_ERR_SHAPE;
     if (D != 64 && D != 128) return TFA_ERR_HEAD_DIM;
     if (p.rot < 0 || p.rot > D || p.rot % 16 != 0 || !std::isfinite(p.eps) || p.eps < 0.f || !std::isfinite(p.mscale))

@@ -127,6 +127,23 @@ def test_native_calls_pass_statuses_and_refusals_on():
 
 
 @pytest.mark.gpu
+def test_integers_that_do_not_fit_are_refused():
+    """A C call's int would drop their upper bits: start 2^32 would write row 0."""
+    c = tb.kv4_cache(1, 1, 64, D, device="cuda")
+    rows, freq = _rows(0, 1, 1, 2, D).cuda(), tb.rope_inv_freq(D, device="cuda")[0]
+    lens = torch.ones(1, dtype=torch.int32, device="cuda")
+    big = 2 ** 32 + 5
+    for call in (lambda: tb.kv4_append(rows, rows, *c, start=big), lambda: tb.kv4_read(*c, start=big, rows=1),
+                 lambda: tb.kv4_read(*c, rows=big), lambda: tb.kv4_decode(rows, *c, lens, window=big),
+                 lambda: tb.kv4_decode(rows, *c, lens, window=9, first=big),
+                 lambda: tb.kv4_prefill(rows, *c, S=big), lambda: tb.qk_norm_rope(rows, rows, -big, freq),
+                 lambda: tb.prefill(rows, rows, rows, window=big, first=2),
+                 lambda: tb.prefill_lse(rows, rows, rows, window=4, first=big)):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.gpu
 def test_native_calls_on_a_stream_that_is_current():
     """The current stream is the one a call runs on, and the one its outputs belong to."""
     call = _calls("cuda")["decode"]

@@ -98,6 +98,7 @@ CASES = [
     ("cut_key_tiles", 2, 4, 2, 1500, 1500, 128, 100, 4),
     ("two_cut_tiles_prefix", 1, 3, 1, 1200, 4000, 64, 128, 200),
     ("uncut_tiles", 1, 2, 1, 900, 900, 128, 100, 600),
+    ("window_int_max", 1, 4, 2, 300, 700, 128, 2 ** 31 - 1, 2 ** 31 - 1),
     ("most_parts", 1, 1, 1, 9000, 9000, 64, 1, 1),
 ]
 IDS = [c[0] for c in CASES]

@@ -3,8 +3,10 @@
 
 Tolerances, from the roundings.  Writing is exact: steps, minima and codes are
 those of the definition.  Reading rounds c s + m once in fp32 and once to bf16.
-Decoding rounds p s to bf16 (2^-8 of each term of sum_j w_j s c_j) and the output
-to bf16 (2^-8); the scores' fp32 sums are of at most 143 s sum|q| a group, in fewer
+Decoding rounds p s to fp16 (less than 2^-8 of each term of sum_j w_j s c_j; the dense
+kernel that longer chunks take rounds p and the values to bf16, 2^-8) and the output
+to bf16 (2^-8); the sum of a group's q is held in two bf16 (2^-17 of the minimum's
+part of the score: inside delta); the scores' fp32 sums are of at most 143 s sum|q| a group, in fewer
 than 64 additions of 2^-24 each (2^-18 of that), which moves the weights by twice
 the scores' error delta: |err| <= 2^-8 (sum_j w_j s c_j + |o|) + 2 delta sum_j w_j |v_j - o|,
 the last sum at most max|v| + |o|.
@@ -268,6 +270,21 @@ def test_what_is_hidden_does_not_reach_the_output():
         bad[which][:, :, cap - L - W + 1] = float("inf")
         got = tb.kv4_decode(q, *bad, n, window=W, first=F)
         assert torch.equal(got[:, :, 1:], clean[:, :, 1:])
+
+
+def test_a_large_step_that_no_row_sees_takes_no_bits():
+    """V's steps bound the fp16 products' range; one of 2^60 just outside the window, in
+    a step of 32 positions that the window begins in, is none of them."""
+    B, Hq, Hkv, D, cap, W, F = 1, 4, 2, 128, 400, 50, 6
+    gen = _gen(12)
+    cache = cache_of(_randn(gen, B, Hkv, cap, D).bfloat16(), _randn(gen, B, Hkv, cap, D).bfloat16(), cap)
+    n = torch.tensor([cap], dtype=torch.int32, device="cuda")
+    for L in (1, 3, 8):
+        q = _randn(gen, B, Hq, L, D).bfloat16()
+        clean = tb.kv4_decode(q, *cache, n, window=W, first=F)
+        bad = [t.clone() for t in cache]
+        bad[3][:, :, F:cap - L - W + 1, :, 0] = 2.0 ** 60
+        assert torch.equal(tb.kv4_decode(q, *bad, n, window=W, first=F), clean)
 
 
 def test_lengths_out_of_range_are_reported_and_give_zeros():
