@@ -15,4 +15,23 @@ int report_cuda(const char *what, cudaError_t e);
 // call's (TFA_ERR_CAPTURE if that would happen inside a graph capture).
 int device_info(cudaStream_t stream, unsigned **status, int *sm_count);
 
+// Launches a kernel that may be set up while the stream's previous one still ends: it
+// calls grid_dep_wait before it touches memory, and grid_dep_launch only then, so that
+// a kernel after it never starts before the one before it has ended.
+template <typename... Args, typename... Given>
+cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         Given... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Args(args)...);
+}
+
 }  // namespace tfa

@@ -125,6 +125,8 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     const bool in = row < p.n_rows;
     const unsigned bh = in ? p.L.of(row) : 0u, i = in ? row - bh * p.L.d : 0u;
     const unsigned b = p.Hkv.of(bh), h = bh - b * p.Hkv.d;
+    grid_dep_wait();
+    grid_dep_launch();
     uint4 k[2] = {}, v[2] = {};
     if (in) {
         const uint4 *src = reinterpret_cast<const uint4 *>(p.k + b * p.sk[0] + h * p.sk[1] + i * p.sk[2] + lane * 16);
@@ -183,9 +185,11 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
     constexpr int LPR = D / 8;
     const unsigned row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
     const int lane = threadIdx.x % LPR;
-    if (row >= p.n_rows) return;
     const unsigned bh = p.rows.of(row), b = p.Hkv.of(bh);
     const int i = static_cast<int>(row - bh * p.rows.d);
+    grid_dep_wait();
+    grid_dep_launch();
+    if (row >= p.n_rows) return;
     const long long first = p.start ? __ldg(p.start + b) : p.start0;
     const long long at = first + i + (i >= p.split ? p.skip : 0);
     uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
@@ -222,8 +226,8 @@ unsigned row_blocks(long long rows, int D) {
 }
 
 int launch_read(const ReadParams &p, unsigned blocks, int D, cudaStream_t s) {
-    (D == 128 ? read_kernel<128> : read_kernel<64>)<<<2 * blocks, 256, 0, s>>>(p);  // twice an append's lanes a row
-    const cudaError_t e = cudaGetLastError();
+    // twice an append's lanes a row
+    const cudaError_t e = launch_after(D == 128 ? read_kernel<128> : read_kernel<64>, 2 * blocks, 256, 0, s, p);
     return e == cudaSuccess ? TFA_OK : report_cuda("kv4 read launch", e);
 }
 
@@ -264,22 +268,14 @@ int launch_decode(DecodeParams &p, int sms, cudaStream_t stream) {
         prepared[dev].store(true, std::memory_order_release);
     }
     const int grid = sms * C::kCtasPerSm < kMaxCtas / NB ? sms * C::kCtasPerSm : kMaxCtas / NB;
-    decode_kernel<D, NB, REP><<<grid, 32 * kWarps, C::kSmemBytes, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda("kv4 decode launch", e);
-    cudaLaunchConfig_t cfg = {};
+    e = launch_after(decode_kernel<D, NB, REP>, grid, 32 * kWarps, C::kSmemBytes, stream, p);
+    if (e != cudaSuccess) return report_cuda("kv4 decode launch", e);
     const int rows = p.chunks > 1 ? C::kRows : p.rows;
     const int items = p.B * p.Hkv * p.chunks * rows;
-    cfg.gridDim = dim3(static_cast<unsigned>(items < 4 * sms ? items : 4 * sms));
     const int warps = grid >= 32 * p.B * p.Hkv * p.chunks ? 16 : 4;  // 32 pieces of a segment or more: join_row
-    cfg.blockDim = dim3(32 * warps);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const auto join = warps == 16 ? join_kernel<D, NB, 16> : join_kernel<D, NB, 4>;
-    if ((e = cudaLaunchKernelEx(&cfg, join, p, grid, rows)) != cudaSuccess)
+    e = launch_after(warps == 16 ? join_kernel<D, NB, 16> : join_kernel<D, NB, 4>, items < 4 * sms ? items : 4 * sms,
+                     32 * warps, 0, stream, p, grid, rows);
+    if (e != cudaSuccess)
         return report_cuda("kv4 join launch", e);
     return TFA_OK;
 }
@@ -317,8 +313,7 @@ extern "C" int tfa_kv4_append(const void *k, const void *v, const long long *str
     p.Hkv = divisor(Hkv);
     p.L = divisor(L);
     p.cap = capacity;
-    (D == 128 ? append_kernel<128> : append_kernel<64>)<<<blocks, 256, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = tfa::launch_after(D == 128 ? append_kernel<128> : append_kernel<64>, blocks, 256, 0, s, p);
     return e == cudaSuccess ? TFA_OK : tfa::report_cuda("kv4 append launch", e);
 }
 

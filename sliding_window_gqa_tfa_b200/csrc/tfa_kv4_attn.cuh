@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB, REP>::kCtasPerSm)
     using C = Cfg<D, NB, REP>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int shared[2 * kMaxSeqs + 1];
+    grid_dep_wait();
     grid_dep_launch();  // the joining kernel may be set up meanwhile; it waits for this one's end
     const Deal deal(p, gridDim.x, shared, blockIdx.x == 0);
 
@@ -877,8 +878,10 @@ __global__ void __launch_bounds__(32 * WARPS) join_kernel(const __grid_constant_
     using C = Cfg<D, NB>;
     __shared__ int shared[2 * kMaxSeqs + 1];
     __shared__ JoinShared<WARPS> sh;
-    const Deal deal(p, grid, shared, false);  // the lengths are the caller's: no need to wait for them
+    // the lengths are there: the main kernel lets this one start after its own wait
+    const Deal deal(p, grid, shared, false);
     grid_dep_wait();
+    grid_dep_launch();
     for (int item = blockIdx.x; item < p.B * deal.HC * rows; item += gridDim.x) {
         const int segment = item / rows, row = item - segment * rows;
         const int b = segment / deal.HC, hc = segment - b * deal.HC;

@@ -172,6 +172,8 @@ __global__ void __launch_bounds__(kThreads, 5) forward_kernel(const __grid_const
     const __nv_bfloat16 *k = p.k + b * p.sk.b + l * p.sk.l;
     __nv_bfloat16 *qo = p.qo + b * p.sqo.b + l * p.sqo.l;
     __nv_bfloat16 *ko = p.ko + b * p.sko.b + l * p.sko.l;
+    grid_dep_wait();
+    grid_dep_launch();
     // the first rows are on their way while the table is computed
     constexpr int kAhead = 2;
     uint2 xa[kAhead], xb[kAhead];
@@ -267,6 +269,8 @@ __device__ __forceinline__ void backward_block(const Params &p, int block, int b
     const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
     const int sub = slot / kHeads, h0 = slot % kHeads;
     const Channels ch(p, lane);
+    grid_dep_wait();
+    grid_dep_launch();
     const Eight w = load_eight(ISQ ? p.wq : p.wk, ch);
     Eight acc = {};
 
@@ -328,7 +332,6 @@ __device__ __forceinline__ void backward_block(const Params &p, int block, int b
         fill += kRows * 2 * kThreads * 16;
         if (fill == fill_end) fill -= kRingBytes;
     };
-    grid_dep_launch();
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch();
     angles(t0, 0);
@@ -419,6 +422,7 @@ __global__ void __launch_bounds__(256) weight_kernel(const float *partial, int q
     const bool isq = col < D;
     const int c = isq ? col : col - D, end = isq ? q_blocks : blocks;
     grid_dep_wait();
+    grid_dep_launch();
     float sum = 0.f;
 #pragma unroll 8
     for (int i = (isq ? 0 : q_blocks) + s; i < end; i += 32) sum += __ldcg(partial + static_cast<size_t>(i) * D + c);
@@ -464,8 +468,7 @@ int launch_forward(Params &p, int D, cudaStream_t stream) {
         return norm ? (inter ? forward_kernel<64, true, true> : forward_kernel<64, true, false>)
                     : (inter ? forward_kernel<64, false, true> : forward_kernel<64, false, false>);
     };
-    pick(p.inter != 0)<<<grid, kThreads, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(pick(p.inter != 0), grid, kThreads, 0, stream, p);
     return e == cudaSuccess ? TFA_OK : report_cuda("qk_norm_rope launch", e);
 }
 
@@ -494,19 +497,9 @@ int launch_backward(Params &p, int D, float *dwq, float *dwk, cudaStream_t strea
         if (e != cudaSuccess) return report_cuda("cudaFuncSetAttribute(norm gradient smem)", e);
         ready.store(true, std::memory_order_release);
     }
-    kern<<<blocks, kThreads, kRingBytes, stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_after(kern, blocks, kThreads, kRingBytes, stream, p);
     if (e != cudaSuccess) return report_cuda("qk_norm_rope gradient launch", e);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * D / 8);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];  // set up while the first kernel runs, which it waits for
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, weight_kernel, static_cast<const float *>(p.partial), p.q_blocks, blocks, D, dwq, dwk);
+    e = launch_after(weight_kernel, 2 * D / 8, 256, 0, stream, p.partial, p.q_blocks, blocks, D, dwq, dwk);
     return e == cudaSuccess ? TFA_OK : report_cuda("norm weight gradient launch", e);
 }
 
