@@ -537,6 +537,10 @@ int launch(DeviceState &st, const void *q, const void *k, const void *v, void *o
         p.ready = nullptr;
         p.ctl = nullptr;
     }
+    if (first) {
+        const cudaError_t e = tfa::launch_after(kern, sh.grid, tfa::kThreads, smem, stream, mq, mk, mv, p);
+        return e == cudaSuccess ? TFA_OK : cuda_fail("kernel launch", e);
+    }
     kern<<<sh.grid, tfa::kThreads, smem, stream>>>(mq, mk, mv, p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? TFA_OK : cuda_fail("kernel launch", e);
@@ -724,9 +728,13 @@ int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void 
     }
     const long long rows = static_cast<long long>(B) * Hq * L;
     const long long threads = rows * 32;
-    bw::delta_kernel<D><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(
-        static_cast<const __nv_bfloat16 *>(o), static_cast<const __nv_bfloat16 *>(dout), bs.delta, rows);
-    cudaError_t e = cudaGetLastError();
+    const unsigned delta_grid = static_cast<unsigned>((threads + 255) / 256);
+    const auto *ob = static_cast<const __nv_bfloat16 *>(o), *dob = static_cast<const __nv_bfloat16 *>(dout);
+    cudaError_t e = cudaSuccess;
+    if (first)
+        e = tfa::launch_after(bw::delta_kernel<D>, delta_grid, 256, 0, stream, ob, dob, bs.delta, rows);
+    else
+        bw::delta_kernel<D><<<delta_grid, 256, 0, stream>>>(ob, dob, bs.delta, rows), e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("delta kernel launch", e);
     CUtensorMap mq, mdo, mk, mv;
     if (encode_map(&mq, q, L, B * Hq, D) || encode_map(&mdo, dout, L, B * Hq, D) ||
@@ -760,9 +768,12 @@ int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void 
         return reinterpret_cast<Kern>(const_cast<void *>(tfa::first_backward_kernel(D, key_mask != nullptr, keys)));
     };
     const Kern dq_kern = first ? first_kern(false) : key_mask ? Kern(bw::dq_kernel<D, true>) : Kern(bw::dq_kernel<D, false>);
-    dq_kern<<<static_cast<int>(nq_items < st.sm_count ? nq_items : st.sm_count), bw::kThreads, smem, stream>>>(
-        mq, mdo, mk, mv, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail("dQ kernel launch", e);
+    const int dq_grid = static_cast<int>(nq_items < st.sm_count ? nq_items : st.sm_count);
+    if (first)
+        e = tfa::launch_after(dq_kern, dq_grid, bw::kThreads, smem, stream, mq, mdo, mk, mv, p);
+    else
+        dq_kern<<<dq_grid, bw::kThreads, smem, stream>>>(mq, mdo, mk, mv, p), e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail("dQ kernel launch", e);
     const FirstCut cut = first_cut(L, S, p.window, first);
     p.cut_tiles = cut.tiles;
     p.parts = cut.parts;
@@ -788,9 +799,8 @@ int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void 
         return cuda_fail("dK/dV kernel launch", e);
     if (cut.tiles) {
         const dim3 grid(static_cast<unsigned>(B) * Hkv, (cut.tiles * 128 * (D / 4) + 255) / 256, 2);
-        reinterpret_cast<void (*)(const bw::BwdParams)>(const_cast<void *>(tfa::first_sum_parts_kernel(D)))
-            <<<grid, 256, 0, stream>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail("partial sums kernel launch", e);
+        const auto sum = reinterpret_cast<void (*)(const bw::BwdParams)>(const_cast<void *>(tfa::first_sum_parts_kernel(D)));
+        if ((e = tfa::launch_after(sum, grid, 256, 0, stream, p)) != cudaSuccess) return cuda_fail("partial sums kernel launch", e);
     }
     return TFA_OK;
 }

@@ -115,6 +115,8 @@ __global__ void __launch_bounds__(256) delta_kernel(const __nv_bfloat16 *o, cons
                                                     float *delta, long long rows) {
     const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
+    grid_dep_wait();  // (with first tokens: launch_after)
+    grid_dep_launch();
     if (row >= rows) return;
     constexpr int kPer = D / 32;  // elements per lane: 4 (D = 128) or 2 (D = 64)
     const __nv_bfloat16 *po = o + row * D + lane * kPer;
@@ -223,6 +225,8 @@ __device__ __forceinline__ float *part_at(const BwdParams &p, int kt, int b, int
 // thread; grid: B Hkv, the cut tiles' rows in blocks, dV and dK.
 template <int D>
 __global__ void __launch_bounds__(256) sum_parts_kernel(const BwdParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
     const int i = blockIdx.y * 256 + threadIdx.x;  // over cut_tiles x 128 rows x D / 4
     const int row = i / (D / 4), c4 = i % (D / 4), kt = row / kBlockK, key = row;
     if (kt >= p.cut_tiles || key >= p.S) return;
@@ -364,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const BwdParams p) {
     using C = Cfg<D>;
     const Setup<D> st = setup<D>(&tm_q, &tm_do, &tm_k, &tm_v);
+    if (FIRST) grid_dep_wait();  // launch_after
     // The dK/dV kernel reads none of this kernel's output: it may take over
     // each SM as soon as this kernel's CTA there retires.
     if (threadIdx.x == 0) grid_dep_launch();

@@ -1221,6 +1221,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (LY == kLayoutFirst) {  // launched while the stream's previous kernel ends (launch_after)
+        grid_dep_wait();
+        grid_dep_launch();
+    }
 #ifdef TFA_TRACE
     if (threadIdx.x == 0 && blockIdx.x < 1024) g_tfa_cta_time[blockIdx.x][0] = globaltimer_ns();
 #endif
