@@ -300,16 +300,44 @@ struct FirstCut {
         return tiles ? static_cast<size_t>(tiles) * B * Hkv * parts * 2 * 128 * D * sizeof(float) : 0;
     }
 };
-FirstCut first_cut(int L, int S, int window, int first) {
+// Where there are fewer key tiles than SMs (few KV heads) all of them are cut, into the
+// number of parts for which the longest item, or an SM's share, and the sums' cost are
+// least, in steps (a query tile of a head): adding up a part took some 0.04 steps, the
+// second kernel 3 (7 heads on 1 KV head, 1236 rows, window 727: forward and gradients
+// 173 us, cut about 95).
+FirstCut first_cut(int B, int Hkv, int G, int L, int S, int window, int first, int sms) {
     FirstCut c;
-    const int tiles = (first + tfa::kBlockK - 1) / tfa::kBlockK;
-    if (first <= 0 || tiles > 4) return c;
+    const int tiles = (first + tfa::kBlockK - 1) / tfa::kBlockK, all_tiles = (S + tfa::kBlockK - 1) / tfa::kBlockK;
+    if (first <= 0) return c;
     const tfa::KeyRange all = tfa::ktile_query_range(L, S, 1, 0, 0);
     const int n = all.hi - all.lo + 1, inside = (window < L ? window : L) / tfa::kBlockQ + 1;
     const int parts = (n + inside - 1) / inside;
-    if (parts < 2) return c;
-    c.tiles = tiles;
-    c.parts = parts < 32 ? parts : 32;
+    if (parts >= 2 && tiles <= 4) {
+        c.tiles = tiles;
+        c.parts = parts < 32 ? parts : 32;
+    }
+    const long long items = static_cast<long long>(B) * Hkv * all_tiles;
+    if (items >= sms || n < 2) return c;
+    int seen = 0, most = 0;  // key tiles that some row sees, the most query tiles of an uncut one
+    long long steps = 0;
+    for (int kt = 0; kt < all_tiles; ++kt) {
+        const tfa::KeyRange qr = tfa::ktile_query_range(L, S, 1, kt < tiles ? 0 : window, kt);
+        const int nq = qr.hi >= qr.lo ? qr.hi - qr.lo + 1 : 0;
+        seen += nq > 0;
+        steps += nq;
+        const int longest = kt < c.tiles ? (nq + c.parts - 1) / c.parts : nq;
+        most = longest > most ? longest : most;
+    }
+    if (4 * seen < 3 * all_tiles) return c;  // parts of tiles that nobody sees would only be written
+    const double share = static_cast<double>(steps) * G * B * Hkv / sms;
+    auto cost = [&](double longest, long long part_items) {
+        return (longest > share ? longest : share) + (part_items ? 3 + 0.04 * part_items : 0.);
+    };
+    double best = cost(static_cast<double>(most) * G, static_cast<long long>(B) * Hkv * c.tiles * c.parts);
+    for (int cut = 2; cut <= n && cut <= 32 && items * cut <= 4 * sms; ++cut) {
+        const double x = cost(static_cast<double>((n + cut - 1) / cut) * G, items * cut);
+        if (x < best) best = x, c.tiles = all_tiles, c.parts = cut;
+    }
     return c;
 }
 
@@ -774,7 +802,7 @@ int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void 
     else
         dq_kern<<<dq_grid, bw::kThreads, smem, stream>>>(mq, mdo, mk, mv, p), e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("dQ kernel launch", e);
-    const FirstCut cut = first_cut(L, S, p.window, first);
+    const FirstCut cut = first_cut(B, Hkv, Hq / Hkv, L, S, p.window, first, st.sm_count);
     p.cut_tiles = cut.tiles;
     p.parts = cut.parts;
     p.part = bs.part;
@@ -918,7 +946,7 @@ extern "C" int tfa_prefill_first_backward(const void *q, const void *k, const vo
     std::lock_guard<std::mutex> lk(g_mutex);
     const int f = first < S ? first : S;
     if ((rc = device_state(s, &st)) || (rc = bwd_scratch(*st, s, static_cast<size_t>(B) * Hq * L, D, &bs,
-                                                         first_cut(L, S, window, f).bytes(B, Hkv, D))))
+                                                         first_cut(B, Hkv, Hq / Hkv, L, S, window, f, st->sm_count).bytes(B, Hkv, D))))
         return rc;
     return (D == 128) ? backward_impl<128>(*st, nullptr, *bs, q, k, v, dout, dq, dk, dv, B, Hq, Hkv, L, S, scale, 1,
                                            window, key_mask, s, o, lse, f)

@@ -99,6 +99,9 @@ CASES = [
     ("two_cut_tiles_prefix", 1, 3, 1, 1200, 4000, 64, 128, 200),
     ("uncut_tiles", 1, 2, 1, 900, 900, 128, 100, 600),
     ("window_int_max", 1, 4, 2, 300, 700, 128, 2 ** 31 - 1, 2 ** 31 - 1),
+    ("few_key_tiles_g7", 1, 7, 1, 1236, 1692, 128, 727, 85),
+    ("few_key_tiles_b2", 2, 4, 1, 700, 700, 64, 300, 3),
+    ("few_key_tiles_first_past_all", 1, 6, 2, 520, 600, 128, 200, 600),
     ("most_parts", 1, 1, 1, 9000, 9000, 64, 1, 1),
 ]
 IDS = [c[0] for c in CASES]
