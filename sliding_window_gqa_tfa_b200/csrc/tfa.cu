@@ -303,7 +303,7 @@ struct FirstCut {
 // Where there are fewer key tiles than SMs (few KV heads) all of them are cut, into the
 // number of parts for which the longest item, or an SM's share, and the sums' cost are
 // least, in steps (a query tile of a head): adding up a part took some 0.04 steps, the
-// second kernel 3 (7 heads on 1 KV head, 1236 rows, window 727: forward and gradients
+// second kernel 3 (7 heads on 1 KV head, 1236 rows, window 727: gradients 120 us, cut
 // 173 us, cut about 95).
 FirstCut first_cut(int B, int Hkv, int G, int L, int S, int window, int first, int sms) {
     FirstCut c;
@@ -500,13 +500,21 @@ int launch(DeviceState &st, const void *q, const void *k, const void *v, void *o
     sh.first = ad.first;
     sh.n_qp = tfa::shape_n_qp(L);
     auto steps_of = [&](const tfa::Shape &x) { return first ? tfa::total_steps<true>(x) : tfa::total_steps(x); };
-    // First layout, packed: the finalizer of a cut tile merges its pack_heads L rows
-    // alone, about a step for every five (measured: 128 rows over a 1024-token window
-    // 43 us cut, 21 us whole; over 16384 tokens 80 us cut, 172 us whole).
-    const int cut_cost = tfa::kPieceCostSteps + (first && packed ? pack_heads * L / 5 : 0);
     auto makespan = [&](const tfa::Shape &x) {
-        const int cost = x.split ? cut_cost : tfa::kPieceCostSteps;
-        return first ? tfa::makespan_estimate<true>(x, p.W, cost) : tfa::makespan_estimate(x, p.W);
+        if (!first) return tfa::makespan_estimate(x, p.W);
+        int cost = tfa::kPieceCostSteps;
+        if (x.split) {
+            // First layout: what the finalizer of a cut tile spends on the `others` that hold
+            // parts of it.  A whole tile's rows take it 3 steps for each (35 others: 199 us, uncut
+            // 75 us; 5: 50, 28; 2 of 29 steps: 96, 139); a packed tile's one for each pass over
+            // 1024 channels and eight others (18 others, 100 rows: 52 us, uncut 50; 4 rows, 34
+            // others: 18, 49; 74 rows, 3: 39, 20).
+            const long long others = static_cast<long long>(tfa::longest_item<true>(x)) * x.grid / p.W + 1;
+            const long long passes = (static_cast<long long>(pack_heads) * L * D + 1023) / 1024;
+            const long long merge = packed ? passes * ((others + 7) / 8) : 3 * others;
+            cost += static_cast<int>(merge < 100000 ? merge : 100000);
+        }
+        return tfa::makespan_estimate<true>(x, p.W, cost);
     };
     p.W = varlen ? 0 : steps_of(sh);  // varlen: per-sequence lengths live on the device
     // Head pairs for causal calls whose items are short (at most 16 key tiles

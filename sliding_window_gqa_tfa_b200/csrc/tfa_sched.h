@@ -300,4 +300,12 @@ inline long long makespan_estimate(Shape s, long long W, int piece_cost = kPiece
     return worst;
 }
 
+// The most steps of an item.
+template <bool FIRST = false>
+inline int longest_item(const Shape &s) {
+    int most = 0;
+    for (int r = 0; r < s.n_qp; ++r) most = imax(most, item_steps<FIRST>(s, group_qp(s, r)));
+    return most;
+}
+
 }  // namespace tfa

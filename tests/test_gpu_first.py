@@ -94,6 +94,7 @@ CASES = [
     ("window_past_all", 1, 2, 1, 100, 300, 64, 2 ** 30, 5),
     ("first128_window128", 1, 4, 1, 256, 1024, 128, 128, 128),
     ("cut_ranges", 1, 1, 1, 260, 20000, 128, 9000, 70),
+    ("cut_items", 1, 80, 20, 256, 9000, 64, 8000, 70),
     ("many_items", 3, 16, 4, 513, 900, 64, 200, 9),
     ("cut_key_tiles", 2, 4, 2, 1500, 1500, 128, 100, 4),
     ("two_cut_tiles_prefix", 1, 3, 1, 1200, 4000, 64, 128, 200),
