@@ -393,13 +393,23 @@ int decode(const void *q, const void *k_codes, const void *k_meta, const void *v
 // are but walks them once for every 16 rows of a KV head, or is unpacked for the dense
 // kernel.  Measured (D = 128, 4 or 7 query heads a KV head): up to 64 rows the first is
 // always ahead (16 x 8 KV heads, 5000 positions: 138 against 160 us; one sequence of
-// 5000: 18 against 51 us); beyond, while its own time, some 3.4e-6 us a row and
-// position, stays below the dense kernel's 40 to 60 us for merging short tiles
-// (128 rows, one sequence of 5000: 28 against 76 us; 16 sequences: 270 against 160 us).
+// 5000: 18 against 51 us); beyond, while its own time stays below the dense kernel's,
+// which is long where few items leave it many pieces to join (128 rows, one sequence of
+// 5000: 28 against 76 us; 16 sequences: 270 against 160 us; 200 rows of one head over
+// 12000 positions: 18 against 446 us, of 32 heads 233 against 100 us).  The estimates,
+// in us, met the faster one or came within 15 % of it at 236 of 240 sizes.
 bool few_rows(int B, int Hq, int Hkv, int L, const Seen &sn) {
     const long long rows = static_cast<long long>(Hq / Hkv) * L;
     if (B > kMaxSeqs || static_cast<long long>(B) * Hq * L > (1ll << 26)) return false;
-    return rows <= 64 || (L < 128 && static_cast<double>(B) * Hkv * sn.rows() * rows <= 12e6);
+    if (rows <= 64) return true;
+    const double pairs = static_cast<double>(B) * Hkv * sn.rows() * rows;
+    if (L < 128) return pairs <= 12e6;
+    const double own = 9 + 4.6e-6 * pairs;
+    // items of two query tiles, their key tiles of 1.75 us, the other pieces of a cut item
+    const double sms = 148, items = static_cast<double>(B) * Hq * ((L + 255) / 256), tiles = sn.rows() / 128.;
+    const double whole = 14 + 1.75 * tiles * std::ceil(items / sms), others = sms / items < tiles ? sms / items : tiles;
+    const double cut = 25 + 1.75 * items * tiles / sms + 5 * others;
+    return own < (items >= sms ? whole : items >= 32 && whole < cut ? whole : cut);
 }
 
 }  // namespace

@@ -344,7 +344,7 @@ __device__ __forceinline__ void backward_block(const Params &p, int block, int b
         if (ch.turns) f.load(tab[which][token ? sub : 0], lane);  // a slot without a token turns zeros
         __nv_bfloat16 *op = o0;
         for (int base = 0; base < heads; base += kRows * kHeads) {
-            // this round's rows are there, all lanes' parts of them, and the last round's are read
+            // the rows are there, all lanes' parts of them, and those before them are read
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
             __syncwarp();
             fetch();

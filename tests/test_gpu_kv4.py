@@ -394,6 +394,10 @@ PREFILL = [
     (1, 2, 1, 40, 500, 64, 500, 2 ** 31 - 1, 9),
     (40, 2, 2, 3, 70, 64, 77, 0, 0),
     (40, 8, 2, 130, 200, 64, 210, 50, 4),
+    # many rows and heads: the dense kernel
+    (2, 32, 2, 200, 1000, 128, 1000, 0, 0),
+    (2, 32, 2, 260, 1000, 128, 1001, 100, 4),
+    (4, 32, 4, 300, 700, 64, 720, 128, 600),
 ]
 
 
@@ -428,9 +432,9 @@ def test_prefill(c):
 def test_prefill_is_the_dense_attention_of_the_values_read_back():
     gen = _gen(21)
     cache = cache_of(_randn(gen, 2, 2, 600, 128).bfloat16(), _randn(gen, 2, 2, 600, 128).bfloat16(), 640)
-    q = _randn(gen, 2, 8, 130, 128).bfloat16()
+    q = _randn(gen, 2, 32, 260, 128).bfloat16()
     k, v = tb.kv4_read(*cache, rows=600)
-    sinks = _randn(gen, 8)
+    sinks = _randn(gen, 32)
     a = dict(softcap=20.0, sinks=sinks)
     assert torch.equal(tb.kv4_prefill(q, *cache, S=600), tb.prefill(q, k, v))
     assert torch.equal(tb.kv4_prefill(q, *cache, S=600, **a), tb.prefill(q, k, v, **a))
@@ -465,8 +469,8 @@ def test_prefill_workspace_is_used_within_its_size():
     gen = _gen(23)
     cache = cache_of(_randn(gen, 1, 2, 400, 64).bfloat16(), _randn(gen, 1, 2, 400, 64).bfloat16(), 400)
     for L in (20, 200):  # few rows, and many
-        q = _randn(gen, 1, 4, L, 64).bfloat16()
-        need = tb.lib().tfa_kv4_prefill_workspace(1, 4, 2, L, 400, 64, 30, 4)
+        q = _randn(gen, 1, 64, L, 64).bfloat16()
+        need = tb.lib().tfa_kv4_prefill_workspace(1, 64, 2, L, 400, 64, 30, 4)
         ws = torch.full((need + 64,), 77, dtype=torch.uint8, device="cuda")
         got = tb.kv4_prefill(q, *cache, S=400, window=30, first=4, workspace=ws)
         assert torch.equal(got, tb.kv4_prefill(q, *cache, S=400, window=30, first=4)) and (ws[need:] == 77).all()
@@ -478,7 +482,7 @@ def test_few_rows_and_many_agree():
     """Chunks on both sides of the border between the two kernels: the same rows."""
     gen = _gen(24)
     cache = cache_of(_randn(gen, 1, 2, 900, 128).bfloat16(), _randn(gen, 1, 2, 900, 128).bfloat16(), 900)
-    q = _randn(gen, 1, 8, 200, 128).bfloat16()
+    q = _randn(gen, 1, 64, 200, 128).bfloat16()
     whole = tb.kv4_prefill(q, *cache, S=900, window=300, first=3)
     n = torch.tensor([900], dtype=torch.int32, device="cuda")
     for L in (1, 8, 33, 127):

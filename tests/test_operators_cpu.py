@@ -219,13 +219,16 @@ def test_kv4_prefill_refusals(over, code):
 def test_kv4_workspaces():
     size, few = tb.lib().tfa_kv4_prefill_workspace, tb.lib().tfa_kv4_decode_workspace(8, 2, 1, 128)
     assert size(2, 16, 4, 200, 1000, 128, 0, 0) == 2 * 4 * 1000 * 128 * 4
-    assert size(2, 16, 4, 200, 1000, 64, 20, 5) == 2 * 4 * (5 + 219) * 64 * 4
-    assert size(1, 4, 1, 200, 1000, 64, 20, 781) == 1000 * 64 * 4  # the first tokens meet the window
-    assert size(1, 4, 1, 200, 1000, 64, 2 ** 31 - 1, 2 ** 31 - 1) == 1000 * 64 * 4
+    assert size(2, 64, 4, 200, 1000, 64, 20, 5) == 2 * 4 * (5 + 219) * 64 * 4
+    assert size(1, 64, 1, 200, 1000, 64, 20, 781) == 1000 * 64 * 4  # the first tokens meet the window
+    assert size(1, 64, 1, 200, 1000, 64, 2 ** 31 - 1, 2 ** 31 - 1) == 1000 * 64 * 4
     assert size(1, 1, 1, 10, 9, 64, 20, 0) == 0
     # few rows: the kernel of tfa_kv4_decode and its pieces
     assert size(64, 32, 8, 16, 5000, 128, 0, 0) == few
     assert size(1, 32, 8, 32, 5000, 128, 0, 0) == few
+    assert size(1, 1, 1, 200, 12000, 128, 0, 0) == few  # one item, which the dense kernel would cut for all SMs
+    assert size(2, 16, 4, 200, 1000, 64, 20, 5) == tb.lib().tfa_kv4_decode_workspace(8, 2, 1, 64)
+    assert size(1, 56, 8, 2048, 8192, 128, 0, 0) == 8 * 8192 * 128 * 4
     assert size(16, 32, 8, 32, 5000, 128, 0, 0) == 16 * 8 * 5000 * 128 * 4
     assert size(2000, 8, 8, 1, 10, 128, 0, 0) == 2000 * 8 * 10 * 128 * 4  # more sequences than it takes
     assert tb.lib().tfa_kv4_decode_workspace(8, 2, 1, 128) == 4 * 640 * 8 * 130 * 4
