@@ -397,7 +397,7 @@ int decode(const void *q, const void *k_codes, const void *k_meta, const void *v
 // which is long where few items leave it many pieces to join (128 rows, one sequence of
 // 5000: 28 against 76 us; 16 sequences: 270 against 160 us; 200 rows of one head over
 // 12000 positions: 18 against 446 us, of 32 heads 233 against 100 us).  The estimates,
-// in us, met the faster one or came within 15 % of it at 236 of 240 sizes.
+// in us, met the faster one or came within 15 % of it at 237 of 240 sizes.
 bool few_rows(int B, int Hq, int Hkv, int L, const Seen &sn) {
     const long long rows = static_cast<long long>(Hq / Hkv) * L;
     if (B > kMaxSeqs || static_cast<long long>(B) * Hq * L > (1ll << 26)) return false;

@@ -166,3 +166,106 @@ def test_native_calls_on_a_stream_that_is_current():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, tb.kv4_decode(q, *c, lens))
+
+
+def _step(q, k, v, w, freq, cache, lens, window, first):
+    """A decoding step in one stream: its kernels start while the ones before them end."""
+    qr, kr = tb.qk_norm_rope(q, k, lens, freq, q_weight=w, k_weight=w)
+    tb.kv4_append(kr, v, *cache, start=lens)
+    return tb.kv4_decode(qr, *cache, lens + 1, window=window, first=first)
+
+
+@pytest.mark.gpu
+def test_a_chain_of_calls_needs_no_synchronisation():
+    """Steps whose lengths and rows are written just before them, by slow kernels, with
+    and without a wait between any two calls: the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    n, hq, hkv, cap, d = 4, 8, 2, 3000, 128
+    freq, _ = tb.rope_inv_freq(d, device="cuda")
+    w = torch.randn(d, generator=g, device="cuda").bfloat16()
+    slow = torch.randn(4096, 4096, generator=g, device="cuda")
+    base = torch.tensor([2900, 1, 700, 1500], dtype=torch.int32, device="cuda")
+    rows = torch.randn(12, n, 1, hq + 2 * hkv, d, generator=g, device="cuda").bfloat16()
+
+    def run(wait):
+        cache = tb.kv4_cache(n, hkv, cap, d, device="cuda")
+        lens, outs = torch.zeros_like(base), []
+        qkv = torch.empty_like(rows[0])
+        for i in range(12):
+            slow @ slow  # keeps the stream busy while the next calls are made
+            qkv.copy_(rows[i])
+            lens.copy_(base + i)
+            q, k, v = qkv.split([hq, hkv, hkv], dim=2)
+            v = v.transpose(1, 2)
+            if wait:
+                torch.cuda.synchronize()
+                qr, kr = tb.qk_norm_rope(q, k, lens, freq, q_weight=w, k_weight=w)
+                torch.cuda.synchronize()
+                tb.kv4_append(kr, v, *cache, start=lens)
+                torch.cuda.synchronize()
+                outs.append(tb.kv4_decode(qr, *cache, lens + 1, window=1000, first=4))
+                torch.cuda.synchronize()
+            else:
+                outs.append(_step(q, k, v, w, freq, cache, lens, 1000, 4))
+        return torch.stack(outs)
+
+    want = run(True)
+    for _ in range(3):
+        assert torch.equal(run(False), want)
+
+
+@pytest.mark.gpu
+def test_training_calls_back_to_back():
+    """Norms, windowed attention with first tokens and all gradients, call after call."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    b, hq, hkv, n, d = 1, 4, 2, 500, 128
+    freq, _ = tb.rope_inv_freq(d, device="cuda")
+    q0, k0, do = (torch.randn(b, n, h, d, generator=g, device="cuda").bfloat16() for h in (hq, hkv, hq))
+    v = torch.randn(b, hkv, n, d, generator=g, device="cuda").bfloat16()
+    do = do.transpose(1, 2).contiguous()
+    w = torch.randn(d, generator=g, device="cuda").bfloat16()
+
+    def run(wait):
+        pause = torch.cuda.synchronize if wait else lambda: None
+        q, k = tb.qk_norm_rope(q0, k0, 0, freq, q_weight=w, k_weight=w)
+        pause()
+        saved = tb.prefill_lse(q, k, v, window=100, first=4)
+        pause()
+        dq, dk, dv = tb.backward(q, k, v, do, window=100, first=4, saved=saved)
+        pause()
+        return (*tb.qk_norm_rope_backward(dq, dk, q0, k0, 0, freq, q_weight=w, k_weight=w), dv, saved[0])
+
+    want = run(True)
+    for _ in range(5):
+        for x, y in zip(run(False), want):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_captured_into_one_graph():
+    """A captured fork and join: each call waits for what it needs, on either stream."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    d, cap, n = 64, 200, 3
+    freq, _ = tb.rope_inv_freq(d, device="cuda")
+    q, k, v = (torch.randn(n, 1, h, d, generator=g, device="cuda").bfloat16() for h in (4, 2, 2))
+    w = torch.randn(d, generator=g, device="cuda").bfloat16()
+    lens = torch.tensor([100, 0, 150], dtype=torch.int32, device="cuda")
+    caches = [tb.kv4_cache(n, 2, cap, d, device="cuda") for _ in range(3)]
+    want = _step(q, k, v.transpose(1, 2), w, freq, caches[2], lens, 50, 2)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        kept = [q.clone(), k.clone()]
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            a = _step(*kept, v.transpose(1, 2), w, freq, caches[0], lens, 50, 2)
+        b = _step(*kept, v.transpose(1, 2), w, freq, caches[1], lens, 50, 2)
+        here.wait_stream(side)
+        both = torch.stack([a, b])
+        last = tb.kv4_decode(both[0], *caches[1], lens + 1, window=50, first=2)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(both[0], want) and torch.equal(both[1], want)
+        assert torch.equal(last, tb.kv4_decode(want, *caches[2], lens + 1, window=50, first=2))
