@@ -763,7 +763,7 @@ int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void 
         lse = bs.lse;
     }
     const long long rows = static_cast<long long>(B) * Hq * L;
-    const long long threads = rows * 32;
+    const long long threads = (rows + bw::kDeltaRows - 1) / bw::kDeltaRows * 32;
     const unsigned delta_grid = static_cast<unsigned>((threads + 255) / 256);
     const auto *ob = static_cast<const __nv_bfloat16 *>(o), *dob = static_cast<const __nv_bfloat16 *>(dout);
     cudaError_t e = cudaSuccess;
