@@ -388,9 +388,10 @@ size_t tfa_kv4_decode_workspace(int Hq, int Hkv, int L, int D);
 
 /* tfa_kv4_prefill -- the same attention for chunks of any L >= 1 rows, every
  * sequence with S cached positions (L <= S, else TFA_ERR_SHAPE; S <= capacity, else
- * TFA_ERR_CACHE).  A chunk of few rows takes tfa_kv4_decode's kernel; for the others the positions that some
- * row sees are brought back to bf16 in the workspace and the dense kernel runs on
- * them (scratch and graph capture as for tfa_prefill).  workspace: device memory of
+ * TFA_ERR_CACHE).  Chunks of few rows, or of few heads, take tfa_kv4_decode's kernel,
+ * where it is the faster; for the others the positions that some row sees are brought
+ * back to bf16 in the workspace and the dense kernel runs on them (scratch and graph
+ * capture as for tfa_prefill).  workspace: device memory of
  * tfa_kv4_prefill_workspace(B, Hq, Hkv, L, S, D, window, first) bytes, 16-byte
  * aligned, not shared by calls that overlap. */
 int tfa_kv4_prefill(const void *q, const void *k_codes, const void *k_meta, const void *v_codes, const void *v_meta,
