@@ -218,7 +218,8 @@ int tfa_prefill_varlen(const void *q, const void *k, const void *v, void *o,
  * dk = scale dS^T Q, dv = P^T dout.  The call re-runs the forward (its output
  * and per-row log-sum-exp go to a per-stream workspace of 2 B Hq L (D + 4)
  * bytes, grown on demand; growth during graph capture returns
- * TFA_ERR_CAPTURE), then three kernels, all asynchronous on `stream`: a
+ * TFA_ERR_CAPTURE, and a workspace that a captured call uses is kept when a
+ * later one outgrows it, so its graph may still be replayed), then three kernels, all asynchronous on `stream`: a
  * delta kernel, the dQ kernel, and the dK/dV kernel, launched with
  * programmatic stream serialisation so that its CTAs start on the SMs the dQ
  * kernel's CTAs leave (it reads nothing dQ writes).  The dK/dV kernel does

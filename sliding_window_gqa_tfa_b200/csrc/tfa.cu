@@ -38,13 +38,16 @@ struct SplitScratch {
 
 // Workspace of the backward pass, per (device, stream), grown on demand: the
 // recomputed forward output and per-row log-sum-exp, and delta = rowsum(dO o O);
-// with first tokens, the partial sums of the cut key tiles.
+// with first tokens, the partial sums of the cut key tiles.  Once a call has been
+// captured, its graph holds these addresses for as long as it lives: buffers that a
+// later call outgrows are then kept (until process exit), not freed.
 struct BwdScratch {
     void *o = nullptr;
     float *lse = nullptr, *delta = nullptr;
     size_t rows = 0, o_bytes = 0;
     float *part = nullptr;
     size_t part_bytes = 0;
+    bool rows_captured = false, part_captured = false;  // o, lse, delta; part
 };
 
 constexpr int kVariantsPerD = 30;  // forward kernel variants per head dim (variant_index)
@@ -249,6 +252,12 @@ int split_scratch(DeviceState &st, cudaStream_t stream, SplitScratch **out) {
     return TFA_OK;
 }
 
+// Whether `stream` is being captured.
+bool capturing(cudaStream_t stream) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    return cudaStreamIsCapturing(stream, &cs) == cudaSuccess && cs == cudaStreamCaptureStatusActive;
+}
+
 // The backward workspace for `stream`, at least `rows` rows of D columns and
 // `part_bytes` bytes of partial sums.
 int bwd_scratch(DeviceState &st, cudaStream_t stream, size_t rows, int D, BwdScratch **out, size_t part_bytes = 0) {
@@ -256,12 +265,15 @@ int bwd_scratch(DeviceState &st, cudaStream_t stream, size_t rows, int D, BwdScr
     const size_t o_bytes = rows * static_cast<size_t>(D) * 2;
     if (bs.rows < rows || bs.o_bytes < o_bytes) {
         if (int rc = refuse_under_capture(stream, "a larger backward workspace")) return rc;
-        cudaFree(bs.o);
-        cudaFree(bs.lse);
-        cudaFree(bs.delta);
+        if (!bs.rows_captured) {
+            cudaFree(bs.o);
+            cudaFree(bs.lse);
+            cudaFree(bs.delta);
+        }
         bs.o = nullptr;
         bs.lse = bs.delta = nullptr;
         bs.rows = bs.o_bytes = 0;
+        bs.rows_captured = false;
         cudaError_t e = cudaMalloc(&bs.o, o_bytes);
         if (e == cudaSuccess) e = cudaMalloc(&bs.lse, rows * sizeof(float));
         if (e == cudaSuccess) e = cudaMalloc(&bs.delta, rows * sizeof(float));
@@ -278,12 +290,17 @@ int bwd_scratch(DeviceState &st, cudaStream_t stream, size_t rows, int D, BwdScr
     }
     if (bs.part_bytes < part_bytes) {
         if (int rc = refuse_under_capture(stream, "a larger backward workspace")) return rc;
-        cudaFree(bs.part);
+        if (!bs.part_captured) cudaFree(bs.part);
         bs.part = nullptr;
         bs.part_bytes = 0;
+        bs.part_captured = false;
         const cudaError_t e = cudaMalloc(&bs.part, part_bytes);
         if (e != cudaSuccess) return cuda_fail("cudaMalloc(backward partial sums)", e);
         bs.part_bytes = part_bytes;
+    }
+    if (capturing(stream)) {
+        bs.rows_captured = true;
+        bs.part_captured = bs.part_captured || part_bytes > 0;
     }
     *out = &bs;
     return TFA_OK;

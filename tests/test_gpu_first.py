@@ -224,3 +224,41 @@ def test_captured_training_step():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, o2) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("L2,S2,W2", [(300, 700, 200), (900, 1300, 200)])  # as many rows, more rows
+def test_a_captured_step_outlives_a_larger_workspace(L2, S2, W2):
+    """A training step captured on a stream, then steps on the same stream that need
+    more workspace: the graph's replay writes neither into freed memory (which the
+    canaries take) nor anything else than before."""
+    q, k, v, do = _make(1, 8, 2, 300, 4000, 128, 12)
+    others = _make(1, 8, 2, L2, S2, 128, 13)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+
+    def step(x, W):
+        saved = tb.prefill_lse(*x[:3], window=W, first=4)
+        return tb.backward(*x, window=W, first=4, saved=saved)
+
+    with torch.cuda.stream(s):
+        want = step((q, k, v, do), 40)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = step((q, k, v, do), 40)
+    with torch.cuda.stream(s):
+        want2 = step(others, W2)
+    torch.cuda.synchronize()
+    canaries = [torch.full((1 << n,), 7, dtype=torch.uint8, device="cuda") for n in range(12, 28) for _ in range(4)]
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all((c == 7).all() for c in canaries)
+    with torch.cuda.stream(s):
+        again = step(others, W2)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(again, want2))
