@@ -394,12 +394,16 @@ size_t tfa_kv4_decode_workspace(int Hq, int Hkv, int L, int D);
  * back to bf16 in the workspace and the dense kernel runs on them (scratch and graph
  * capture as for tfa_prefill).  workspace: device memory of
  * tfa_kv4_prefill_workspace(B, Hq, Hkv, L, S, D, window, first) bytes, 16-byte
- * aligned, not shared by calls that overlap. */
+ * aligned, not shared by calls that overlap.  That size is this call's: a chunk of
+ * fewer rows may take the other kernel and need more.  One workspace for several
+ * chunks holds tfa_kv4_prefill_workspace_most bytes, enough for every chunk of at
+ * most L rows over at most S positions. */
 int tfa_kv4_prefill(const void *q, const void *k_codes, const void *k_meta, const void *v_codes, const void *v_meta,
                     void *o, int B, int Hq, int Hkv, int L, int S, int capacity, int D,
                     float scale, int window, int first, float softcap, const float *sinks,
                     void *workspace, tfa_stream_t stream);
 size_t tfa_kv4_prefill_workspace(int B, int Hq, int Hkv, int L, int S, int D, int window, int first);
+size_t tfa_kv4_prefill_workspace_most(int B, int Hq, int Hkv, int L, int S, int D, int window, int first);
 
 /* Debug flags for tfa_prefill_debug. */
 #define TFA_DEBUG_NO_TILE_SKIP  1u /* visit every key tile, even fully masked ones   */

@@ -132,6 +132,8 @@ def lib():
             L.tfa_kv4_prefill.restype = i32
             L.tfa_kv4_prefill_workspace.argtypes = [i32] * 8
             L.tfa_kv4_prefill_workspace.restype = ctypes.c_size_t
+            L.tfa_kv4_prefill_workspace_most.argtypes = [i32] * 8
+            L.tfa_kv4_prefill_workspace_most.restype = ctypes.c_size_t
             L.tfa_kv4_decode_workspace.argtypes = [i32] * 4
             L.tfa_kv4_decode_workspace.restype = ctypes.c_size_t
             L.tfa_qk_norm_rope_workspace.argtypes = [i32]
@@ -990,8 +992,8 @@ def kv4_prefill(q, k_codes, k_meta, v_codes, v_meta, *, S, scale=None, window=0,
                 out=None, workspace=None, stream=None):
     """Causal attention [B,Hq,L,D] of chunks of any L >= 1 rows over the first S rows of
     the 4-bit cache (the chunk's own rows last among them); window and first as for
-    kv4_decode.  workspace: uint8 of tfa_kv4_prefill_workspace bytes, by default
-    allocated here."""
+    kv4_decode.  workspace: uint8 of tfa_kv4_prefill_workspace bytes (or, for chunks of
+    several sizes, tfa_kv4_prefill_workspace_most), by default allocated here."""
     if _calls is not None and stream is None:
         made = _calls.prefill(q, k_codes, k_meta, v_codes, v_meta, S, scale, window, first, softcap, sinks, out, workspace)
         if made is not None:

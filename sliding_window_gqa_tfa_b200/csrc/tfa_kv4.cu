@@ -442,6 +442,14 @@ extern "C" size_t tfa_kv4_prefill_workspace(int B, int Hq, int Hkv, int L, int S
     return few_rows(B, Hq, Hkv, L, sn) ? decode_workspace(D) : static_cast<size_t>(B) * Hkv * sn.rows() * D * 4;
 }
 
+// The positions that are brought back, min(S, first + L + window - 1) with a window and
+// S without, grow with L and S, and the other kernel's size is a constant.
+extern "C" size_t tfa_kv4_prefill_workspace_most(int B, int Hq, int Hkv, int L, int S, int D, int window, int first) {
+    if (B < 1 || Hkv < 1 || Hq < 1 || L < 1 || S < L || D < 1 || first < 0) return 0;
+    const size_t dense = static_cast<size_t>(B) * Hkv * seen(L, S, window, first).rows() * D * 4, few = decode_workspace(D);
+    return dense > few ? dense : few;
+}
+
 // A long chunk's products are the tensor core's to bound, so K and V are brought back
 // to bf16 once (a rounding of each value, as a bf16 cache has), next to which they would
 // be read by every query tile, and the dense kernel runs on them.  Only positions that

@@ -1,6 +1,7 @@
 """Refusals of the long-context operators, before any CUDA call: the pointers here
 are never dereferenced."""
 import ctypes
+import random
 
 import pytest
 
@@ -233,3 +234,22 @@ def test_kv4_workspaces():
     assert size(2000, 8, 8, 1, 10, 128, 0, 0) == 2000 * 8 * 10 * 128 * 4  # more sequences than it takes
     assert tb.lib().tfa_kv4_decode_workspace(8, 2, 1, 128) == 4 * 640 * 8 * 130 * 4
     assert tb.lib().tfa_kv4_decode_workspace(8, 0, 1, 128) == 0
+
+
+def test_one_workspace_for_chunks_of_several_sizes():
+    """A smaller chunk may need more than a larger one; _most covers them all."""
+    size, most = tb.lib().tfa_kv4_prefill_workspace, tb.lib().tfa_kv4_prefill_workspace_most
+    assert size(1, 8, 1, 2048, 2048, 64, 0, 0) < size(1, 8, 1, 5, 2048, 64, 0, 0) <= most(1, 8, 1, 2048, 2048, 64, 0, 0)
+    r = random.Random(1)
+    for _ in range(3000):
+        B, Hkv, G, D = r.choice([1, 2, 16, 1500]), r.choice([1, 2, 8]), r.choice([1, 2, 4, 7]), r.choice([64, 128])
+        W = r.choice([0, 0, 1, 128, 1024, 2 ** 31 - 1])
+        F = r.choice([0, 1, 4, 300, 2 ** 31 - 1]) if W else 0
+        L = r.randint(1, r.choice([8, 130, 4000]))
+        S = L + r.randint(0, r.choice([1, 1000, 20000]))
+        bound = most(B, G * Hkv, Hkv, L, S, D, W, F)
+        for _ in range(5):
+            l = r.randint(1, L)
+            s = r.randint(l, S)
+            assert size(B, G * Hkv, Hkv, l, s, D, W, F) <= bound, (B, G, Hkv, L, S, l, s, D, W, F)
+    assert most(1, 1, 1, 10, 9, 64, 20, 0) == 0
