@@ -322,7 +322,9 @@ int tfa_prefill_first(const void *q, const void *k, const void *v, void *o, floa
 
 /* tfa_prefill_first_backward -- gradients of tfa_prefill_first (no softcap, no
  * sinks) from its saved output and log-sum-exp; arguments, workspace and errors as
- * for tfa_prefill_backward_saved. */
+ * for tfa_prefill_backward_saved.  Where key tiles are cut (tfa_plan_first_cut) the
+ * workspace also holds the parts' sums, 1024 D bytes for each of tiles x B x Hkv x
+ * parts, which are at most four times the device's SMs (78 MB of 148 SMs and D = 128). */
 int tfa_prefill_first_backward(const void *q, const void *k, const void *v, const void *o,
                                const float *lse, const void *dout, void *dq, void *dk, void *dv,
                                int B, int Hq, int Hkv, int L, int S, int D, float scale,
@@ -510,6 +512,12 @@ int tfa_plan_qtile(int L, int S, int causal, int window, int has_key_mask, int q
  * key and value gradients are zero).  Returns TFA_OK, TFA_ERR_SHAPE for an
  * out-of-range tile, or a validation error for the sizes.  No device work. */
 int tfa_plan_ktile(int L, int S, int causal, int window, int ktile, int *qt_lo, int *qt_hi);
+
+/* tfa_plan_first_cut -- host view of how tfa_prefill_first_backward's dK/dV pass on a
+ * device of `sms` SMs cuts key tiles: the first *tiles ones into *parts parts each
+ * over their query tiles (0 and 1: none is cut).  Returns TFA_OK, TFA_ERR_SHAPE for
+ * sms < 1, or a validation error for the sizes (D is taken as 128).  No device work. */
+int tfa_plan_first_cut(int B, int Hq, int Hkv, int L, int S, int window, int first, int sms, int *tiles, int *parts);
 
 /* tfa_plan_pieces -- host view of the work one CTA of a grid of `grid` CTAs
  * performs (no device work).  The work of (batch, query head, pair of 128-row

@@ -110,6 +110,8 @@ def lib():
             L.tfa_plan_qtile.restype = i32
             L.tfa_plan_ktile.argtypes = [i32] * 5 + [ctypes.POINTER(i32), ctypes.POINTER(i32)]
             L.tfa_plan_ktile.restype = i32
+            L.tfa_plan_first_cut.argtypes = [i32] * 8 + [ctypes.POINTER(i32), ctypes.POINTER(i32)]
+            L.tfa_plan_first_cut.restype = i32
             L.tfa_plan_pieces.argtypes = [i32] * 9 + [P, i32, ctypes.POINTER(i32),
                                                       ctypes.POINTER(ctypes.c_longlong)]
             L.tfa_plan_pieces.restype = i32
@@ -249,6 +251,13 @@ def tfa_plan_ktile(L, S, causal, window, ktile):
     lo, hi = ctypes.c_int(0), ctypes.c_int(0)
     rc = lib().tfa_plan_ktile(L, S, int(bool(causal)), window, ktile, ctypes.byref(lo), ctypes.byref(hi))
     return rc, lo.value, hi.value
+
+
+def tfa_plan_first_cut(B, Hq, Hkv, L, S, window, first, sms):
+    """(status, key tiles that the gradient with first tokens cuts, parts of each)."""
+    tiles, parts = ctypes.c_int(0), ctypes.c_int(0)
+    rc = lib().tfa_plan_first_cut(B, Hq, Hkv, L, S, window, first, sms, ctypes.byref(tiles), ctypes.byref(parts))
+    return rc, tiles.value, parts.value
 
 
 def tfa_plan_pieces(B, Hq, L, S, causal, window, grid, split, cta, max_pieces=4096):

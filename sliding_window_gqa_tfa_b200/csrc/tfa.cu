@@ -306,55 +306,95 @@ int bwd_scratch(DeviceState &st, cudaStream_t stream, size_t rows, int D, BwdScr
     return TFA_OK;
 }
 
-// How the first tokens' key tiles are cut in the backward pass: into parts of about
-// as many query tiles as a key tile inside the window has.  Whole, one such tile
-// kept one CTA busy twice as long as the others (4096 rows, window 1024, 8 KV heads:
-// forward and gradients 508 us, cut 422 us).  At most 32 parts, which bounds the workspace, and
-// no cut beyond 4 tiles: there are then enough long items to even out.
+// How the first tokens' key tiles are cut in the backward pass.  `tiles` of them go in
+// `parts` parts each, whose sums are kept in fp32 until they are added up.
 struct FirstCut {
     int tiles = 0, parts = 1;
     size_t bytes(int B, int Hkv, int D) const {
         return tiles ? static_cast<size_t>(tiles) * B * Hkv * parts * 2 * 128 * D * sizeof(float) : 0;
     }
 };
-// Where there are fewer key tiles than SMs (few KV heads) all of them are cut, into the
-// number of parts for which the longest item, or an SM's share, and the sums' cost are
-// least, in steps (a query tile of a head): adding up a part took some 0.04 steps, the
-// second kernel 3 (7 heads on 1 KV head, 1236 rows, window 727: gradients 120 us, cut
-// 173 us, cut about 95).
+
+// The most that one of `sms` CTAs is dealt in the snake order of bwd::ItemIter.
+constexpr int kDealSms = 512;
+struct Dealt {
+    int sms;
+    long long x = 0, all = 0, diff[kDealSms + 1] = {};
+    explicit Dealt(int sms_) : sms(sms_) {}
+    void add(long long count, long long cost) {  // `count` items of a cost, the next ones
+        while (count > 0) {
+            const int pos = static_cast<int>(x % sms);
+            if (pos == 0 && count >= sms) {
+                const long long rounds = count / sms;
+                all += rounds * cost;
+                x += rounds * sms;
+                count -= rounds * sms;
+                continue;
+            }
+            const int take = count < sms - pos ? static_cast<int>(count) : sms - pos;
+            const int lo = (x / sms) % 2 ? sms - pos - take : pos;
+            diff[lo] += cost;
+            diff[lo + take] -= cost;
+            x += take;
+            count -= take;
+        }
+    }
+    long long most() const {
+        long long run = 0, top = 0;
+        for (int i = 0; i < sms; ++i) {
+            run += diff[i];
+            top = run > top ? run : top;
+        }
+        return all + top;
+    }
+};
+
+// A cut is taken where it shortens the longest CTA by more than the sums cost, in steps
+// (a query tile of a head): adding up a part took some 0.04 steps, the second kernel 3.
+// Two kinds are tried.  Up to 4 tiles of first tokens, which every later row sees, into
+// parts of about as many query tiles as a key tile inside the window has (4096 rows,
+// window 1024, 8 KV heads: forward and gradients 508 us, cut 422 us); beyond, there are
+// enough long items to even out.  And all key tiles, where they are fewer than the SMs
+// (7 heads on 1 KV head, 1236 rows, window 727: gradients 120 us, cut 46 us).
+// A cut has at most 4 parts an SM, which bounds the workspace: 78 MB for 148 SMs and
+// D = 128.  (16 sequences of 4096 rows, 16 heads on 8, window 128: gradients 1060 us,
+// with the first tokens' tiles cut for nothing 1158 us and 268 MB.)
 FirstCut first_cut(int B, int Hkv, int G, int L, int S, int window, int first, int sms) {
     FirstCut c;
+    if (first <= 0 || sms < 1 || sms > kDealSms) return c;
     const int tiles = (first + tfa::kBlockK - 1) / tfa::kBlockK, all_tiles = (S + tfa::kBlockK - 1) / tfa::kBlockK;
-    if (first <= 0) return c;
     const tfa::KeyRange all = tfa::ktile_query_range(L, S, 1, 0, 0);
     const int n = all.hi - all.lo + 1, inside = (window < L ? window : L) / tfa::kBlockQ + 1;
-    const int parts = (n + inside - 1) / inside;
-    if (parts >= 2 && tiles <= 4) {
-        c.tiles = tiles;
-        c.parts = parts < 32 ? parts : 32;
-    }
-    const long long items = static_cast<long long>(B) * Hkv * all_tiles;
-    if (items >= sms || n < 2) return c;
-    int seen = 0, most = 0;  // key tiles that some row sees, the most query tiles of an uncut one
-    long long steps = 0;
-    for (int kt = 0; kt < all_tiles; ++kt) {
-        const tfa::KeyRange qr = tfa::ktile_query_range(L, S, 1, kt < tiles ? 0 : window, kt);
-        const int nq = qr.hi >= qr.lo ? qr.hi - qr.lo + 1 : 0;
-        seen += nq > 0;
-        steps += nq;
-        const int longest = kt < c.tiles ? (nq + c.parts - 1) / c.parts : nq;
-        most = longest > most ? longest : most;
-    }
-    if (4 * seen < 3 * all_tiles) return c;  // parts of tiles that nobody sees would only be written
-    const double share = static_cast<double>(steps) * G * B * Hkv / sms;
-    auto cost = [&](double longest, long long part_items) {
-        return (longest > share ? longest : share) + (part_items ? 3 + 0.04 * part_items : 0.);
+    if (n < 2) return c;
+    const long long bg = static_cast<long long>(B) * Hkv, most_parts = 4ll * sms;
+    const long long room = tiles <= 4 ? most_parts / (bg * tiles) : 0, wanted = (n + inside - 1) / inside;
+    const int parts = static_cast<int>(wanted < 32 ? (wanted < room ? wanted : room) : room < 32 ? room : 32);
+    const bool every = bg * all_tiles < sms;
+    if (parts < 2 && !every) return c;
+    int seen = 0;  // key tiles that some row sees
+    auto cost = [&](const FirstCut &f) {
+        Dealt d(sms);
+        seen = 0;
+        for (int kt = 0; kt < all_tiles; ++kt) {
+            const tfa::KeyRange qr = tfa::ktile_query_range(L, S, 1, kt < tiles ? 0 : window, kt);
+            const long long nq = qr.hi >= qr.lo ? qr.hi - qr.lo + 1 : 0;
+            seen += nq > 0;
+            const int into = kt < f.tiles ? f.parts : 1;
+            for (int i = 0; i < into; ++i) d.add(bg, (nq * (i + 1) / into - nq * i / into) * G);
+        }
+        return static_cast<double>(d.most()) + (f.tiles ? 3 + 0.04 * static_cast<double>(bg * f.tiles * f.parts) : 0.);
     };
-    double best = cost(static_cast<double>(most) * G, static_cast<long long>(B) * Hkv * c.tiles * c.parts);
-    for (int cut = 2; cut <= n && cut <= 32 && items * cut <= 4 * sms; ++cut) {
-        const double x = cost(static_cast<double>((n + cut - 1) / cut) * G, items * cut);
-        if (x < best) best = x, c.tiles = all_tiles, c.parts = cut;
-    }
+    double best = cost(c);
+    auto consider = [&](int t, int into) {
+        FirstCut f;
+        f.tiles = t;
+        f.parts = into;
+        const double x = cost(f);
+        if (x < best) best = x, c = f;
+    };
+    if (parts >= 2) consider(tiles, parts);
+    if (every && 4 * seen >= 3 * all_tiles)  // else parts of tiles that nobody sees would only be written
+        for (int into = 2; into <= n && into <= 32 && bg * all_tiles * into <= most_parts; ++into) consider(all_tiles, into);
     return c;
 }
 
@@ -765,7 +805,7 @@ int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void 
                   const void *v, const void *dout, void *dq, void *dk, void *dv, int B, int Hq,
                   int Hkv, int L, int S, float scale, int causal, int window, const float *key_mask,
                   cudaStream_t stream, const void *o_saved = nullptr, const float *lse_saved = nullptr,
-                  int first = 0) {
+                  int first = 0, const FirstCut &cut = FirstCut()) {
     namespace bw = tfa::bwd;
     const void *o = o_saved;
     const float *lse = lse_saved;
@@ -827,7 +867,6 @@ int backward_impl(DeviceState &st, SplitScratch *ss, BwdScratch &bs, const void 
     else
         dq_kern<<<dq_grid, bw::kThreads, smem, stream>>>(mq, mdo, mk, mv, p), e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("dQ kernel launch", e);
-    const FirstCut cut = first_cut(B, Hkv, Hq / Hkv, L, S, p.window, first, st.sm_count);
     p.cut_tiles = cut.tiles;
     p.parts = cut.parts;
     p.part = bs.part;
@@ -970,13 +1009,13 @@ extern "C" int tfa_prefill_first_backward(const void *q, const void *k, const vo
     BwdScratch *bs = nullptr;
     std::lock_guard<std::mutex> lk(g_mutex);
     const int f = first < S ? first : S;
-    if ((rc = device_state(s, &st)) || (rc = bwd_scratch(*st, s, static_cast<size_t>(B) * Hq * L, D, &bs,
-                                                         first_cut(B, Hkv, Hq / Hkv, L, S, window, f, st->sm_count).bytes(B, Hkv, D))))
-        return rc;
+    if ((rc = device_state(s, &st))) return rc;
+    const FirstCut cut = first_cut(B, Hkv, Hq / Hkv, L, S, window, f, st->sm_count);
+    if ((rc = bwd_scratch(*st, s, static_cast<size_t>(B) * Hq * L, D, &bs, cut.bytes(B, Hkv, D)))) return rc;
     return (D == 128) ? backward_impl<128>(*st, nullptr, *bs, q, k, v, dout, dq, dk, dv, B, Hq, Hkv, L, S, scale, 1,
-                                           window, key_mask, s, o, lse, f)
+                                           window, key_mask, s, o, lse, f, cut)
                       : backward_impl<64>(*st, nullptr, *bs, q, k, v, dout, dq, dk, dv, B, Hq, Hkv, L, S, scale, 1,
-                                          window, key_mask, s, o, lse, f);
+                                          window, key_mask, s, o, lse, f, cut);
 }
 
 extern "C" int tfa_prefill_debug(const void *q, const void *k, const void *v, void *o, int B,
@@ -1238,6 +1277,20 @@ extern "C" int tfa_plan_ktile(int L, int S, int causal, int window, int ktile, i
     const tfa::KeyRange r = tfa::ktile_query_range(L, S, causal, causal ? window : 0, ktile);
     *qt_lo = r.lo;
     *qt_hi = r.hi;
+    return TFA_OK;
+}
+
+extern "C" int tfa_plan_first_cut(int B, int Hq, int Hkv, int L, int S, int window, int first, int sms, int *tiles,
+                                  int *parts) {
+    const int rc = validate(nullptr, nullptr, nullptr, nullptr, B, Hq, Hkv, L, S, 128, 1.0f, 1, window, nullptr, false,
+                            L >= 1 && L <= TFA_MAX_DECODE_ROWS);
+    if (rc) return rc;
+    if (window <= 0 || first < 0) return TFA_ERR_WINDOW;
+    if (!tiles || !parts) return TFA_ERR_NULL;
+    if (sms < 1) return TFA_ERR_SHAPE;
+    const FirstCut c = first_cut(B, Hkv, Hq / Hkv, L, S, window < S ? window : S, first < S ? first : S, sms);
+    *tiles = c.tiles;
+    *parts = c.parts;
     return TFA_OK;
 }
 

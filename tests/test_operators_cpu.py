@@ -253,3 +253,51 @@ def test_one_workspace_for_chunks_of_several_sizes():
             s = r.randint(l, S)
             assert size(B, G * Hkv, Hkv, l, s, D, W, F) <= bound, (B, G, Hkv, L, S, l, s, D, W, F)
     assert most(1, 1, 1, 10, 9, 64, 20, 0) == 0
+
+
+def _longest(B, Hkv, G, L, S, window, first, sms, tiles, parts):
+    """Steps of the CTA that is dealt the most, item by item in the kernel's snake order."""
+    items = []
+    for kt in range((S + 127) // 128):
+        rc, lo, hi = tb.tfa_plan_ktile(L, S, True, 0 if kt * 128 < first else window, kt)
+        assert rc == tb.TFA_OK
+        n, into = max(0, hi - lo + 1), parts if kt < tiles else 1
+        for i in range(into):
+            items += [(n * (i + 1) // into - n * i // into) * G] * (B * Hkv)
+    load = [0] * sms
+    for x, w in enumerate(items):
+        load[x % sms if x // sms % 2 == 0 else sms - 1 - x % sms] += w
+    return max(load)
+
+
+def test_first_cut_shortens_the_longest_cta_and_is_bounded():
+    r = random.Random(2)
+    cut = 0
+    for _ in range(400):
+        B, Hkv, G = r.choice([1, 2, 4, 9, 16, 64]), r.choice([1, 2, 8]), r.choice([1, 2, 4, 7])
+        L = r.randint(1, r.choice([300, 2000, 9000]))
+        S = L + r.choice([0, 0, r.randint(0, 4000)])
+        window, first, sms = r.choice([1, 100, 128, 727, 1024, 4000]), r.choice([1, 4, 130, 512, 5000]), r.choice([148, 132, 60])
+        rc, tiles, parts = tb.tfa_plan_first_cut(B, G * Hkv, Hkv, L, S, window, first, sms)
+        assert rc == tb.TFA_OK and (tiles > 0) == (parts > 1)
+        assert B * Hkv * tiles * parts <= 4 * sms
+        if tiles:
+            cut += 1
+            a, b = (_longest(B, Hkv, G, L, S, window, min(first, S), sms, *c) for c in ((0, 1), (tiles, parts)))
+            assert b + 3 < a, (B, Hkv, G, L, S, window, first, sms)
+    assert cut > 100
+
+
+def test_first_cut_of_known_shapes():
+    plan = tb.tfa_plan_first_cut
+    assert plan(1, 32, 8, 4096, 4096, 1024, 4, 148) == (tb.TFA_OK, 1, 4)  # a training step of one sequence
+    # enough items to even out: nothing to save, whatever the window
+    for B, first in ((16, 4), (64, 4), (64, 512)):
+        for L in (4096, 8192):
+            assert plan(B, 32, 8, L, L, 128, first, 148) == (tb.TFA_OK, 0, 1)
+    assert plan(1, 7, 1, 1236, 1692, 727, 85, 148)[1] == 14  # few key tiles: all of them
+    assert plan(1, 8, 2, 300, 300, 100, 0, 148) == (tb.TFA_OK, 0, 1)
+    assert plan(1, 8, 2, 300, 300, 0, 4, 148)[0] == tb.TFA_ERR_WINDOW
+    assert plan(1, 8, 2, 300, 300, 9, -1, 148)[0] == tb.TFA_ERR_WINDOW
+    assert plan(1, 8, 2, 300, 300, 9, 4, 0)[0] == tb.TFA_ERR_SHAPE
+    assert plan(1, 8, 3, 300, 300, 9, 4, 148)[0] == tb.TFA_ERR_HEADS
