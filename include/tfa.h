@@ -272,7 +272,8 @@ int tfa_prefill_backward_saved(const void *q, const void *k, const void *v, cons
  *                 for long contexts by the caller); unread when rot == 0
  *   positions     int32 device: [B] with positions_per_row == 0 (row i of sequence
  *                 b is at positions[b] + i), [B, L] with positions_per_row != 0;
- *                 NULL: row i of every sequence is at first_position + i
+ *                 NULL: row i of every sequence is at first_position + i; a sum
+ *                 may pass 2^31
  *   rot           rotated channels, a multiple of 16 in [0, D]; 0: norms only
  *   Hq, Hkv       1 to 65536; B L at most 2^30
  *   interleaved   0: pair i is channels (i, i + rot / 2); else (2i, 2i + 1)

@@ -55,9 +55,11 @@ struct Params {
     int q_blocks;    // gradient: blocks that take query rows, the first ones
 };
 
-__device__ __forceinline__ int position(const Params &p, int b, int l) {
-    if (!p.pos) return p.pos0 + l;
-    return p.pos_per_row ? __ldg(p.pos + static_cast<long long>(b) * p.L + l) : __ldg(p.pos + b) + l;
+// 64 bits: a row behind a first position near 2^31 lies past an int.
+__device__ __forceinline__ long long position(const Params &p, int b, int l) {
+    if (!p.pos) return static_cast<long long>(p.pos0) + l;
+    return p.pos_per_row ? __ldg(p.pos + static_cast<long long>(b) * p.L + l)
+                         : static_cast<long long>(__ldg(p.pos + b)) + l;
 }
 
 // The cosines and sines of a position's pairs, times mscale; a gradient's sines are negated.
@@ -70,7 +72,7 @@ __device__ __forceinline__ double turns_per_token(const Params &p, int i) {
     return p.inv_freq[i] * kInv2Pi;
 }
 template <int D>
-__device__ __forceinline__ void angle(const Params &p, int pos, double per_token, int i, Table<D> &tab) {
+__device__ __forceinline__ void angle(const Params &p, long long pos, double per_token, int i, Table<D> &tab) {
     double turns = static_cast<double>(pos) * per_token;
     turns -= rint(turns);
     float s, c;

@@ -211,3 +211,20 @@ def test_scaled_frequencies():
     assert ((g <= f) & (g >= f / 4 - 1e-20)).all()
     g, m = tb.rope_inv_freq(128, 1e6, scaling="linear", factor=8.0)
     assert m == 1.0 and torch.allclose(g, f / 8, rtol=1e-14, atol=0)
+
+
+@pytest.mark.parametrize("as_int", [True, False])
+def test_positions_past_31_bits(as_int):
+    """Rows behind a first position near 2^31: the angle goes on, it does not wrap."""
+    start = 2 ** 31 - 3
+    q, k, wq, wk, f, _ = _make(2, 9, 4, 2, 128, 128, 10)
+    first = start if as_int else torch.full((2,), start, dtype=torch.int32, device="cuda")
+    rows = start + torch.arange(9, device="cuda").expand(2, 9)
+    qo, ko = tb.qk_norm_rope(q, k, first, f, q_weight=wq, k_weight=wk)
+    for x, w, got in ((q, wq, qo), (k, wk, ko)):
+        ref, size = _reference(x, w, rows, f, 128, False, 1.0, 1e-6)
+        assert ((got.transpose(1, 2).double() - ref).abs() <= 2 ** -8 * ref.abs() + 2 ** -18 * size).all()
+    back = tb.qk_norm_rope_backward(qo, ko, q, k, first, f, q_weight=wq, k_weight=wk)
+    for dy, x, w, got in ((qo, q, wq, back[0]), (ko, k, wk, back[1])):
+        ref, size, _, _ = _reference_backward(dy, x, w, rows, f, 128, False, 1.0, 1e-6)
+        assert ((got.double() - ref).abs() <= 2 ** -8 * ref.abs() + 2 ** -18 * size).all()
