@@ -266,7 +266,8 @@ int tfa_prefill_backward_saved(const void *q, const void *k, const void *v, cons
  *                 or rows of a key cache.  May be the inputs themselves (the same
  *                 pointers and strides); any other overlap is undefined.
  *   strides       HOST array of 12: the element strides over (batch, token, head)
- *                 of q, k, q_out, k_out, multiples of 8
+ *                 of q, k, q_out, k_out, multiples of 8 (unread where a
+ *                 dimension's size is 1)
  *   q_weight, k_weight  bf16 [D], or both NULL: no norm
  *   inv_freq      fp64 [rot / 2] device: radians per position of each pair (scaled
  *                 for long contexts by the caller); unread when rot == 0
@@ -345,7 +346,7 @@ int tfa_prefill_first_backward(const void *q, const void *k, const void *v, cons
 /* tfa_kv4_append -- writes L new rows of every sequence into the cache.
  *   k, v      bf16 [B, Hkv, L, D], 16-byte aligned, any strides with the channels
  *             contiguous; strides: HOST array of 6, the element strides over
- *             (batch, head, row) of k and v, multiples of 8
+ *             (batch, head, row) of k and v, multiples of 8 (unread where a size is 1)
  *   start     int32 [B] device: row i of sequence b goes to cache row start[b] + i;
  *             start[b] < 0: the sequence takes nothing.  Rows at or past the
  *             capacity are not written, and tfa_check_status returns

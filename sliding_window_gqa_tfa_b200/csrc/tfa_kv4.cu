@@ -295,9 +295,10 @@ extern "C" int tfa_kv4_append(const void *k, const void *v, const long long *str
     AppendParams p = {};
     p.k = static_cast<const __nv_bfloat16 *>(k);
     p.v = static_cast<const __nv_bfloat16 *>(v);
-    for (int i = 0; i < 3; ++i) {
-        p.sk[i] = strides[i];
-        p.sv[i] = strides[3 + i];
+    const int sizes[3] = {B, Hkv, L};
+    for (int i = 0; i < 3; ++i) {  // (a dimension of size 1 has a stride that no address uses)
+        p.sk[i] = sizes[i] > 1 ? strides[i] : 0;
+        p.sv[i] = sizes[i] > 1 ? strides[3 + i] : 0;
         if (p.sk[i] % 8 || p.sv[i] % 8) return TFA_ERR_ALIGN;
     }
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4)) return TFA_ERR_ALIGN;

@@ -452,7 +452,10 @@ int check(const Params &p, int D) {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool aligned(const Strides &s) { return s.b % 8 == 0 && s.l % 8 == 0 && s.h % 8 == 0; }
-Strides strides(const long long *s) { return Strides{s[0], s[1], s[2]}; }
+// (A dimension of size 1 has a stride that no address uses, which may be anything.)
+Strides strides(const long long *s, int B, int L, int H) {
+    return Strides{B > 1 ? s[0] : 0, L > 1 ? s[1] : 0, H > 1 ? s[2] : 0};
+}
 
 int launch_forward(Params &p, int D, cudaStream_t stream) {
     const int n_rows = p.Hq + p.Hkv, slots = kThreads / (D / 8);
@@ -522,10 +525,10 @@ extern "C" int tfa_qk_norm_rope(const void *q, const void *k, void *q_out, void 
     p.k = static_cast<const __nv_bfloat16 *>(k);
     p.qo = static_cast<__nv_bfloat16 *>(q_out);
     p.ko = static_cast<__nv_bfloat16 *>(k_out);
-    p.sq = strides(strd);
-    p.sk = strides(strd + 3);
-    p.sqo = strides(strd + 6);
-    p.sko = strides(strd + 9);
+    p.sq = strides(strd, B, L, Hq);
+    p.sk = strides(strd + 3, B, L, Hkv);
+    p.sqo = strides(strd + 6, B, L, Hq);
+    p.sko = strides(strd + 9, B, L, Hkv);
     p.wq = static_cast<const __nv_bfloat16 *>(q_weight);
     p.wk = static_cast<const __nv_bfloat16 *>(k_weight);
     p.inv_freq = inv_freq;
@@ -570,12 +573,12 @@ extern "C" int tfa_qk_norm_rope_backward(const void *dq_out, const void *dk_out,
     p.dk = static_cast<const __nv_bfloat16 *>(dk_out);
     p.qo = static_cast<__nv_bfloat16 *>(dq);
     p.ko = static_cast<__nv_bfloat16 *>(dk);
-    p.sdq = strides(strd);
-    p.sdk = strides(strd + 3);
-    p.sq = norm ? strides(strd + 6) : p.sdq;
-    p.sk = norm ? strides(strd + 9) : p.sdk;
-    p.sqo = strides(strd + 12);
-    p.sko = strides(strd + 15);
+    p.sdq = strides(strd, B, L, Hq);
+    p.sdk = strides(strd + 3, B, L, Hkv);
+    p.sq = norm ? strides(strd + 6, B, L, Hq) : p.sdq;
+    p.sk = norm ? strides(strd + 9, B, L, Hkv) : p.sdk;
+    p.sqo = strides(strd + 12, B, L, Hq);
+    p.sko = strides(strd + 15, B, L, Hkv);
     p.wq = static_cast<const __nv_bfloat16 *>(q_weight);
     p.wk = static_cast<const __nv_bfloat16 *>(k_weight);
     p.inv_freq = inv_freq;

@@ -269,3 +269,18 @@ def test_calls_on_two_streams_captured_into_one_graph():
         torch.cuda.synchronize()
         assert torch.equal(both[0], want) and torch.equal(both[1], want)
         assert torch.equal(last, tb.kv4_decode(want, *caches[2], lens + 1, window=50, first=2))
+
+
+@pytest.mark.gpu
+def test_strides_of_single_rows_do_not_count():
+    """A dimension of size 1 has a stride that no address uses."""
+    freq, _ = tb.rope_inv_freq(D, device="cuda")
+    q, k = _rows(0, 1, 1, 4, D).cuda(), _rows(1, 1, 1, 1, D).cuda()
+    want = tb.qk_norm_rope(q, k, 3, freq)
+    odd = lambda t: t.as_strided(t.shape, [3 if n == 1 else s for n, s in zip(t.shape, t.stride())])
+    got = tb.qk_norm_rope(odd(q), odd(k), 3, freq, q_out=odd(torch.empty_like(want[0])), k_out=odd(torch.empty_like(want[1])))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    cache, other = (tb.kv4_cache(1, 1, 4, D, device="cuda") for _ in range(2))
+    tb.kv4_append(k, k, *cache, start=1)
+    tb.kv4_append(odd(k), odd(k), *other, start=1)
+    assert all(torch.equal(a, b) for a, b in zip(cache, other))
