@@ -12,6 +12,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import operator
 import os
 import re
 import struct
@@ -572,7 +573,9 @@ _current_device = torch.cuda.current_device
 
 
 def _int32(x, name):
-    """x, which a C call takes as an int; ctypes would drop the bits that do not fit."""
+    """x (an int, or what stands for one) as a C call's int; ctypes would drop the bits
+    that do not fit."""
+    x = operator.index(x)
     if not -2 ** 31 <= x < 2 ** 31:
         raise ValueError(f"{name} must fit in 32 bits")
     return x
@@ -598,7 +601,7 @@ def _check_on(t, name, dtype, ndim, index=None, rows=False):
     raise ValueError(f"{name} must have a contiguous last dimension" if rows else f"{name} must be contiguous")
 
 
-def _first_inputs(q, k, v, causal, window, first, key_mask):
+def _first_inputs(q, k, v, causal, key_mask):
     _check_on(q, "q", _BF16, 4)
     dev = q.get_device()
     _check_on(k, "k", _BF16, 4, dev)
@@ -613,9 +616,11 @@ def _first_inputs(q, k, v, causal, window, first, key_mask):
             raise ValueError("key_mask must be [B, S]")
     if not causal:
         raise ValueError("first tokens need causal attention with a window")
-    _int32(window, "window")
-    _int32(first, "first")
     return dev, (B, Hq, kv[1], L, kv[2], D)
+
+
+def _scale(scale, D):
+    return D ** -0.5 if scale is None else float(scale)
 
 
 def _prefill_first(q, k, v, scale, causal, window, first, key_mask, softcap, sinks, out, lse, want_lse, stream):
@@ -624,7 +629,8 @@ def _prefill_first(q, k, v, scale, causal, window, first, key_mask, softcap, sin
         made = _calls.prefill_first(q, k, v, scale, window, first, key_mask, softcap, sinks, out, lse, want_lse)
         if made is not None:
             return _native(made, "tfa_prefill_first")
-    dev, dims = _first_inputs(q, k, v, causal, window, first, key_mask)
+    dev, dims = _first_inputs(q, k, v, causal, key_mask)
+    window, first = _int32(window, "window"), _int32(first, "first")
     if sinks is not None:
         _check_on(sinks, "sinks", _F32, 1, dev)
         if sinks.shape[0] != dims[1]:
@@ -644,8 +650,8 @@ def _prefill_first(q, k, v, scale, causal, window, first, key_mask, softcap, sin
             lse = torch.empty(q.shape[:3], dtype=_F32, device=q.device)
         rc = (_lib or lib()).tfa_prefill_first(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
-            *dims, dims[5] ** -0.5 if scale is None else scale, window, first,
-            key_mask.data_ptr() if key_mask is not None else None, softcap,
+            *dims, _scale(scale, dims[5]), window, first,
+            key_mask.data_ptr() if key_mask is not None else None, float(softcap),
             sinks.data_ptr() if sinks is not None else None, _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_prefill_first")
@@ -658,7 +664,8 @@ def _backward_first(q, k, v, dout, scale, causal, window, first, key_mask, out, 
         made = _calls.backward_first(q, k, v, dout, *saved, scale, window, first, key_mask)
         if made is not None:
             return _native(made, "tfa_prefill_first_backward")
-    dev, dims = _first_inputs(q, k, v, causal, window, first, key_mask)
+    dev, dims = _first_inputs(q, k, v, causal, key_mask)
+    window, first = _int32(window, "window"), _int32(first, "first")
     o, lse = saved
     for t, n in ((dout, "dout"), (o, "o")):
         _check_on(t, n, _BF16, 4, dev)
@@ -678,7 +685,7 @@ def _backward_first(q, k, v, dout, scale, causal, window, first, key_mask, out, 
         dq, dk, dv = out
         rc = (_lib or lib()).tfa_prefill_first_backward(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(),
-            dk.data_ptr(), dv.data_ptr(), *dims, dims[5] ** -0.5 if scale is None else scale, window, first,
+            dk.data_ptr(), dv.data_ptr(), *dims, _scale(scale, dims[5]), window, first,
             key_mask.data_ptr() if key_mask is not None else None, _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_prefill_first_backward")
@@ -732,10 +739,10 @@ def _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight):
     elif q_weight is not k_weight:
         raise ValueError("q_weight and k_weight must be given together")
     per_row, first, ptr = 0, 0, None
-    if isinstance(positions, int):
+    if not isinstance(positions, torch.Tensor):
         first = _int32(positions, "positions")
     else:
-        per_row = 1 if isinstance(positions, torch.Tensor) and positions.dim() == 2 else 0
+        per_row = 1 if positions.dim() == 2 else 0
         _check_on(positions, "positions", _I32, 1 + per_row, dev)
         if positions.shape != ((B, L) if per_row else (B,)):
             raise ValueError("positions must be an int, [B] or [B, L]")
@@ -793,8 +800,8 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
         (ob, oh, ol, _), (pb, ph, pl, _) = q_out.stride(), k_out.stride()
         rc = (_lib or lib()).tfa_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-            _PACK12(qb, ql, qh, kb, kl, kh, ob, ol, oh, pb, pl, ph), *mid, *dims, interleaved, eps, mscale,
-            _raw_stream(dev))
+            _PACK12(qb, ql, qh, kb, kl, kh, ob, ol, oh, pb, pl, ph), *mid, *dims, bool(interleaved), float(eps),
+            float(mscale), _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_qk_norm_rope")
     return q_out, k_out
@@ -831,7 +838,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
         rc = L_.tfa_qk_norm_rope_backward(
             dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(), dk.data_ptr(), pq, pk,
             _PACK18(*_heads(dq_out), *_heads(dk_out), *_tokens(q), *_tokens(k), *_tokens(dq), *_tokens(dk)), *mid,
-            *dims, interleaved, eps, mscale, pw, _raw_stream(dev))
+            *dims, bool(interleaved), float(eps), float(mscale), pw, _raw_stream(dev))
     if rc != TFA_OK:
         raise TfaError(rc, "tfa_qk_norm_rope_backward")
     return dq, dk, dwq, dwk
@@ -876,7 +883,7 @@ def _kv4_check(k_codes, k_meta, v_codes, v_meta):
 
 def _kv4_start(start, B, dev):
     """(device pointer or None, first row) of an int or int32 [B]."""
-    if isinstance(start, int):
+    if not isinstance(start, torch.Tensor):
         return None, _int32(start, "start")
     _check_on(start, "start", _I32, 1, dev)
     if start.shape[0] != B:
@@ -924,7 +931,7 @@ def kv4_read(k_codes, k_meta, v_codes, v_meta, *, start=0, rows=None, out=None, 
         if ptr is not None:
             raise ValueError("rows must be given with a start for each sequence")
         rows = cap - first
-    _int32(rows, "rows")
+    rows = _int32(rows, "rows")
     with _scope(dev, stream):
         if out is None:
             out = k_meta.new_empty((B, Hkv, rows, D)), k_meta.new_empty((B, Hkv, rows, D))
@@ -989,7 +996,7 @@ def kv4_decode(q, k_codes, k_meta, v_codes, v_meta, lens, *, scale=None, window=
         workspace = _kv4_workspace(workspace, L_.tfa_kv4_decode_workspace(Hq, Hkv, L, D), dev, k_codes)
         rc = L_.tfa_kv4_decode(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
                                   v_meta.data_ptr(), lens.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, cap, D,
-                                  D ** -0.5 if scale is None else scale, window, first, softcap,
+                                  _scale(scale, D), window, first, float(softcap),
                                   sinks.data_ptr() if sinks is not None else None, workspace.data_ptr(),
                                   _raw_stream(dev))
     if rc != TFA_OK:
@@ -1009,7 +1016,7 @@ def kv4_prefill(q, k_codes, k_meta, v_codes, v_meta, *, S, scale=None, window=0,
             return _native(made, "tfa_kv4_prefill")
     B, Hkv, cap, D, dev = _kv4_check(k_codes, k_meta, v_codes, v_meta)
     _kv4_query(q, B, D, dev, sinks, out)
-    _int32(S, "S")
+    S = _int32(S, "S")
     Hq, L = q.shape[1], q.shape[2]
     window, first = _int32(window, "window"), _int32(first, "first")
     with _scope(dev, stream):
@@ -1019,7 +1026,7 @@ def kv4_prefill(q, k_codes, k_meta, v_codes, v_meta, *, S, scale=None, window=0,
         workspace = _kv4_workspace(workspace, max(need, 16), dev, k_codes)
         rc = (_lib or lib()).tfa_kv4_prefill(q.data_ptr(), k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(),
                                    v_meta.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, S, cap, D,
-                                   D ** -0.5 if scale is None else scale, window, first, softcap,
+                                   _scale(scale, D), window, first, float(softcap),
                                    sinks.data_ptr() if sinks is not None else None, workspace.data_ptr(),
                                    _raw_stream(dev))
     if rc != TFA_OK:

@@ -284,3 +284,37 @@ def test_strides_of_single_rows_do_not_count():
     tb.kv4_append(k, k, *cache, start=1)
     tb.kv4_append(odd(k), odd(k), *other, start=1)
     assert all(torch.equal(a, b) for a, b in zip(cache, other))
+
+
+@pytest.mark.gpu
+def test_numbers_of_numpy_and_of_torch(monkeypatch):
+    """Sizes, scales and flags as prefill takes them: numpy's numbers and one-element
+    tensors beside Python's, on both ways into the library."""
+    np = pytest.importorskip("numpy")
+    q, k = _rows(0, 1, 40, 4, D).cuda(), _rows(1, 1, 40, 2, D).cuda()
+    freq, _ = tb.rope_inv_freq(D, device="cuda")
+    w = _rows(2, D).cuda()
+    qh, kh = q.transpose(1, 2).contiguous(), k.transpose(1, 2).contiguous()
+    one = tb.kv4_cache(1, 2, 64, D, device="cuda")
+    lens = torch.full((1,), 40, dtype=torch.int32, device="cuda")
+
+    def run(i, f, t):
+        tb.kv4_append(kh, kh, *one, start=i(3))
+        saved = tb.prefill_lse(qh, kh, kh, window=i(9), first=i(2), scale=f(0.25))
+        return [*tb.qk_norm_rope(q, k, i(5), freq, q_weight=w, k_weight=w, eps=f(1e-5), interleaved=t(True), mscale=f(0.5)),
+                *tb.qk_norm_rope_backward(qh, kh, q, k, i(5), freq, q_weight=w, k_weight=w, eps=f(1e-5), interleaved=t(True)),
+                *tb.kv4_read(*one, start=i(3), rows=i(7)), *saved,
+                tb.kv4_decode(qh[:, :, :2].contiguous(), *one, lens, window=i(9), first=i(2), scale=f(0.25), softcap=f(3.0)),
+                tb.kv4_prefill(qh, *one, S=i(43), window=i(9), first=i(2), scale=f(0.25), softcap=f(3.0)),
+                tb.prefill(qh, kh, kh, window=i(9), first=i(2), softcap=f(3.0)),
+                *tb.backward(qh, kh, kh, qh, window=i(9), first=i(2), scale=f(0.25), saved=saved)]
+
+    want = run(int, float, bool)
+    tb.lib()
+    for native in (tb._calls, None):
+        monkeypatch.setattr(tb, "_calls", native)
+        for i, f, t in ((np.int64, np.float32, np.bool_), (np.int32, np.float64, bool),
+                        (int, lambda x: torch.tensor(x, dtype=torch.float64), bool)):
+            for a, b in zip(want, run(i, f, t)):
+                # (numpy's float32 rounds 1e-5 as the C call does)
+                assert torch.equal(a, b)
