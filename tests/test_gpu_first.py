@@ -262,3 +262,20 @@ def test_a_captured_step_outlives_a_larger_workspace(L2, S2, W2):
         again = step(others, W2)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(again, want2))
+
+
+def test_unseen_keys_reach_neither_gradient_of_keys_and_values():
+    """NaN and infinities in K and V between the first tokens and the window: the
+    gradients are those of clean inputs, zero where no row looks."""
+    for D, G in ((128, 2), (64, 1)):
+        q, k, v, do = _make(1, 2 * G, 2, 200, 2000, D, 14)
+        W, F = 256, 4
+        saved = tb.prefill_lse(q, k, v, window=W, first=F)
+        want = tb.backward(q, k, v, do, window=W, first=F, saved=saved)
+        lo = (2000 - 200 - W + 1) // 128 * 128
+        for bad in (float("nan"), float("inf")):
+            k2, v2 = k.clone(), v.clone()
+            k2[:, :, 128:lo], v2[:, :, 128:lo] = bad, bad
+            got = tb.backward(q, k2, v2, do, window=W, first=F, saved=saved)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+            assert (got[1][:, :, 128:lo] == 0).all() and (got[2][:, :, 128:lo] == 0).all()

@@ -492,3 +492,121 @@ def test_few_rows_and_many_agree():
         assert ((part.double() - whole[:, :, -L:].double()).abs() <= 2 ** -5 * (1 + ref.abs())).all()
         if L <= 8:
             assert torch.equal(part, tb.kv4_decode(q[:, :, -L:].contiguous(), *cache, n, window=300, first=3))
+
+
+SCALES = [
+    # B, Hq, Hkv, L, D, cap, lens, window, first, softcap
+    (2, 14, 2, 1, 128, 700, [700, 65], 0, 0, 0.0),
+    (2, 4, 2, 3, 128, 300, [300, 2], 50, 4, 0.0),
+    (1, 32, 2, 2, 64, 500, [500], 0, 0, 0.0),
+    (3, 3, 3, 1, 64, 400, [400, 1, 0], 33, 1, 0.0),
+    (2, 14, 2, 8, 128, 300, [300, 9], 0, 0, 12.0),
+]
+
+
+@pytest.mark.parametrize("scale", [-0.11, -1.0, 0.0, 0.5])
+@pytest.mark.parametrize("c", SCALES, ids=["-".join(map(str, c[:6])) for c in SCALES])
+def test_decode_scales(c, scale):
+    """Scales of either sign and 0 (the mean of what a row sees), against the definition."""
+    B, Hq, Hkv, L, D, cap, lens, window, first, softcap = c
+    if scale == 0 and softcap > 0:
+        pytest.skip("refused")
+    gen = _gen(30)
+    cache = cache_of(_randn(gen, B, Hkv, cap, D).bfloat16(), _randn(gen, B, Hkv, cap, D).bfloat16(), cap)
+    q = _randn(gen, B, Hq, L, D).bfloat16()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = tb.kv4_decode(q, *cache, n, scale=scale, window=window, first=first, softcap=softcap)
+    tb.check_status()
+    ref, bound = reference(q, cache, lens, scale, window, first, softcap)
+    assert ((got.double() - ref).abs() <= bound).all()
+
+
+def _lost(cache, lens, L, window):
+    """What the fp16 range takes at most: a product p s is rounded to no less than 2^-25
+    in units where the sum of the weights is at least 2^(7 - es), 2^es at most twice the
+    largest step of V; a code is at most 15, so 15 2^-31 of that step a position."""
+    out = torch.zeros(len(lens), cache[0].shape[1], dtype=torch.float64, device="cuda")
+    for b, n in enumerate(lens):
+        if n:
+            lo = max(0, n - L - window + 1) if window else 0
+            out[b] = (n - lo) * 15 * 2.0 ** -31 * cache[3][b, :, lo:n, :, 0].double().amax((1, 2))
+    return out
+
+
+@pytest.mark.parametrize("along", ["grow", "shrink", "mixed"])
+@pytest.mark.parametrize("c", [
+    # B, Hq, Hkv, L, D, lens, window
+    (1, 2, 2, 1, 128, [3000], 0), (1, 4, 2, 3, 128, [2000], 0), (1, 7, 1, 1, 64, [4000], 0), (1, 14, 1, 2, 128, [1500], 0),
+    (40, 4, 2, 1, 64, [61 + 40 * i for i in range(40)], 0), (3, 8, 8, 2, 64, [2000, 90, 1000], 700),
+], ids=lambda c: "-".join(map(str, c[:5])))
+def test_decode_with_steps_of_many_sizes(along, c):
+    """V whose steps differ by 2^12 along the sequence and by 2^8 between groups, in one
+    piece and in many: the weights' reference follows them, and pieces with references
+    of their own are joined.  Single positions are 2^6 above the others."""
+    B, Hq, Hkv, L, D, lens, window = c
+    cap = max(lens)
+    gen = _gen(31)
+    x = torch.linspace(0, 12, cap, device="cuda")
+    e = {"grow": x, "shrink": x.flip(0), "mixed": 12 * torch.rand(cap, generator=gen, device="cuda")}[along]
+    e = e + 6 * (torch.rand(cap, generator=gen, device="cuda") < 0.01)
+    groups = 2.0 ** (-8.0 * torch.rand(B, Hkv, cap, D // 32, 1, generator=gen, device="cuda"))
+    v = (_randn(gen, B, Hkv, cap, D // 32, 32) * groups).flatten(-2) * torch.exp2(e)[:, None]
+    cache = cache_of((2 * _randn(gen, B, Hkv, cap, D)).bfloat16(), v.bfloat16(), cap)
+    q = _randn(gen, B, Hq, L, D).bfloat16()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = tb.kv4_decode(q, *cache, n, window=window)
+    tb.check_status()
+    ref, bound = reference(q, cache, lens, D ** -0.5, window)
+    lost = _lost(cache, lens, L, window).repeat_interleave(Hq // Hkv, 1)[:, :, None, None]
+    assert ((got.double() - ref).abs() <= bound + lost).all()
+    assert torch.equal(got, tb.kv4_decode(q, *cache, n, window=window))
+
+
+@pytest.mark.parametrize("D,L", [(128, 1), (64, 1), (128, 5)])
+def test_decode_with_a_few_large_key_channels(D, L):
+    """Two channels of K 30 times the others and of one sign, as rotary keys often have:
+    their groups' steps are large, and the scores are as exact as ever."""
+    gen = _gen(32)
+    B, Hq, Hkv, cap, lens = 2, 8, 2, 900, [900, 333]
+    k = _randn(gen, B, Hkv, cap, D)
+    k[..., 5] += 30
+    k[..., D - 7] -= 30
+    cache = cache_of(k.bfloat16(), _randn(gen, B, Hkv, cap, D).bfloat16(), cap)
+    q = _randn(gen, B, Hq, L, D).bfloat16()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for window, first in ((0, 0), (100, 4)):
+        got = tb.kv4_decode(q, *cache, n, window=window, first=first)
+        ref, bound = reference(q, cache, lens, D ** -0.5, window, first)
+        assert ((got.double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("c", [
+    # B, Hq, Hkv, L, S, D, window, first, large key channels
+    (2, 32, 2, 200, 1000, 128, 0, 0, False), (2, 32, 2, 260, 1000, 128, 100, 4, True), (4, 32, 4, 300, 700, 64, 128, 600, False),
+    (16, 32, 8, 40, 700, 128, 0, 0, True), (1, 56, 8, 513, 1025, 128, 0, 0, False), (2, 28, 4, 333, 1500, 64, 500, 70, True),
+], ids=lambda c: "-".join(map(str, c)))
+def test_long_chunks_against_the_values_read_back(c):
+    """The dense kernel's chunks against the definition over the values that kv4_read
+    gives (K and V rounded to bf16 once; the read back is tested by itself), so that only
+    the weights' and the output's roundings are left: 2^-8 (sum w |v| + |o|), the fp32
+    sums (2^-16 of the absolute ones) as 2^-14."""
+    B, Hq, Hkv, L, S, D, window, first, large = c
+    gen = _gen(33)
+    k = _randn(gen, B, Hkv, S, D)
+    if large:
+        k[..., 3] += 20
+    cache = cache_of(k.bfloat16(), _randn(gen, B, Hkv, S, D).bfloat16(), S + 5)
+    assert tb.lib().tfa_kv4_prefill_workspace(B, Hq, Hkv, L, S, D, window, first) != tb.lib().tfa_kv4_decode_workspace(Hq, Hkv, L, D)
+    q = _randn(gen, B, Hq, L, D).bfloat16()
+    got = tb.kv4_prefill(q, *cache, S=S, window=window, first=first)
+    tb.check_status()
+    ks, vs = (t.double() for t in tb.kv4_read(*cache, rows=S))
+    pos, j = S - L + torch.arange(L, device="cuda")[:, None], torch.arange(S, device="cuda")
+    see = (j <= pos) & ((j > pos - window) | (j < first)) if window > 0 else j <= pos
+    for b in range(B):
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            w = torch.softmax((q[b, h].double() @ ks[b, g].T * D ** -0.5).masked_fill(~see, -math.inf), 1)
+            ref = w @ vs[b, g]
+            bound = (2 ** -8 + 2 ** -14) * (w @ vs[b, g].abs() + ref.abs())
+            assert ((got[b, h].double() - ref).abs() <= bound).all()
