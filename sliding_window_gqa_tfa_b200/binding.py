@@ -16,7 +16,9 @@ import operator
 import os
 import re
 import struct
+import sys
 import threading
+import warnings
 
 import torch
 
@@ -150,12 +152,21 @@ _calls = None  # csrc/calls.cpp's module, once the library is loaded
 
 
 def _load_calls(L):
+    """Only the way into the library depends on this module: without it, or where it was
+    built for another torch (whose tensors it reads) or Python, the wrappers' own code
+    makes the same calls, for some 10 us more each."""
     global _calls
     try:
         from . import _calls as module
     except ImportError as e:
-        raise RuntimeError("_calls.so is missing or built for another torch: build it with "
-                           "`python -m sliding_window_gqa_tfa_b200.build`") from e
+        found = str(e)
+    else:
+        here = f"torch {torch.__version__}, Python {sys.version_info.major}.{sys.version_info.minor}"
+        found = None if module.built_for == here else f"it was built for {module.built_for}, this is {here}"
+    if found is not None:
+        warnings.warn(f"_calls.so cannot be used ({found}): calls take longer; build it with "
+                      "`python -m sliding_window_gqa_tfa_b200.build`", RuntimeWarning, stacklevel=3)
+        return
     module.use(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
         "tfa_qk_norm_rope", "tfa_qk_norm_rope_backward", "tfa_qk_norm_rope_workspace", "tfa_kv4_append",
         "tfa_kv4_read", "tfa_kv4_decode", "tfa_kv4_decode_workspace", "tfa_prefill_first",

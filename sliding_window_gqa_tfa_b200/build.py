@@ -9,7 +9,8 @@ source, or any header, is newer than the object).
 The library is written next to this file; it links the CUDA runtime
 statically and resolves the driver's cuTensorMapEncodeTiled at run time, so it
 needs no library path beyond the NVIDIA driver.  _calls.so takes the library's
-addresses from it and resolves torch's from the torch that is imported.
+addresses from it and resolves torch's from the torch that is imported, which must
+be the one it was built for; the binding goes without it otherwise.
 """
 from __future__ import annotations
 
@@ -51,7 +52,9 @@ def calls_command(out: str) -> list[str]:
     base = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", base, "-isystem",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DTFA_BUILT_FOR="torch {torch.__version__}, Python {sys.version_info.major}.{sys.version_info.minor}"',
+            "-isystem", base, "-isystem",
             sysconfig.get_paths()["include"], "-isystem", cuda, "-o", out, CALLS_SOURCE,
             "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
             "-ltorch_python"]

@@ -452,4 +452,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls(void) { return PyModule_Create(&module); }
+// built_for: the torch whose tensors this code reads, and the Python.
+PyMODINIT_FUNC PyInit__calls(void) {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", TFA_BUILT_FOR) < 0) Py_CLEAR(m);
+    return m;
+}

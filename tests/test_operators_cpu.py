@@ -301,3 +301,30 @@ def test_first_cut_of_known_shapes():
     assert plan(1, 8, 2, 300, 300, 9, -1, 148)[0] == tb.TFA_ERR_WINDOW
     assert plan(1, 8, 2, 300, 300, 9, 4, 0)[0] == tb.TFA_ERR_SHAPE
     assert plan(1, 8, 3, 300, 300, 9, 4, 148)[0] == tb.TFA_ERR_HEADS
+
+
+@pytest.mark.parametrize("how", ["missing", "another torch"])
+def test_the_library_loads_without_its_native_calls(how, monkeypatch):
+    """Everything that does not need them works, and says what is not there."""
+    import sys
+
+    import sliding_window_gqa_tfa_b200 as package
+    import torch
+
+    tb.lib()
+    assert tb._calls is not None
+    monkeypatch.setattr(tb, "_lib", None)
+    monkeypatch.setattr(tb, "_calls", None)
+    if how == "missing":
+        monkeypatch.delattr(package, "_calls")
+        monkeypatch.setitem(sys.modules, package.__name__ + "._calls", None)
+    else:
+        monkeypatch.setattr(torch, "__version__", "1.0")
+    with pytest.warns(RuntimeWarning, match="_calls.so"):
+        tb.lib()
+    assert tb._calls is None
+    assert tb.tfa_plan_ktile(200, 300, True, 0, 0) == (tb.TFA_OK, 0, 1)
+    assert tb.tfa_plan_first_cut(1, 32, 8, 4096, 4096, 1024, 4, 148) == (tb.TFA_OK, 1, 4)
+    assert _chunk(L=0) == tb.TFA_ERR_SHAPE
+    with pytest.raises(ValueError, match="CUDA"):
+        tb.prefill(*[torch.zeros(1, 1, 16, 64, dtype=torch.bfloat16)] * 3, window=4, first=1)
