@@ -95,6 +95,14 @@ float number(PyObject *o) {
     }
     return static_cast<float>(v);
 }
+int truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {  // (the wrapper's code asks again, and raises)
+        PyErr_Clear();
+        throw Unusual{};
+    }
+    return v;
+}
 float scale_or(PyObject *o, int64_t D) {
     return o == Py_None ? static_cast<float>(1. / std::sqrt(static_cast<double>(D))) : number(o);
 }
@@ -186,8 +194,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 11, [&]() -> PyObject * {
         const Rope r(a);
         const float eps = number(a[6]), mscale = number(a[8]);
-        const int inter = PyObject_IsTrue(a[7]);
-        need(inter >= 0);
+        const int inter = truth(a[7]);
         const at::Tensor qo = given_or_empty(a[9], r.q, {r.B, r.Hq, r.L, r.D}, true);
         const at::Tensor ko = given_or_empty(a[10], r.k, {r.B, r.Hkv, r.L, r.D}, true);
         Strides s;
@@ -208,8 +215,7 @@ PyObject *rope_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Rope r(a);
         need(r.wq != nullptr);
         const float eps = number(a[6]), mscale = number(a[8]);
-        const int inter = PyObject_IsTrue(a[7]);
-        need(inter >= 0);
+        const int inter = truth(a[7]);
         const at::Tensor &gq = sized(rows(beside(r.q, a[9], at::kBFloat16, 4)), {r.B, r.Hq, r.L, r.D});
         const at::Tensor &gk = sized(rows(beside(r.q, a[10], at::kBFloat16, 4)), {r.B, r.Hkv, r.L, r.D});
         const at::Tensor dq = at::empty({r.B, r.L, r.Hq, r.D}, r.q.options());
@@ -381,8 +387,7 @@ PyObject *prefill_first(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const float scale = scale_or(a[3], d.D), softcap = number(a[7]);
         const int window = integer(a[4]), first = integer(a[5]);
         const float *sinks = sinks_of(a[8], d.q);
-        const int want = PyObject_IsTrue(a[11]);
-        need(want >= 0);
+        const int want = truth(a[11]);
         const at::Tensor o = given_or_empty(a[9], d.q, d.q.sizes());
         at::Tensor lse;
         if (a[10] != Py_None)

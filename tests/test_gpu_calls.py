@@ -318,3 +318,15 @@ def test_numbers_of_numpy_and_of_torch(monkeypatch):
             for a, b in zip(want, run(i, f, t)):
                 # (numpy's float32 rounds 1e-5 as the C call does)
                 assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_a_flag_without_a_truth_value_is_refused():
+    q, k = _rows(0, 1, 2, 4, D).cuda(), _rows(1, 1, 2, 2, D).cuda()
+    freq, _ = tb.rope_inv_freq(D, device="cuda")
+    flag = torch.ones(2)  # bool() of it raises
+    with pytest.raises(RuntimeError):
+        tb.qk_norm_rope(q, k, 0, freq, interleaved=flag)
+    with pytest.raises(RuntimeError):
+        tb.qk_norm_rope_backward(q.transpose(1, 2), k.transpose(1, 2), q, k, 0, freq, q_weight=q[0, 0, 0],
+                                 k_weight=k[0, 0, 0], interleaved=flag)
