@@ -707,9 +707,11 @@ def rope_inv_freq(rot, base=10000.0, *, scaling=None, factor=1.0, original=8192,
     """(inv_freq, mscale) for qk_norm_rope: fp64 [rot/2] radians per position, base^(-2i/rot).
 
     scaling: None; "linear" (every pair's frequency divided by factor); "llama3" or
-    "yarn" (pairs that turn less than once in the `original` positions are divided
-    by factor, those that turn more than 4, or 32, times are kept, between them a
-    linear ramp over the turns; yarn's mscale is 0.1 ln(factor) + 1)."""
+    "yarn": pairs that turn often within the `original` positions are kept, those that
+    turn less than once are divided by factor, and a ramp lies between them.  llama3's
+    ramp is linear in a pair's turns, from 1 to 4.  yarn's is linear in its index, from
+    the last pair of at least 32 turns to the first of at most 1 (the ramp that
+    published checkpoints use), and its mscale is 0.1 ln(factor) + 1."""
     if rot < 0 or rot % 2:
         raise ValueError("rot must be even and >= 0")
     if not (factor > 0 and original > 0 and base > 0):
@@ -718,11 +720,21 @@ def rope_inv_freq(rot, base=10000.0, *, scaling=None, factor=1.0, original=8192,
     mscale = 1.0
     if scaling == "linear":
         f = f / factor
-    elif scaling in ("llama3", "yarn"):
-        fast = 4.0 if scaling == "llama3" else 32.0
-        keep = ((original * f / (2 * math.pi) - 1.0) / (fast - 1.0)).clamp(0.0, 1.0)
+    elif scaling == "llama3":
+        keep = ((original * f / (2 * math.pi) - 1.0) / 3.0).clamp(0.0, 1.0)
         f = f * keep + f / factor * (1 - keep)
-        if scaling == "yarn" and factor > 1:
+    elif scaling == "yarn":
+        if base <= 1:
+            raise ValueError("yarn's ramp needs a base above 1")
+
+        def place(turns):  # the index, not a whole number, of a pair with so many turns
+            return rot * math.log(original / (2 * math.pi * turns)) / (2 * math.log(base))
+
+        low, high = max(math.floor(place(32.0)), 0), min(math.ceil(place(1.0)), rot - 1)
+        index = torch.arange(rot // 2, dtype=torch.float64)
+        keep = 1 - ((index - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1 - keep)
+        if factor > 1:
             mscale = 0.1 * math.log(factor) + 1.0
     elif scaling is not None:
         raise ValueError('scaling must be None, "linear", "llama3" or "yarn"')

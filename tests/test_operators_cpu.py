@@ -328,3 +328,38 @@ def test_the_library_loads_without_its_native_calls(how, monkeypatch):
     assert _chunk(L=0) == tb.TFA_ERR_SHAPE
     with pytest.raises(ValueError, match="CUDA"):
         tb.prefill(*[torch.zeros(1, 1, 16, 64, dtype=torch.bfloat16)] * 3, window=4, first=1)
+
+
+@pytest.mark.parametrize("rot,base,factor,original", [(128, 1e6, 4.0, 8192), (64, 1e4, 32.0, 4096), (128, 5e5, 8.0, 32768),
+                                                      (16, 1e4, 2.5, 100)])
+def test_scaled_frequencies_pair_by_pair(rot, base, factor, original):
+    """yarn: a ramp over the pairs' indexes between the whole indexes around the pairs of
+    32 turns and of 1 turn in the original positions; llama3: over the wavelengths."""
+    import math
+
+    f = [base ** (-2 * i / rot) for i in range(rot // 2)]
+    lo, hi = (rot * math.log(original / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (32, 1))
+    lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), rot - 1)
+    got, mscale = tb.rope_inv_freq(rot, base, scaling="yarn", factor=factor, original=original, device="cpu")
+    assert mscale == pytest.approx(0.1 * math.log(factor) + 1)
+    for i, x in enumerate(got.tolist()):
+        ramp = min(max((i - lo) / (hi - lo), 0.0), 1.0)
+        assert x == pytest.approx(f[i] / factor * ramp + f[i] * (1 - ramp), rel=1e-12)
+    got, mscale = tb.rope_inv_freq(rot, base, scaling="llama3", factor=factor, original=original, device="cpu")
+    assert mscale == 1.0
+    for i, x in enumerate(got.tolist()):
+        wave = 2 * math.pi / f[i]
+        if wave < original / 4:
+            want = f[i]
+        elif wave > original:
+            want = f[i] / factor
+        else:
+            smooth = (original / wave - 1) / 3
+            want = (1 - smooth) * f[i] / factor + smooth * f[i]
+        assert x == pytest.approx(want, rel=1e-12)
+
+
+def test_yarn_needs_a_base_above_one():
+    with pytest.raises(ValueError):
+        tb.rope_inv_freq(16, 1.0, scaling="yarn", factor=2.0, device="cpu")
+    assert tb.rope_inv_freq(0, 1e4, scaling="yarn", factor=2.0, device="cpu")[0].numel() == 0
