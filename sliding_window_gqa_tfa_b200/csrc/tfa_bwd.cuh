@@ -539,8 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = q0 + r;
             const bool valid = row < p.L;
             const size_t idx = static_cast<size_t>(it.b * p.Hq + it.h) * p.L + row;
-            const float lse_r = valid ? __ldg(p.lse + idx) : CUDART_INF_F;
-            const float dl_r = valid ? __ldg(p.delta + idx) : 0.f;
+            const float lse_r = valid ? load_input<FIRST>(p.lse + idx) : CUDART_INF_F;
+            const float dl_r = valid ? load_input<FIRST>(p.delta + idx) : 0.f;
             const int pos = (p.S - p.L) + row;
             const int hi_abs = p.causal ? imin(pos, p.S - 1) : p.S - 1;
             const int lo_abs = (p.causal && p.window > 0) ? pos - p.window + 1 : 0;
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (needs) {
                             const int k = k32 + e;
                             const bool al = (FIRST ? ((keep >> e) & 1u) != 0u : k >= lo_abs && k <= hi_abs) &&
-                                            (!KM || __ldg(km_row + k) > 0.5f);
+                                            (!KM || load_input<FIRST>(km_row + k) > 0.5f);
                             pe = al ? pe : 0.f;
                         }
                         pr[32 * c2 + e] = pe;
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const KItem it = k_item<FIRST>(p, ii.item);
             const int key = it.kt * kBlockK + r;
             const bool kvalid = key < p.S;
-            const bool kept = kvalid && (!KM || __ldg(p.key_mask + static_cast<size_t>(it.b) * p.S + key) > 0.5f);
+            const bool kept = kvalid && (!KM || load_input<FIRST>(p.key_mask + static_cast<size_t>(it.b) * p.S + key) > 0.5f);
             // the query rows that see this key: [q_lo, q_hi] (empty when not kept)
             int q_lo = p.causal ? imax(0, key - P) : 0;
             int q_hi = (p.causal && p.window > 0) ? imin(p.L - 1, key - P + p.window - 1) : p.L - 1;
@@ -827,8 +827,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c2 = 0; c2 < 2; ++c2) {
                     const int q = q0 + 64 * hf + 32 * c2 + lane;
-                    nxt[2 * c2] = q < p.L ? -__ldg(lse_h + q) : -CUDART_INF_F;
-                    nxt[2 * c2 + 1] = q < p.L ? __ldg(dl_h + q) : 0.f;
+                    nxt[2 * c2] = q < p.L ? -load_input<FIRST>(lse_h + q) : -CUDART_INF_F;
+                    nxt[2 * c2 + 1] = q < p.L ? load_input<FIRST>(dl_h + q) : 0.f;
                 }
             };
             fetch(0);

@@ -17,7 +17,10 @@ int device_info(cudaStream_t stream, unsigned **status, int *sm_count);
 
 // Launches a kernel that may be set up while the stream's previous one still ends: it
 // calls grid_dep_wait before it touches memory, and grid_dep_launch only then, so that
-// a kernel after it never starts before the one before it has ended.
+// a kernel after it never starts before the one before it has ended.  Inputs are not
+// read through the read-only path (load_input).  (kv4::join_kernel reads the lengths
+// before its wait: the kernel before it, its own call's, neither writes them nor
+// launches it before its own wait.)
 template <typename... Args, typename... Given>
 cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                          Given... args) {

@@ -353,7 +353,7 @@ __device__ void load_role(const Params &p, const CUtensorMap *tm_q, const CUtens
                     for (int i = 0; i < 4; ++i) {
                         const int n = 32 * i + lane;
                         const int key = j * kBlockK + n;
-                        const bool keep = key < p.S && __ldg(km_row + key) > 0.5f;
+                        const bool keep = key < p.S && load_input<LY == kLayoutFirst>(km_row + key) > 0.5f;
                         *reinterpret_cast<uint16_t *>(blk + bias_offset(n, 0)) = keep ? 0x0000u : 0xFF80u;
                     }
                     fence_proxy_async_smem();  // the tensor core reads it through the async proxy
@@ -606,7 +606,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // output head `head`, against reference maximum m (raw-score units).
 __device__ __forceinline__ float add_sink(const Params &p, float l, float m, float c, int head) {
     if (p.sinks == nullptr || m == -CUDART_INF_F) return l;  // an empty row stays 0
-    return l + ex2(fmaf(__ldg(p.sinks + head), kLog2e, -m * c));
+    return l + ex2(fmaf(p.sinks[head], kLog2e, -m * c));
 }
 
 // Epilogue / score variants of the kernel, fixed at compile time so that a

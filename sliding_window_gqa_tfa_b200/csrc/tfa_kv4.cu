@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
         v[0] = src[0];
         v[1] = src[1];
     }
-    const long long first = p.start ? __ldg(p.start + b) : p.start0;
+    const long long first = p.start ? load_input<true>(p.start + b) : p.start0;
     uint32_t km, vm;
     const unsigned long long kc = encode(k[0], k[1], km), vc = encode(v[0], v[1], vm);
     if (!in || first < 0) return;  // a sequence without a place takes nothing
@@ -190,13 +190,13 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
     grid_dep_wait();
     grid_dep_launch();
     if (row >= p.n_rows) return;
-    const long long first = p.start ? __ldg(p.start + b) : p.start0;
+    const long long first = p.start ? load_input<true>(p.start + b) : p.start0;
     const long long at = first + i + (i >= p.split ? p.skip : 0);
     uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
     if (first >= 0 && at < p.cap) {
         const size_t src = static_cast<size_t>(bh) * p.cap + at, code = src * LPR + lane, word = src * (D / kGroup) + lane / 4;
-        const uint32_t kc = __ldg(reinterpret_cast<const uint32_t *>(p.c.kc) + code), km = __ldg(p.c.km + word);
-        const uint32_t vc = __ldg(reinterpret_cast<const uint32_t *>(p.c.vc) + code), vm = __ldg(p.c.vm + word);
+        const uint32_t kc = load_input<true>(reinterpret_cast<const uint32_t *>(p.c.kc) + code), km = load_input<true>(p.c.km + word);
+        const uint32_t vc = load_input<true>(reinterpret_cast<const uint32_t *>(p.c.vc) + code), vm = load_input<true>(p.c.vm + word);
         k = values8(kc, __uint_as_float(km << 16), __uint_as_float(km & 0xffff0000u));
         v = values8(vc, __uint_as_float(vm << 16), __uint_as_float(vm & 0xffff0000u));
     } else if (first >= 0 && lane == 0) {

@@ -123,14 +123,14 @@ struct Deal {
         float all = 0.f;
         int count = 0;
         if (B <= 32) {
-            if (lane < B) n = p.lens ? __ldg(p.lens + lane) : p.all;
+            if (lane < B) n = p.lens ? load_input<true>(p.lens + lane) : p.all;
             if (report && threadIdx.x < 32 && (n < 0 || n > p.cap)) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
             mine = span_of(p, n).steps;
             count = __popc(__ballot_sync(0xffffffffu, mine > 0));
             all = static_cast<float>(mine);
         } else {
             for (int b = threadIdx.x; b < B; b += blockDim.x) {
-                const int len = p.lens ? __ldg(p.lens + b) : p.all;
+                const int len = p.lens ? load_input<true>(p.lens + b) : p.all;
                 if (report && (len < 0 || len > p.cap)) atomicOr(p.status, TFA_DEVICE_BAD_SEQLENS);
                 steps_of[b] = span_of(p, len).steps;
             }
@@ -206,7 +206,7 @@ struct Deal {
         return B <= 32 ? __shfl_sync(0xffffffffu, k, b) : first[b + 1] - first[b];
     }
     __device__ __forceinline__ int length(const DecodeParams &p, int b) const {
-        return B <= 32 ? __shfl_sync(0xffffffffu, n, b) : p.lens ? __ldg(p.lens + b) : p.all;
+        return B <= 32 ? __shfl_sync(0xffffffffu, n, b) : p.lens ? load_input<true>(p.lens + b) : p.all;
     }
 };
 
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB, REP>::kCtasPerSm)
                 qv[nb][gr] = make_uint4(0u, 0u, 0u, 0u);
                 const int row = 8 * nb + g % C::kCols;
                 if (row < n_rows)
-                    qv[nb][gr] = __ldg(reinterpret_cast<const uint4 *>(p.q + (qrow + row) * D + 32 * gr + 8 * t));
+                    qv[nb][gr] = load_input<true>(reinterpret_cast<const uint4 *>(p.q + (qrow + row) * D + 32 * gr + 8 * t));
             }
 
         // copies of step j into stage st: codes in 16-byte chunks, steps and minima row by
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NB, REP>::kCtasPerSm)
             }
             if (cuts == 1) {
                 if (p.sinks && mx > -CUDART_INF_F)
-                    sum += ex2(fmaf(__ldg(p.sinks + h * p.G + (row0 + row) / p.L), kLog2e, -mx));
+                    sum += ex2(fmaf(load_input<true>(p.sinks + h * p.G + (row0 + row) / p.L), kLog2e, -mx));
                 const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
                 *reinterpret_cast<uint2 *>(p.o + (qrow + row) * D + 4 * c4) =
                     make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
@@ -863,7 +863,7 @@ __device__ __forceinline__ void join_row(const DecodeParams &p, JoinShared<WARPS
             x = fmaf(f, sh.o[w][2 * threadIdx.x], x);
             y = fmaf(f, sh.o[w][2 * threadIdx.x + 1], y);
         }
-        if (p.sinks && mx > -CUDART_INF_F) sum += ex2(fmaf(__ldg(p.sinks + head), kLog2e, -mx));
+        if (p.sinks && mx > -CUDART_INF_F) sum += ex2(fmaf(load_input<true>(p.sinks + head), kLog2e, -mx));
         const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
         reinterpret_cast<uint32_t *>(out)[threadIdx.x] = pack_bf16(x * inv, y * inv);
     }

@@ -318,6 +318,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// A value that an earlier kernel of the stream may have written.  A kernel that is
+// launched while that one ends (EARLY: launch_after) takes an ordinary load, which its
+// grid_dep_wait orders; the read-only path (__ldg) wants data that nobody writes from
+// the kernel's launch on.
+template <bool EARLY, typename T>
+__device__ __forceinline__ T load_input(const T *p) {
+    if constexpr (EARLY) return *p;
+    else return __ldg(p);
+}
 // The n lowest bits, n clamped to [0, 32].
 __device__ __forceinline__ uint32_t bits_below(int n) {
     uint32_t m;

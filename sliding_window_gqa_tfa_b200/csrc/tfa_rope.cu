@@ -58,8 +58,8 @@ struct Params {
 // 64 bits: a row behind a first position near 2^31 lies past an int.
 __device__ __forceinline__ long long position(const Params &p, int b, int l) {
     if (!p.pos) return static_cast<long long>(p.pos0) + l;
-    return p.pos_per_row ? __ldg(p.pos + static_cast<long long>(b) * p.L + l)
-                         : static_cast<long long>(__ldg(p.pos + b)) + l;
+    return p.pos_per_row ? load_input<true>(p.pos + static_cast<long long>(b) * p.L + l)
+                         : static_cast<long long>(load_input<true>(p.pos + b)) + l;
 }
 
 // The cosines and sines of a position's pairs, times mscale; a gradient's sines are negated.

@@ -3,6 +3,8 @@ point, rejects bad arguments before touching the GPU, and its work
 enumeration (the tile scheduler's host view) is exact against the oracle's
 visibility rule.  No compute call runs here."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -271,3 +273,17 @@ def test_lse_and_saved_backward_reject_before_launch():
         assert L_.tfa_prefill_backward_saved(*bad, *i, 0.1, 1, 0, None, None) == tb.TFA_ERR_ALIGN
     assert L_.tfa_prefill_backward_saved(*args, 1, 8, 2, 64, 200, 96, 0.1, 1, 0, None,
                                          None) == tb.TFA_ERR_HEAD_DIM
+
+
+def test_kernels_that_start_early_do_not_read_inputs_through_the_read_only_path():
+    """Kernels launched while the kernel before them ends (launch_after): the read-only
+    path wants data that nobody writes from the launch on, which only variants with an
+    ordinary launch have (load_input<false>, the cu_seqlens of packed batches)."""
+    csrc = os.path.join(os.path.dirname(tb.__file__), "csrc")
+    found = []
+    for name in sorted(os.listdir(csrc)):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(csrc, name)).read())
+        found += [(name, line.strip()) for line in text.splitlines()
+                  if re.search(r"__ldg\b|ld\.global\.nc|__restrict__", line)]
+    allowed = [("tfa_ptx.cuh", "else return __ldg(p);")]
+    assert [f for f in found if f not in allowed and not (f[0] == "tfa_kernel.cuh" and "p.cu_" in f[1])] == []
