@@ -7,6 +7,7 @@
 namespace tfa {
 
 constexpr int kMaxDevices = 64;  // device_info refuses others
+constexpr int kSms = 148;        // of a B200, for rules that choose between variants without a device
 
 // Record which CUDA call failed (readable through tfa_last_error); TFA_ERR_CUDA.
 int report_cuda(const char *what, cudaError_t e);

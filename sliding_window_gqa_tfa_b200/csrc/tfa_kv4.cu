@@ -392,25 +392,34 @@ int decode(const void *q, const void *k_codes, const void *k_meta, const void *v
 
 // Whether a chunk goes to the kernel for few rows, which multiplies the codes as they
 // are but walks them once for every 16 rows of a KV head, or is unpacked for the dense
-// kernel.  Measured (D = 128, 4 or 7 query heads a KV head): up to 64 rows the first is
-// always ahead (16 x 8 KV heads, 5000 positions: 138 against 160 us; one sequence of
-// 5000: 18 against 51 us); beyond, while its own time stays below the dense kernel's,
-// which is long where few items leave it many pieces to join (128 rows, one sequence of
-// 5000: 28 against 76 us; 16 sequences: 270 against 160 us; 200 rows of one head over
-// 12000 positions: 18 against 446 us, of 32 heads 233 against 100 us).  The estimates,
-// in us, met the faster one or came within 15 % of it at 237 of 240 sizes.
-bool few_rows(int B, int Hq, int Hkv, int L, const Seen &sn) {
-    const long long rows = static_cast<long long>(Hq / Hkv) * L;
+// kernel: by estimates of both, in us.  The first spends a start for each piece (16 rows
+// of a KV head; 2 blocks an SM) and a time for each of its rows and positions; the other
+// the read back, and its key tiles in rounds of the SMs, or cut over all of them with a
+// join.  Fitted to 1,181 sizes (D = 64 and 128, 1 to 16 heads a KV head, 1 to 8 KV heads,
+// 1 to 16 sequences, 1 to 1,200 rows over 21 to 14,000 positions, windows of 1,024): the
+// rule took the faster one or came within 15 % of it at 1,127, at most 2.3 times off
+// (1,065 and 4.0 with a rule of the rows and of the products alone).  E.g. (D = 128) 128
+// rows a KV head, one sequence of 5000: 28 against 76 us; 16 sequences: 270 against 160
+// us; 200 rows of one head over 12000 positions: 18 against 446 us; 210 rows on 4 KV heads
+// of 16 sequences of 159: 48 against 16 us.  (The SMs are those of a B200, not the
+// device's count: tfa_kv4_prefill_workspace, which follows the rule, knows no device.)
+bool few_rows(int B, int Hq, int Hkv, int L, int D, const Seen &sn) {
+    const int G = Hq / Hkv;
+    const long long rows = static_cast<long long>(G) * L;
     if (B > kMaxSeqs || static_cast<long long>(B) * Hq * L > (1ll << 26)) return false;
-    if (rows <= 64) return true;
-    const double pairs = static_cast<double>(B) * Hkv * sn.rows() * rows;
-    if (L < 128) return pairs <= 12e6;
-    const double own = 9 + 4.6e-6 * pairs;
-    // items of two query tiles, their key tiles of 1.75 us, the other pieces of a cut item
-    const double sms = 148, items = static_cast<double>(B) * Hq * ((L + 255) / 256), tiles = sn.rows() / 128.;
-    const double whole = 14 + 1.75 * tiles * std::ceil(items / sms), others = sms / items < tiles ? sms / items : tiles;
-    const double cut = 25 + 1.75 * items * tiles / sms + 5 * others;
-    return own < (items >= sms ? whole : items >= 32 && whole < cut ? whole : cut);
+    if (rows <= 8) return true;  // its narrow form, always ahead
+    const double d = D / 128., n = static_cast<double>(sn.rows()), heads = static_cast<double>(B) * Hkv;
+    const double pieces = heads * static_cast<double>((rows + 15) / 16);
+    const double own = 9 + (4.5 + 4.8 * d) * pieces / (2 * tfa::kSms) + (0.8 + 2.4 * d) * 16e-6 * pieces * n;
+    const bool packed = L <= 128;  // several heads' rows in a tile
+    const int per = L < 128 ? 128 / L : 1;
+    const double items = packed ? heads * ((G + per - 1) / per) : heads * G * ((L + 255) / 256);
+    const double tiles = std::ceil(n / 128), step = 1.3 + 0.8 * d, start = packed ? 11.5 : 16;
+    const double whole = start + step * tiles * std::ceil(items / tfa::kSms);
+    const double others = tfa::kSms / items < tiles ? tfa::kSms / items : tiles;  // pieces of a cut item
+    const double cut = start + 8 + step * items * tiles / tfa::kSms + 3 * others;
+    const double dense = (items < 4 * tfa::kSms && cut < whole ? cut : whole) + 0.9e-6 * heads * n * D;
+    return own < 1.1 * dense;
 }
 
 }  // namespace
@@ -440,7 +449,7 @@ extern "C" int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_
 extern "C" size_t tfa_kv4_prefill_workspace(int B, int Hq, int Hkv, int L, int S, int D, int window, int first) {
     if (B < 1 || Hkv < 1 || Hq < 1 || L < 1 || S < L || D < 1 || first < 0) return 0;
     const Seen sn = seen(L, S, window, first);
-    return few_rows(B, Hq, Hkv, L, sn) ? decode_workspace(D) : static_cast<size_t>(B) * Hkv * sn.rows() * D * 4;
+    return few_rows(B, Hq, Hkv, L, D, sn) ? decode_workspace(D) : static_cast<size_t>(B) * Hkv * sn.rows() * D * 4;
 }
 
 // The positions that are brought back, min(S, first + L + window - 1) with a window and
@@ -469,7 +478,7 @@ extern "C" int tfa_kv4_prefill(const void *q, const void *k_codes, const void *k
     if (!std::isfinite(softcap) || softcap < 0.f || (softcap > 0.f && scale == 0.f)) return TFA_ERR_SOFTCAP;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(sinks, 4) || !aligned(workspace, 16)) return TFA_ERR_ALIGN;
     const Seen sn = seen(L, S, window, first);
-    if (few_rows(B, Hq, Hkv, L, sn))
+    if (few_rows(B, Hq, Hkv, L, D, sn))
         return decode(q, k_codes, k_meta, v_codes, v_meta, nullptr, S, o, B, Hq, Hkv, L, capacity, D, scale, window, first,
                       softcap, sinks, workspace, reinterpret_cast<cudaStream_t>(stream));
     const int rows = static_cast<int>(sn.rows());

@@ -462,7 +462,7 @@ int launch_forward(Params &p, int D, cudaStream_t stream) {
     const int tokens = p.B * p.L;
     // A block takes all of a token's rows, so that its angles are computed once,
     // unless that leaves SMs without a block (decoding): then one round of rows.
-    p.rows_per_block = tokens >= 4 * 148 ? n_rows : slots;
+    p.rows_per_block = tokens >= 4 * kSms ? n_rows : slots;
     const dim3 grid(tokens, (n_rows + p.rows_per_block - 1) / p.rows_per_block);
     const bool norm = p.wq != nullptr;
     using Kern = void (*)(Params);

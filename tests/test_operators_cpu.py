@@ -363,3 +363,20 @@ def test_yarn_needs_a_base_above_one():
     with pytest.raises(ValueError):
         tb.rope_inv_freq(16, 1.0, scaling="yarn", factor=2.0, device="cpu")
     assert tb.rope_inv_freq(0, 1e4, scaling="yarn", factor=2.0, device="cpu")[0].numel() == 0
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,L,S,D,few", [
+    # measured on both kernels, us: few rows, dense
+    (16, 28, 4, 30, 159, 128, False),  # 48, 16
+    (4, 64, 4, 125, 230, 64, False),  # 69, 21
+    (16, 64, 4, 11, 97, 64, False),  # many pieces of three steps
+    (16, 64, 8, 8, 311, 128, False),
+    (1, 28, 4, 128, 5000, 128, True),  # 28, 76
+    (1, 1, 1, 200, 12000, 128, True),  # 18, 446
+    (1, 32, 4, 32, 8000, 64, True),
+    (16, 8, 8, 1, 60, 128, True),
+    (16, 64, 8, 1, 60, 64, True),
+])
+def test_which_chunks_take_the_kernel_for_few_rows(B, Hq, Hkv, L, S, D, few):
+    size = tb.lib().tfa_kv4_prefill_workspace(B, Hq, Hkv, L, S, D, 0, 0)
+    assert size == (tb.lib().tfa_kv4_decode_workspace(Hq, Hkv, L, D) if few else B * Hkv * S * D * 4)
