@@ -371,7 +371,7 @@ def test_yarn_needs_a_base_above_one():
     (4, 64, 4, 125, 230, 64, False),  # 69, 21
     (16, 64, 4, 11, 97, 64, False),  # many pieces of three steps
     (16, 64, 8, 8, 311, 128, False),
-    (1, 28, 4, 128, 5000, 128, True),  # 28, 76
+    (1, 32, 8, 32, 5000, 128, True),  # 28, 76
     (1, 1, 1, 200, 12000, 128, True),  # 18, 446
     (1, 32, 4, 32, 8000, 64, True),
     (16, 8, 8, 1, 60, 128, True),
