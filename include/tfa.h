@@ -264,7 +264,8 @@ int tfa_prefill_backward_saved(const void *q, const void *k, const void *v, cons
  *                 channels contiguous: views of a joint projection are fine
  *   q_out, k_out  bf16, likewise: [B, Hq, L, D] for the attention entry points,
  *                 or rows of a key cache.  May be the inputs themselves (the same
- *                 pointers and strides); any other overlap is undefined.
+ *                 pointers and strides); any other overlap is undefined, and a
+ *                 stride of 0 over more than one row TFA_ERR_SHAPE.
  *   strides       HOST array of 12: the element strides over (batch, token, head)
  *                 of q, k, q_out, k_out, multiples of 8 (unread where a
  *                 dimension's size is 1)

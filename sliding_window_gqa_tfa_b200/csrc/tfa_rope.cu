@@ -442,6 +442,10 @@ int check(const Params &p, int D) {
     if (p.B < 1 || p.L < 1 || static_cast<long long>(p.B) * p.L > (1ll << 30) || p.Hq > (1 << 16) ||
         p.Hkv > (1 << 16))
         return TFA_ERR_SHAPE;
+    // an output whose rows are one and the same place (an expanded tensor)
+    if ((p.B > 1 && (!p.sqo.b || !p.sko.b)) || (p.L > 1 && (!p.sqo.l || !p.sko.l)) || (p.Hq > 1 && !p.sqo.h) ||
+        (p.Hkv > 1 && !p.sko.h))
+        return TFA_ERR_SHAPE;
     if (D != 64 && D != 128) return TFA_ERR_HEAD_DIM;
     if (p.rot < 0 || p.rot > D || p.rot % 16 != 0 || !std::isfinite(p.eps) || p.eps < 0.f || !std::isfinite(p.mscale))
         return TFA_ERR_ROPE;

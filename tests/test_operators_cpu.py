@@ -380,3 +380,21 @@ def test_yarn_needs_a_base_above_one():
 def test_which_chunks_take_the_kernel_for_few_rows(B, Hq, Hkv, L, S, D, few):
     size = tb.lib().tfa_kv4_prefill_workspace(B, Hq, Hkv, L, S, D, 0, 0)
     assert size == (tb.lib().tfa_kv4_decode_workspace(Hq, Hkv, L, D) if few else B * Hkv * S * D * 4)
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_rope_refuses_outputs_whose_rows_share_a_place(back):
+    import struct
+
+    n, out = (18, 12) if back else (12, 6)
+    for i in range(out, n):
+        for size in (1, 2):
+            s = [1 << 20, 4096, 128] * (n // 3)
+            s[i] = 0
+            dims = [2, 2, 2]
+            dims[(i - out) % 3] = size
+            args = [struct.pack(f"{n}q", *s), A16, A16, A16, ctypes.c_void_p(0x10002), 0, 0, *dims, dims[2], 128, 64, 0, 1e-6, 1.0]
+            lib = tb.lib()
+            rc = (lib.tfa_qk_norm_rope_backward(*[A16] * 8, *args, A16, None) if back
+                  else lib.tfa_qk_norm_rope(*[A16] * 4, *args, None))
+            assert rc == (tb.TFA_ERR_SHAPE if size == 2 else tb.TFA_ERR_ALIGN)  # (else the positions are refused)
