@@ -23,6 +23,10 @@
  * Layout: every tensor is contiguous row-major with the head dimension
  * innermost, bf16 stored as 16-bit words:
  *   q, o : [B, Hq,  L, D]        k, v : [B, Hkv, S, D]        key_mask : [B, S] fp32
+ * K and V are finite wherever a 128-key tile that some row sees reaches, masked
+ * positions included: a weight of 0 times a V that is not finite is NaN, in every
+ * row of the query tile, and so is the score of a K that only the key mask drops.
+ * (Tiles that no row sees are not loaded.)
  *
  * Ownership: every pointer passed to tfa_prefill is caller-owned DEVICE memory
  * on the current CUDA device; the call neither allocates nor frees the tensors
@@ -314,7 +318,8 @@ size_t tfa_qk_norm_rope_workspace(int D);
  * + i) sees key j iff j <= p and (j > p - window or j < first), and the key mask
  * keeps it.  window > 0 and first >= 0, else TFA_ERR_WINDOW; with first = 0 it is
  * tfa_prefill's window.  Key tiles that hold neither first tokens nor window are
- * skipped without loading them.
+ * skipped without loading them.  As in tfa_prefill the softmax weights are rounded to
+ * bf16 against a row's running maximum for the product with V, and the output is.
  *   lse      NULL, or as for tfa_prefill_lse (not with softcap or sinks:
  *            TFA_ERR_SOFTCAP)
  *   softcap, sinks  as for tfa_attention_ex
@@ -324,10 +329,11 @@ int tfa_prefill_first(const void *q, const void *k, const void *v, void *o, floa
                       const float *key_mask, float softcap, const float *sinks, tfa_stream_t stream);
 
 /* tfa_prefill_first_backward -- gradients of tfa_prefill_first (no softcap, no
- * sinks) from its saved output and log-sum-exp; arguments, workspace and errors as
- * for tfa_prefill_backward_saved.  Where key tiles are cut (tfa_plan_first_cut) the
- * workspace also holds the parts' sums, 1024 D bytes for each of tiles x B x Hkv x
- * parts, which are at most four times the device's SMs (78 MB of 148 SMs and D = 128). */
+ * sinks) from its saved output and log-sum-exp; arguments, workspace, roundings (P and
+ * dS to bf16) and errors as for tfa_prefill_backward_saved.  Where key tiles are cut
+ * (tfa_plan_first_cut) the workspace also holds the parts' sums, 1024 D bytes for each
+ * of tiles x B x Hkv x parts, which are at most four times the device's SMs (78 MB
+ * with 148 SMs and D = 128). */
 int tfa_prefill_first_backward(const void *q, const void *k, const void *v, const void *o,
                                const float *lse, const void *dout, void *dq, void *dk, void *dv,
                                int B, int Hq, int Hkv, int L, int S, int D, float scale,
@@ -353,7 +359,9 @@ int tfa_prefill_first_backward(const void *q, const void *k, const void *v, cons
  *             capacity are not written, and tfa_check_status returns
  *             TFA_ERR_SEQLENS.  NULL: every sequence starts at first_row, checked
  *             here (TFA_ERR_CACHE).
- * Other rows of the cache are left as they are.  Asynchronous on `stream`. */
+ * Other rows of the cache are left as they are.  Asynchronous on `stream`, and like
+ * the other calls on a 4-bit cache capturable after one call on the device
+ * (TFA_ERR_CAPTURE: it creates the status word). */
 int tfa_kv4_append(const void *k, const void *v, const long long *strides,
                    void *k_codes, void *k_meta, void *v_codes, void *v_meta,
                    const int *start, int first_row, int B, int Hkv, int L, int capacity, int D,
@@ -368,7 +376,8 @@ int tfa_kv4_read(const void *k_codes, const void *k_meta, const void *v_codes, c
                  int B, int Hkv, int rows, int capacity, int D, tfa_stream_t stream);
 
 /* tfa_kv4_decode -- tfa_decode over the 4-bit cache, sequences of their own lengths.
- *   q, o      bf16 [B, Hq, L, D], 1 <= L <= TFA_MAX_DECODE_ROWS, B <= 1024
+ *   q, o      bf16 [B, Hq, L, D], 1 <= L <= TFA_MAX_DECODE_ROWS, B <= 1024,
+ *             B Hq L <= 2^26
  *   lens      int32 [B] device: cached positions of each sequence, its L new rows
  *             among them (they are the last).  Row i is at position p = lens[b] - L
  *             + i and sees the positions j <= p, with a window (window > 0) those
@@ -380,12 +389,15 @@ int tfa_kv4_read(const void *k_codes, const void *k_meta, const void *v_codes, c
  *   softcap, sinks  as for tfa_attention_ex
  *   workspace device memory of tfa_kv4_decode_workspace(Hq, Hkv, L, D) bytes,
  *             16-byte aligned; not shared by calls that overlap
- * The codes enter the products exactly; the softmax weights times a step are
- * rounded to fp16, against a power of two above the steps seen: a term below
- * 2^-30 of the largest may be lost, and steps of V are taken to lie in [2^-40,
- * 2^80], channels of q in [-2^100, 2^100] (those 2^-28 below a row's largest lose
- * bits).  Asynchronous on `stream`; after one call on the device (which creates
- * its status word) it may be captured, and each replay reads the lengths anew. */
+ * The codes enter the products exactly; the softmax weights times a step of V are
+ * rounded to fp16: by 2^-11 of the product, or 2^-31 of the largest step that the
+ * call's rows see where that is more (and a code is at most 15).  Where one position's
+ * steps are 2^20 times the others', those keep some 10 bits.  Steps of V are taken to
+ * lie in [2^-40, 2^80], its values in [-2^70, 2^70], channels of q in [-2^100, 2^100]
+ * (those 2^-28 below a row's largest lose bits).  A cached row that is not finite
+ * reaches the query rows that see it, and no others.  Asynchronous on `stream`; after
+ * one call on the device (which creates its status word) it may be captured, and each
+ * replay reads the lengths anew. */
 int tfa_kv4_decode(const void *q, const void *k_codes, const void *k_meta, const void *v_codes, const void *v_meta,
                    const int *lens, void *o, int B, int Hq, int Hkv, int L, int capacity, int D,
                    float scale, int window, int first, float softcap, const float *sinks,
@@ -397,7 +409,10 @@ size_t tfa_kv4_decode_workspace(int Hq, int Hkv, int L, int D);
  * TFA_ERR_CACHE).  Chunks of few rows, or of few heads, take tfa_kv4_decode's kernel,
  * where it is the faster; for the others the positions that some row sees are brought
  * back to bf16 in the workspace and the dense kernel runs on them (scratch and graph
- * capture as for tfa_prefill).  workspace: device memory of
+ * capture as for tfa_prefill).  There K and V are rounded to bf16 once more, as a bf16
+ * cache's would be, and so are the softmax weights: an error of 0.0033 of the output where
+ * the other kernel's is 0.0017, its own rounding; and a V that is not finite reaches all
+ * rows of a query tile that loads it.  workspace: device memory of
  * tfa_kv4_prefill_workspace(B, Hq, Hkv, L, S, D, window, first) bytes, 16-byte
  * aligned, not shared by calls that overlap.  That size is this call's: a chunk of
  * fewer rows may take the other kernel and need more.  One workspace for several

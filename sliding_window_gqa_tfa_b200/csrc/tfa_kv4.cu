@@ -59,8 +59,9 @@ struct AppendParams {
 };
 
 // Both kernels: a lane takes 16 channels of K and of V, half a group, so a row is
-// D / 16 lanes.  They should be bound by the bytes moved (2.625 a channel each), which
-// needs few instructions beside (4 x 2047 rows of 8 heads, append and read: 49.6 us
+// D / 16 lanes.  They should be bound by the bytes moved (2.625 a channel each); what
+// is measured is the wait for loads (append: 0.61 instructions a scheduler and cycle),
+// which is short with few instructions beside (4 x 2047 rows of 8 heads, append and read: 49.6 us
 // with 64-bit row indexes and IEEE divisions for the codes, 22.2 us without, 18.5 us
 // with K and V found at once and packed arithmetic; the 88 MB would take 13.4).
 // The codes of a lane's 16 channels, a and b, and the word of the step and minimum of

@@ -26,10 +26,10 @@
 // as a group's rows are few, so the products are transposed: positions (K) and
 // channels (V) are the 16-row side of mma.m16n8k16, the query rows its 8-column
 // side, and eight rows cost what the codes need anyway.  Every warp walks its own
-// 32-position steps with its own asynchronous copies and its own running
-// maximum and sum; nothing in the loop waits for another warp.  The fragments
-// come straight from the codes: a lane's word of 8 codes gives four bf16 pairs,
-// in an order of channels that q is laid out in once.
+// 32-position steps with its own asynchronous copies and its own reference and
+// sum; nothing in the loop waits for another warp.  The fragments come straight
+// from the codes: a lane's word of 8 codes gives four fp16 pairs, in an order of
+// channels that q is laid out in once.
 //
 // A segment is a sequence's KV head and a chunk of its rows.  Lengths are read on
 // the device, where every CTA works out the same deal (Deal): longer sequences'

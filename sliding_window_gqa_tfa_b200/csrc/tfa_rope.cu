@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 5) forward_kernel(const __grid_const
 // strides; other head counts than multiples of 8 leave slots idle in the last round.
 // The next group's angles are computed while this one's rows are, one a thread, between
 // two barriers.  Rows are copied to shared memory kAhead rounds before they are needed.
-// Instructions bound it more than the memory: 4 x 2047 tokens of 24 heads took 44 us
+// Latency bounds it (0.57 instructions a scheduler and cycle, fixed latencies the first
+// stall, DRAM at 41 %), which fewer instructions shorten: 4 x 2047 tokens of 24 heads took 44 us
 // with the rows dealt to the slots in order and a channel's partner in another lane (337
 // instructions a warp for two rows), 39 with pairs in a lane and fixed tokens (204), 37
 // with 2 blocks of 102 registers an SM instead of 3 of 80 (169), and takes 35 with two
