@@ -14,6 +14,7 @@ be the one it was built for; the binding goes without it otherwise.
 """
 from __future__ import annotations
 
+import contextlib
 import os
 import subprocess
 import sys
@@ -85,6 +86,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         running.append((cmd, None, subprocess.Popen(cmd)))
     failed = [(cmd, p.returncode) for cmd, _, p in running if p.wait() != 0]
     if failed:
+        for _, obj, _ in running:  # what the others have written
+            with contextlib.suppress(FileNotFoundError):
+                os.remove(calls_tmp if obj is None else obj + f".tmp{os.getpid()}")
         raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
     for _, obj, _ in running:
         if obj is None:
