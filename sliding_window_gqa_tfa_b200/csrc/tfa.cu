@@ -318,24 +318,24 @@ struct FirstCut {
 // The most that one of `sms` CTAs is dealt in the snake order of bwd::ItemIter.
 constexpr int kDealSms = 512;
 struct Dealt {
-    int sms;
-    long long x = 0, all = 0, diff[kDealSms + 1] = {};
+    int sms, pos = 0;  // the next item's place in its round
+    bool back = false;  // a round that goes backwards
+    long long all = 0, sum = 0, diff[kDealSms + 1] = {};
     explicit Dealt(int sms_) : sms(sms_) {}
     void add(long long count, long long cost) {  // `count` items of a cost, the next ones
+        sum += count * cost;
+        if (count >= 2 * sms) {  // two rounds, there and back, leave the place as it is
+            const long long pairs = count / (2 * sms);
+            all += 2 * pairs * cost;
+            count -= 2 * pairs * sms;
+        }
         while (count > 0) {
-            const int pos = static_cast<int>(x % sms);
-            if (pos == 0 && count >= sms) {
-                const long long rounds = count / sms;
-                all += rounds * cost;
-                x += rounds * sms;
-                count -= rounds * sms;
-                continue;
-            }
             const int take = count < sms - pos ? static_cast<int>(count) : sms - pos;
-            const int lo = (x / sms) % 2 ? sms - pos - take : pos;
+            const int lo = back ? sms - pos - take : pos;
             diff[lo] += cost;
             diff[lo + take] -= cost;
-            x += take;
+            pos += take;
+            if (pos == sms) pos = 0, back = !back;
             count -= take;
         }
     }
@@ -372,20 +372,33 @@ FirstCut first_cut(int B, int Hkv, int G, int L, int S, int window, int first, i
     const bool every = bg * all_tiles < sms;
     if (parts < 2 && !every) return c;
     int seen = 0;  // key tiles that some row sees
+    double share = 0;  // of a CTA, whatever the cut
+    auto sums = [&](int t, int into) { return t ? 3 + 0.04 * static_cast<double>(bg * t * into) : 0.; };
     auto cost = [&](const FirstCut &f) {
         Dealt d(sms);
         seen = 0;
         for (int kt = 0; kt < all_tiles; ++kt) {
             const tfa::KeyRange qr = tfa::ktile_query_range(L, S, 1, kt < tiles ? 0 : window, kt);
-            const long long nq = qr.hi >= qr.lo ? qr.hi - qr.lo + 1 : 0;
+            const int nq = qr.hi >= qr.lo ? qr.hi - qr.lo + 1 : 0;  // at most 2^24
             seen += nq > 0;
             const int into = kt < f.tiles ? f.parts : 1;
-            for (int i = 0; i < into; ++i) d.add(bg, (nq * (i + 1) / into - nq * i / into) * G);
+            for (int i = 0, at = 0; i < into; ++i) {
+                const int end = nq * (i + 1) / into;
+                d.add(bg, static_cast<long long>(end - at) * G);
+                at = end;
+            }
         }
-        return static_cast<double>(d.most()) + (f.tiles ? 3 + 0.04 * static_cast<double>(bg * f.tiles * f.parts) : 0.);
+        share = static_cast<double>(d.sum) / sms;
+        return static_cast<double>(d.most()) + sums(f.tiles, f.parts);
     };
     double best = cost(c);
+    // a cut's cost is at least this: a CTA's share, or a part of a tile that every row sees
+    auto least = [&](int t, int into) {
+        const double part = static_cast<double>((n + into - 1) / into) * G;
+        return (share > part ? share : part) + sums(t, into);
+    };
     auto consider = [&](int t, int into) {
+        if (least(t, into) >= best) return;
         FirstCut f;
         f.tiles = t;
         f.parts = into;
@@ -393,8 +406,15 @@ FirstCut first_cut(int B, int Hkv, int G, int L, int S, int window, int first, i
         if (x < best) best = x, c = f;
     };
     if (parts >= 2) consider(tiles, parts);
-    if (every && 4 * seen >= 3 * all_tiles)  // else parts of tiles that nobody sees would only be written
-        for (int into = 2; into <= n && into <= 32 && bg * all_tiles * into <= most_parts; ++into) consider(all_tiles, into);
+    if (every && 4 * seen >= 3 * all_tiles) {  // else parts of tiles that nobody sees would only be written
+        int most = 1, promising = 2;
+        while (most < n && most < 32 && bg * all_tiles * (most + 1) <= most_parts) ++most;
+        for (int into = 3; into <= most; ++into)
+            if (least(all_tiles, into) < least(all_tiles, promising)) promising = into;
+        if (most >= 2) consider(all_tiles, promising);  // first, so that few of the others are worth a look
+        for (int into = 2; into <= most; ++into)
+            if (into != promising) consider(all_tiles, into);
+    }
     return c;
 }
 
