@@ -955,6 +955,10 @@ def kv4_read(k_codes, k_meta, v_codes, v_meta, *, start=0, rows=None, out=None, 
             raise ValueError("rows must be given with a start for each sequence")
         rows = cap - first
     rows = _int32(rows, "rows")
+    if rows < 1:
+        raise TfaError(TFA_ERR_SHAPE, "tfa_kv4_read")
+    if ptr is None and not 0 <= first <= cap - rows:  # before anything of that size is allocated
+        raise TfaError(TFA_ERR_CACHE, "tfa_kv4_read")
     with _scope(dev, stream):
         if out is None:
             out = k_meta.new_empty((B, Hkv, rows, D)), k_meta.new_empty((B, Hkv, rows, D))

@@ -290,7 +290,7 @@ PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t n) {
         int first;
         c.start(a[4], &start, &first);
         const int count = integer(a[5]);
-        need(count >= 0);
+        need(count >= 1 && (start || (first >= 0 && first <= c.cap - count)));
         const at::Tensor k = at::empty({c.B, c.Hkv, count, c.D}, c.km.options()), v = at::empty(k.sizes(), k.options());
         const tfa_stream_t stream = stream_of(c.kc);
         const int rc = without_gil([&] {

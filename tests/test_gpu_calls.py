@@ -330,3 +330,19 @@ def test_a_flag_without_a_truth_value_is_refused():
     with pytest.raises(RuntimeError):
         tb.qk_norm_rope_backward(q.transpose(1, 2), k.transpose(1, 2), q, k, 0, freq, q_weight=q[0, 0, 0],
                                  k_weight=k[0, 0, 0], interleaved=flag)
+
+
+@pytest.mark.gpu
+def test_read_refuses_before_it_allocates(monkeypatch):
+    c = tb.kv4_cache(1, 1, 64, D, device="cuda")
+    tb.lib()
+    for native in (tb._calls, None):
+        monkeypatch.setattr(tb, "_calls", native)
+        for kw, code in ((dict(start=0, rows=2 ** 31 - 1), tb.TFA_ERR_CACHE), (dict(start=60, rows=5), tb.TFA_ERR_CACHE),
+                         (dict(start=-1, rows=1), tb.TFA_ERR_CACHE), (dict(start=65), tb.TFA_ERR_SHAPE),
+                         (dict(start=0, rows=0), tb.TFA_ERR_SHAPE), (dict(start=0, rows=-4), tb.TFA_ERR_SHAPE)):
+            torch.cuda.reset_peak_memory_stats()
+            before = torch.cuda.memory_allocated()
+            with pytest.raises(tb.TfaError) as e:
+                tb.kv4_read(*c, **kw)
+            assert e.value.code == code and torch.cuda.max_memory_allocated() == before
